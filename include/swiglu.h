@@ -360,6 +360,103 @@ uint64_t swiglu_mlp_noalloc_scratch_bytes(void);
 int swiglu_mlp_noalloc(const void *A, const void *W1, const void *W2, const void *W3,
                        const void *R, void *Z, int64_t M, int64_t H, int64_t F, void *stream);
 
+/*
+ * The sparse (mixture-of-experts) form of the MLP block: every token goes
+ * through k of E experts, each a SwiGLU block of its own.  The page's MLP
+ * (section "Definizione del Problema") is each expert; the routing, the
+ * grouping and the norms around the block follow the standard definitions
+ * given here.  The calls in order:
+ *     swiglu_moe_route -> swiglu_fused_grouped -> swiglu_linear_grouped
+ *     -> swiglu_residual_norm
+ * The sizes of the experts' groups stay on the device: no call reads them on
+ * the host, so the whole block can be captured in a CUDA graph.
+ */
+
+/*
+ * The router: for every token the k experts with the largest logits.
+ *     p[t,e] = softmax over e of logits[t,:]
+ *     ids[t,j]     : expert of the j-th largest logit (ties: the lowest number)
+ *     weights[t,j] : scale * p[t, ids[t,j]], divided by the sum of the chosen
+ *                    p where renormalize = 1
+ * and the order of the entries (t, j) by expert that the grouped products use:
+ *     offsets[E+1] : expert e owns the places [offsets[e], offsets[e+1])
+ *     rows[place]  : the token at that place; within an expert, places follow
+ *                    t * k + j
+ *     slots[t,j]   : the entry's place
+ * A logit of -inf masks its expert: it is never chosen.  A choice that finds
+ * no expert left has id -1, weight 0 and slot -1; the places from offsets[E]
+ * on hold rows = -1.  A NaN logit ranks above every number, and its token's
+ * weights are NaN.  Sums are FP32; the result does not depend on timing.
+ *   logits : device, [T,E], BF16 (logits_fp32 = 0) or FP32 (1)  (read)
+ *   ids, rows, slots : device, int32 [T,k], [T*k], [T,k]  (written)
+ *   weights : device, FP32 [T,k]  (written);  offsets : device, int32 [E+1]
+ *   workspace : device scratch of at least swiglu_moe_route_workspace_size()
+ *       bytes (0 for a few tokens; may then be NULL), 4-byte aligned
+ * 1 <= k <= min(E, 32), E <= 1024, T * k < 2^31.  Every pointer aligned to its
+ * element; no output overlaps another buffer.  T = 0 zeroes offsets.
+ */
+uint64_t swiglu_moe_route_workspace_size(int64_t T, int64_t E, int64_t k);
+int swiglu_moe_route(const void *logits, int32_t logits_fp32, int32_t renormalize, float scale,
+                     int32_t *ids, float *weights, int32_t *offsets, int32_t *rows,
+                     int32_t *slots, int64_t T, int64_t E, int64_t k, void *workspace,
+                     uint64_t workspace_bytes, void *stream);
+
+/*
+ * Products grouped by expert: the places [offsets[e], offsets[e+1]) belong to
+ * expert e, and
+ *     swiglu_fused_grouped :  Y[p] = SiLU(a W1[e]) (.) (a W2[e])
+ *     swiglu_linear_grouped:  Z[p] = a W[e]
+ * with a = A[rows[p]], or A[p] where rows is NULL (then T must equal P).
+ * BF16 in, FP32 accumulate, one rounding to BF16.
+ *   A       : device, BF16 [T,K]  (read)
+ *   W1, W2, W : device, BF16 [E,K,N]  (read)
+ *   offsets : device, int32 [E+1]  (read at kernel time); values are clamped
+ *       to [0, P] and to be non-decreasing
+ *   rows    : device, int32 [P] or NULL (read at kernel time); a number
+ *       outside [0, T) gives a row of zeros
+ *   Y, Z    : device, BF16 [P,N]; the places before offsets[0] and from
+ *       offsets[E] on are left as they are
+ * Groups may be empty or of any size.  E <= 1024, K and N multiples of 8,
+ * K * N < 2^39, pointers 16-byte aligned (offsets and rows 4-byte); Y must not
+ * overlap an input.  K = 0 or T = 0 makes every product zero: Y is filled
+ * with zeros.  P = 0 or N = 0 enqueues nothing.
+ */
+int swiglu_fused_grouped(const void *A, const void *W1, const void *W2, const int32_t *offsets,
+                         const int32_t *rows, void *Y, int64_t T, int64_t P, int64_t E, int64_t N,
+                         int64_t K, void *stream);
+int swiglu_linear_grouped(const void *X, const void *W, const int32_t *offsets,
+                          const int32_t *rows, void *Z, int64_t T, int64_t P, int64_t E, int64_t N,
+                          int64_t K, void *stream);
+
+/*
+ * The end of a block: the join of the experts' rows, the norm after the
+ * block, its gate and residual, and the norm before the next block:
+ *     z  = sum_j weights[t,j] * Z[slots[t,j]],  or Z[t] where slots is NULL
+ *     n  = z * gamma_post / sqrt(mean z^2 + eps), or z where post_norm = 0
+ *     R' = residual_scale * R + gate (.) n
+ *     H  = R' * gamma_pre / sqrt(mean R'^2 + eps)
+ * FP32 arithmetic; R' (in R's type) and H (BF16) are rounded once, H from the
+ * unrounded R'.  A row whose mean square plus eps is zero normalises to
+ * zeros.  A slot outside [0, P) adds nothing (its weight is not read).
+ *   Z          : device, BF16 [P,D]  (read); P = T where slots is NULL
+ *   slots, weights : device, int32 and FP32 [T,k], or both NULL  (read)
+ *   R          : device, [T,D], BF16 (r_fp32 = 0) or FP32 (1)  (read)
+ *   gamma_post, gamma_pre : device, BF16 [D], or NULL for all ones;
+ *       gamma_post must be NULL where post_norm = 0
+ *   gate       : device, BF16, row t at gate + t * gate_stride (elements; 0 =
+ *       one row for every token), or NULL for all ones
+ *   Rout       : device, like R  (written); may be R itself
+ *   H          : device, BF16 [T,D]  (written), or NULL: not made
+ * D and gate_stride multiples of 8, D <= 32768; gate_stride 0 or >= D;
+ * matrices and gammas 16-byte aligned, slots and weights 4-byte.  Outputs
+ * overlap no other buffer.  eps finite, >= 0.
+ */
+int swiglu_residual_norm(const void *Z, const int32_t *slots, const float *weights, const void *R,
+                         int32_t r_fp32, int32_t post_norm, const void *gamma_post,
+                         const void *gate, int64_t gate_stride, float residual_scale,
+                         const void *gamma_pre, float eps, void *Rout, void *H, int64_t T,
+                         int64_t P, int64_t k, int64_t D, void *stream);
+
 /* swiglu_fused / swiglu_fused_interleaved with an explicit variant
  * (SWIGLU_VARIANT_*) instead of the library's choice; for sweeps and tests. */
 int swiglu_fused_ex(const void *A, const void *W1, const void *W2, void *Y,

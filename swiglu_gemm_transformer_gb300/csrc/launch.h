@@ -68,6 +68,20 @@ cudaError_t launch_dqt(int tok, int wf, const LaunchArgs &la);
 cudaError_t launch_pack_w4_kmajor(const void *Wq, void *Wk, int64_t K, int64_t N, int sm_count,
                                   cudaStream_t s);
 int device_info(uint32_t **err, int *sm_count, uint64_t *timeout_ns, uint64_t *ctx_gen);
+// Tensor map of a BF16 tensor of `rank` dimensions (innermost first; strides in
+// bytes of dimensions 1.. ) with the 128-byte swizzle; call after device_info().
+int encode_bf16_map(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims,
+                    const uint64_t *strides, const uint32_t *box);
+
+// Argument checks shared by the entry points of several files.
+inline bool ptr_aligned(const void *p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+inline bool ranges_overlap(const void *a, uint64_t an, const void *b, uint64_t bn) {
+  if (!a || !b || an == 0 || bn == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + bn && b0 < a0 + an;
+}
 // CTA-pair kernels: whether launches with more units than resident pairs use
 // the dynamic unit schedule.
 bool pair_dynamic_schedule();

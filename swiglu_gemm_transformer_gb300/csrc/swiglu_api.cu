@@ -860,6 +860,23 @@ int device_info(uint32_t **err, int *sm_count, uint64_t *timeout_ns, uint64_t *c
   return SWIGLU_OK;
 }
 
+int encode_bf16_map(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims,
+                    const uint64_t *strides, const uint32_t *box) {
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], one[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    one[i] = 1;
+    if (i > 0) st[i - 1] = strides[i - 1];
+  }
+  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(ptr),
+                              d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SWIGLU_OK : SWIGLU_ERR_CUDA;
+}
+
 bool pair_dynamic_schedule() { return g_pair_dyn.load(std::memory_order_relaxed) != 0; }
 
 }  // namespace swiglu
