@@ -14,18 +14,23 @@
 // N comes in steps of 32, so the product of a tile of n rows costs
 // ceil(n / 32) * 32 rows instead of 128 or 256, and a group of one row
 // costs little more than its weights' stream.
-//   * FUSED: per K slice of 16, two tcgen05.mma.cta_group::2 of M = 128 (64
-//     columns of W1, then of W2, in each CTA) x N rows: gate and up of one
-//     output column land in the same TMEM lane, 128 columns apart, so the
-//     activation needs no exchange between threads.  A pair makes 128 output
-//     columns for up to NT rows;
-//   * linear: one MMA of M = 256 (128 columns of W in each CTA) x N rows; a
-//     pair makes 256 output columns;
+//   * one tcgen05.mma.cta_group::2 of M = 256 x N rows per K slice of 16; each
+//     CTA holds 128 of the M rows: FUSED, 64 columns of W1 and the same 64 of
+//     W2; linear, 128 columns of W.  A pair makes 128 or 256 output columns
+//     for up to NT rows;
+//   * FUSED with two MMAs of M = 128 (gate, up) would put both values of an
+//     output into one TMEM lane, but reads the rows' tile from shared memory
+//     twice and is bound by that (1.31 against 1.57 PFLOP/s of the linear
+//     form at 64 experts x 1024 rows, K = 2048); so the gate lanes (0-63) and
+//     up lanes (64-127) trade half their values through shared memory;
 //   * weights are loaded MN-major straight from the row-major [E, K, N]
 //     tensors through 3-D tensor maps, whose K extent ends at each expert's
 //     last row, so a ragged K step never multiplies the next expert's
-//     weights; each CTA loads its own half of the tile's rows, by TMA gather4
-//     where `rows` names them (one lane per four rows), else by 16-row boxes;
+//     weights;
+//   * four warps of each CTA copy its half of the tile's rows with cp.async,
+//     through `rows` or directly.  TMA gather4 for the same rows took about 75
+//     cycles per four rows however it was issued and bound the kernel (1118
+//     against ... us at 64 experts x 1024 rows, K = 2048, N = 1024);
 //   * accumulators are double-buffered in TMEM (256 columns each).
 // Unit schedule: every CTA reads `offsets`, counts the row tiles of each
 // expert, and the pairs take the units (expert, row tile, column tile) in
@@ -47,10 +52,11 @@ namespace swiglu {
 constexpr int kMaxExperts = 1024;
 
 struct GroupedParams {
+  const __nv_bfloat16 *A;  // [T, K]
   const int32_t *offsets;  // [E + 1]
   const int32_t *rows;     // [P] or null
   __nv_bfloat16 *Y;        // [P, N]
-  int32_t T, P, E, N;      // rows of A, rows of Y, experts, output columns
+  int32_t T, P, E, N, K;   // rows of A, rows of Y, experts, output columns, inner size
   int32_t num_k_blk, num_n_blk;
   uint64_t timeout_ns;
   uint32_t *err;
@@ -69,21 +75,23 @@ struct GroupedCfg {
   static constexpr int STAGE_BYTES = W_BYTES + A_BYTES;
   static constexpr int STAGES = (208 * 1024) / STAGE_BYTES;
   static constexpr int EPI_WARPS = 8;
-  // one warp's staging block: 16 rows x 32 columns BF16, rows 80 bytes apart
+  // one epilogue warp's block: the 16 x 32 FP32 values its partner gives it
+  // (FUSED), then the 16 rows x 32 columns BF16 it stores, rows 80 bytes apart
   // (16-byte reads of eight rows then touch every bank once)
   static constexpr int STG_PITCH = 80;
-  static constexpr int STG_BYTES = 16 * STG_PITCH;
+  static constexpr int STG_BYTES = 16 * 32 * 4;
   static constexpr int STG_OFF = STAGES * STAGE_BYTES;
   static constexpr int TAB_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
   static constexpr int TAB_BYTES = 2 * (kMaxExperts + 1) * 4;
   static constexpr int BAR_OFF = (TAB_OFF + TAB_BYTES + 15) / 16 * 16;
-  static constexpr int NUM_BARS = 2 * STAGES + 5;
+  static constexpr int NUM_BARS = 3 * STAGES + 5;
   static constexpr int SMEM_BYTES = BAR_OFF + NUM_BARS * 8 + 16 + 1024;
   static constexpr int PRODUCER_WARP = EPI_WARPS;
   static constexpr int MMA_WARP = EPI_WARPS + 1;
-  static constexpr int THREADS = 32 * (EPI_WARPS + 2);
-  static constexpr int MMA_M = FUSED ? 128 : 256;
-  static constexpr int UP_COL = 128;   // FUSED: TMEM column offset of the up accumulator
+  static constexpr int ROW_WARP = EPI_WARPS + 2;  // first of the warps that load rows
+  static constexpr int ROW_WARPS = 4;
+  static constexpr int THREADS = 32 * (EPI_WARPS + 2 + ROW_WARPS);
+  static constexpr int MMA_M = 256;
   static constexpr int ACC_COLS = 256; // TMEM columns of one accumulator buffer
   static constexpr int GROUP = 8;
   static_assert(NT % 32 == 0 && NT <= 256, "rows of a tile");
@@ -91,14 +99,27 @@ struct GroupedCfg {
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
+// Named barrier over `threads` threads that returns whether all of them say so.
+__device__ __forceinline__ static bool bar_all(int id, int threads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %3, 0;\n\t"
+      "barrier.cta.red.and.pred b, %1, %2, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
 struct GroupedUnit {
   int e, row0, end, n, nb;  // expert, first row, end of the tile's rows, MMA N, column tile
 };
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
-    swiglu_grouped_kernel(const __grid_constant__ CUtensorMap tmA,
-                          const __grid_constant__ CUtensorMap tmW1,
+    swiglu_grouped_kernel(const __grid_constant__ CUtensorMap tmW1,
                           const __grid_constant__ CUtensorMap tmW2,  // FUSED only
                           const GroupedParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -112,6 +133,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   auto accf_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + b); };
   auto acce_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + 2 + b); };
   const uint32_t drain_bar = bars + 8u * (2 * C::STAGES + 4);
+  auto row_bar = [&](int s) { return bars + 8u * (2 * C::STAGES + 5 + s); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + C::NUM_BARS * 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *off = reinterpret_cast<int *>(smem + C::TAB_OFF);  // [E + 1] group bounds
@@ -125,8 +147,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (warp == C::PRODUCER_WARP && lane == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(full_bar(s), 2);  // the expected bytes of the weights, the peer's rows
       ptx::mbar_init(empty_bar(s), 1);
+      ptx::mbar_init(row_bar(s), 32 * C::ROW_WARPS);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(accf_bar(b), 1);
@@ -135,7 +158,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     ptx::mbar_init(drain_bar, 1);
     *abort_flag = 0;
     ptx::fence_barrier_init();
-    ptx::prefetch_tmap(&tmA);
     ptx::prefetch_tmap(&tmW1);
     if (C::FUSED) ptx::prefetch_tmap(&tmW2);
   }
@@ -214,50 +236,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // ------------------------------------------------------------ TMA producer (both CTAs)
     uint32_t stage = 0, phase = 0, issued = 0;
     bool ok = true;
-    for (int64_t u = cid; ok && u < num_units; u += ncl) {
-      const GroupedUnit un = unit_at(u);
-      const int half = un.n >> 1;  // rows of this CTA
-      const int r0 = un.row0 + static_cast<int>(rank) * half;
-      int idx[4] = {0, 0, 0, 0};
-      if (p.rows != nullptr && 4 * lane < half) {
-        // rows past the tile's end repeat its last one; their products are not stored
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          idx[j] = min(max(__ldg(p.rows + min(r0 + 4 * lane + j, un.end - 1)), 0), p.T - 1);
-      }
-      const int col0 = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS;
-      for (int kb = 0; kb < p.num_k_blk; ++kb) {
-        ok = wait_bar(empty_bar(stage), phase ^ 1u, p.timeout_ns, abort_flag, p.err,
-                      WAIT_PRODUCER_EMPTY);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t sw = base + stage * C::STAGE_BYTES;
-        const uint32_t sa = sw + C::W_BYTES;
-        const uint32_t fb = ptx::mapa_shared(full_bar(stage), 0);
-        if (lane == 0) {
-          if (rank == 0)
-            ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * C::W_BYTES + un.n * C::BK * 2);
+    if (lane == 0) {
+      for (int64_t u = cid; ok && u < num_units; u += ncl) {
+        const GroupedUnit un = unit_at(u);
+        const int col0 = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS;
+        for (int kb = 0; kb < p.num_k_blk; ++kb) {
+          if (!wait_bar(empty_bar(stage), phase ^ 1u, p.timeout_ns, abort_flag, p.err,
+                        WAIT_PRODUCER_EMPTY)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sw = base + stage * C::STAGE_BYTES;
+          const uint32_t fb = ptx::mapa_shared(full_bar(stage), 0);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * C::W_BYTES);
           ptx::tma_load_3d_pair(sw, &tmW1, fb, col0, kb * C::BK, un.e);
           if (C::FUSED)
             ptx::tma_load_3d_pair(sw + C::ATOM_BYTES, &tmW2, fb, col0, kb * C::BK, un.e);
           else
             ptx::tma_load_3d_pair(sw + C::ATOM_BYTES, &tmW1, fb, col0 + 64, kb * C::BK, un.e);
-        }
-        if (p.rows != nullptr) {
-          if (4 * lane < half)
-            ptx::tma_gather4_pair(sa + lane * 512, &tmA, fb, kb * C::BK, idx[0], idx[1], idx[2],
-                                  idx[3]);
-        } else if (16 * lane < half) {
-          ptx::tma_load_2d_pair(sa + lane * 2048, &tmA, fb, kb * C::BK, r0 + 16 * lane);
-        }
-        ++issued;
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1u;
+          ++issued;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
-    }
-    if (lane == 0) {
       if (ok) {
         // Consume the MMA-completion arrivals still due on this CTA's "empty"
         // barriers, so no multicast arrive targets this CTA after it exits.
@@ -269,7 +272,71 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     }
     __syncwarp();
+  } else if (warp >= C::ROW_WARP) {
+    // ------------------------------------------------------------ row loaders (both CTAs)
+    // Thread i copies 16-byte piece i % 8 of rows i / 8 + 16 j of this CTA's
+    // half into the 128-byte swizzle (piece c of row r at c ^ (r % 8)).
+    const int tid = (warp - C::ROW_WARP) * 32 + lane;
+    const int piece = tid & 7, r = tid >> 3;
+    const uint32_t dst = base + C::W_BYTES + r * 128 + ((piece ^ (r & 7)) << 4);
+    constexpr int STEP = 4 * C::ROW_WARPS;   // rows per pass of the four warps
+    constexpr int PASSES = C::NT / 2 / STEP;
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int64_t u = cid; ok && u < num_units; u += ncl) {
+      const GroupedUnit un = unit_at(u);
+      const int half = un.n >> 1;
+      const int passes = half / STEP;
+      const __nv_bfloat16 *src[PASSES];
+#pragma unroll
+      for (int j = 0; j < PASSES; ++j) {
+        // rows past the tile's end repeat its last one; their products are not stored
+        const int at = min(un.row0 + static_cast<int>(rank) * half + r + j * STEP, un.end - 1);
+        const int t = p.rows != nullptr && j < passes ? __ldg(p.rows + at) : at;
+        src[j] = p.A + int64_t(min(max(t, 0), p.T - 1)) * p.K + piece * 8;
+      }
+      for (int kb = 0; kb < p.num_k_blk; ++kb) {
+        if (!wait_bar(empty_bar(stage), phase ^ 1u, p.timeout_ns, abort_flag, p.err,
+                      WAIT_PRODUCER_EMPTY)) {
+          ok = false;
+          break;
+        }
+        const bool in = kb * C::BK + piece * 8 < p.K;  // K is a multiple of 8
+#pragma unroll
+        for (int j = 0; j < PASSES; ++j)
+          if (j < passes)
+            ptx::cp_async16(dst + stage * C::STAGE_BYTES + j * STEP * 128,
+                            src[j] + (in ? kb * C::BK : 0), in);
+        ptx::cp_async_arrive(row_bar(stage));
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    ptx::cp_async_wait_all();
+    __syncwarp();
   } else if (warp == C::MMA_WARP) {
+    if (lane == 0 && rank != 0) {
+      // ---------------------------------------------------------- the odd CTA's rows
+      // Tells the leader that this CTA's rows of a stage have landed: the MMA
+      // reads them through the async proxy, so the fence stands between.
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int64_t u = cid; ok && u < num_units; u += ncl)
+        for (int kb = 0; kb < p.num_k_blk; ++kb) {
+          if (!wait_bar(row_bar(stage), phase, p.timeout_ns, abort_flag, p.err, WAIT_ROWS)) {
+            ok = false;
+            break;
+          }
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(full_bar(stage), 0));
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+    }
     // ------------------------------------------------------------ MMA issuer (leader only)
     if (lane == 0 && rank == 0) {
       uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
@@ -283,10 +350,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + abuf * C::ACC_COLS;
         for (int kb = 0; kb < p.num_k_blk; ++kb) {
-          if (!wait_bar(full_bar(stage), phase, p.timeout_ns, abort_flag, p.err, WAIT_MMA_FULL)) {
+          if (!wait_bar(row_bar(stage), phase, p.timeout_ns, abort_flag, p.err, WAIT_ROWS) ||
+              !wait_bar_cluster(full_bar(stage), phase, p.timeout_ns, abort_flag, p.err,
+                                WAIT_MMA_FULL)) {
             ok = false;
             break;
           }
+          ptx::fence_proxy_async_smem();
           ptx::tc_fence_after();
           const uint32_t sw = base + stage * C::STAGE_BYTES;
           const uint32_t sa = sw + C::W_BYTES;
@@ -299,11 +369,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const uint64_t wdesc = ptx::smem_desc(sw + kk * 2048, C::ATOM_BYTES, 1024, ptx::SW_128B);
             const uint64_t rdesc = ptx::smem_desc(sa + kk * 32, 16, 1024, ptx::SW_128B);
             ptx::mma_f16_pair(d, wdesc, rdesc, idesc, acc);
-            if (C::FUSED) {
-              const uint64_t udesc =
-                  ptx::smem_desc(sw + C::ATOM_BYTES + kk * 2048, C::ATOM_BYTES, 1024, ptx::SW_128B);
-              ptx::mma_f16_pair(d + C::UP_COL, udesc, rdesc, idesc, acc);
-            }
           }
           ptx::mma_commit_pair_mc(empty_bar(stage), 0x3);
           if (++stage == C::STAGES) {
@@ -324,25 +389,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue (warps 0-7, both CTAs)
-    // Warp q (mod 4) reads TMEM lanes [32q, 32q + 32).  FUSED: output column
-    // 32 (q % 2) + lane, rows of the first (q < 2) or second half of the tile
-    // in the TMEM columns; linear: output column 32q + lane, all rows.  Warps
-    // 0-3 take the even 16-row chunks, warps 4-7 the odd ones.
+    // Warp q (mod 4) reads TMEM lanes [32q, 32q + 32), the tile's rows in the
+    // columns.  Linear: lane i is output column 32q + i; FUSED: warps q = 0, 1
+    // hold the gate and q = 2, 3 the up values of output columns 32 (q % 2) + i.
+    // Per 32 rows (FUSED) or 16 rows (linear) of the tile; warps 0-3 take the
+    // even chunks, warps 4-7 the odd ones.
     const int q = warp & 3, h = warp >> 2;
+    constexpr int CH = C::FUSED ? 32 : 16;
+    const bool gate = q < 2;
     const int wcol = C::FUSED ? 32 * (q & 1) : 32 * q;
     uint8_t *stg = smem + C::STG_OFF + warp * C::STG_BYTES;
+    // FUSED: warps q and q ^ 2 trade values; the gate warp finishes a chunk's
+    // first 16 rows, the up warp the last 16 (named barrier of their 64 threads)
+    float *give = reinterpret_cast<float *>(smem + C::STG_OFF + (warp ^ 2) * C::STG_BYTES);
+    const int pair_bar = 1 + 2 * h + (q & 1);
     uint32_t abuf = 0, aphase = 0;
     for (int64_t u = cid; u < num_units; u += ncl) {
       const GroupedUnit un = unit_at(u);
       bool ok = wait_bar(accf_bar(abuf), aphase, p.timeout_ns, abort_flag, p.err,
                          WAIT_EPI_ACC_FULL);
       ok = __all_sync(0xffffffffu, ok);
+      if (C::FUSED) ok = bar_all(pair_bar, 64, ok);  // both warps go on, or neither
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * C::ACC_COLS;
-      const int half = un.n >> 1;
-      const int nchunk = (C::FUSED ? half : un.n) / 16;
-      const int rbase = un.row0 + (C::FUSED ? (q >> 1) * half : 0);
+      const int nchunk = un.n / CH;
       // the lane's column of 8 in the row segments that the warp stores
       const int scol = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS + wcol + (lane & 3) * 8;
       const uint32_t release = ptx::mapa_shared(acce_bar(abuf), 0);
@@ -353,29 +424,44 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
 #pragma unroll 1
       for (int c = h; c < nchunk; c += 2) {
-        uint32_t g[16], v[16];
-        ptx::tmem_ld16(tacc + c * 16, g);
-        if (C::FUSED) ptx::tmem_ld16(tacc + C::UP_COL + c * 16, v);
+        uint32_t v[CH];
+        if constexpr (C::FUSED) ptx::tmem_ld32(tacc + c * CH, v);
+        else ptx::tmem_ld16(tacc + c * CH, v);
         ptx::tmem_wait_ld();
-        ptx::reg_fence(g);
-        if (C::FUSED) ptx::reg_fence(v);
+        ptx::reg_fence(v);
         if (c + 2 >= nchunk) {
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive_cluster_relaxed(release);
         }
+        float y[16];
+        if constexpr (C::FUSED) {
+          if (c != h) asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            give[i * 32 + lane] = __uint_as_float(gate ? v[16 + i] : v[i]);
+          asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+          const float *got = reinterpret_cast<const float *>(stg);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = got[i * 32 + lane];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            y[i] = gate ? silu_mul(__uint_as_float(v[i]), y[i])
+                        : silu_mul(y[i], __uint_as_float(v[16 + i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[i]);
+        }
         __nv_bfloat16 *sp = reinterpret_cast<__nv_bfloat16 *>(stg) + lane;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float y = C::FUSED ? silu_mul(__uint_as_float(g[i]), __uint_as_float(v[i]))
-                                   : __uint_as_float(g[i]);
-          sp[i * (C::STG_PITCH / 2)] = __float2bfloat16_rn(y);
-        }
+        for (int i = 0; i < 16; ++i) sp[i * (C::STG_PITCH / 2)] = __float2bfloat16_rn(y[i]);
         __syncwarp();
+        const int row0 = un.row0 + c * CH + (C::FUSED && !gate ? 16 : 0);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int t = j * 8 + (lane >> 2);
-          const int row = rbase + c * 16 + t;
+          const int row = row0 + t;
           if (row < un.end && scol < p.N) {
             uint4 out = *reinterpret_cast<const uint4 *>(stg + t * C::STG_PITCH + (lane & 3) * 16);
             if (p.rows != nullptr) {
