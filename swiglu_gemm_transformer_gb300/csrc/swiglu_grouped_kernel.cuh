@@ -36,7 +36,10 @@
 // expert, and the pairs take the units (expert, row tile, column tile) in
 // turn; the rows of an expert are split evenly over its row tiles, in steps
 // of 32.  Within an expert, GROUP row tiles walk the column tiles together,
-// so that they share the weights in L2.
+// so that they share the weights in L2.  A warp of its own finds the units,
+// 32 at a time (one per lane), and hands them to the other roles through a
+// ring in shared memory: found by each role for itself, a unit cost about
+// 2 us between two main loops.
 // Every wait is bounded as in the other kernels.
 #pragma once
 
@@ -83,14 +86,18 @@ struct GroupedCfg {
   static constexpr int STG_OFF = STAGES * STAGE_BYTES;
   static constexpr int TAB_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
   static constexpr int TAB_BYTES = 2 * (kMaxExperts + 1) * 4;
-  static constexpr int BAR_OFF = (TAB_OFF + TAB_BYTES + 15) / 16 * 16;
-  static constexpr int NUM_BARS = 3 * STAGES + 5;
+  static constexpr int UNIT_OFF = (TAB_OFF + TAB_BYTES + 15) / 16 * 16;  // two blocks of 32 units
+  static constexpr int BAR_OFF = UNIT_OFF + 2 * 32 * 16;
+  static constexpr int NUM_BARS = 3 * STAGES + 9;
   static constexpr int SMEM_BYTES = BAR_OFF + NUM_BARS * 8 + 16 + 1024;
   static constexpr int PRODUCER_WARP = EPI_WARPS;
   static constexpr int MMA_WARP = EPI_WARPS + 1;
   static constexpr int ROW_WARP = EPI_WARPS + 2;  // first of the warps that load rows
   static constexpr int ROW_WARPS = 4;
-  static constexpr int THREADS = 32 * (EPI_WARPS + 2 + ROW_WARPS);
+  static constexpr int UNIT_WARP = ROW_WARP + ROW_WARPS;
+  static constexpr int THREADS = 32 * (UNIT_WARP + 1);
+  // warps that read the units: epilogue, row loaders, producer, MMA
+  static constexpr int UNIT_READERS = EPI_WARPS + ROW_WARPS + 2;
   static constexpr int MMA_M = 256;
   static constexpr int ACC_COLS = 256; // TMEM columns of one accumulator buffer
   static constexpr int GROUP = 8;
@@ -113,8 +120,45 @@ __device__ __forceinline__ static bool bar_all(int id, int threads, bool ok) {
   return r != 0;
 }
 
-struct GroupedUnit {
-  int e, row0, end, n, nb;  // expert, first row, end of the tile's rows, MMA N, column tile
+// One unit: rows [row0, end) of expert e, column tile nb; row0 = -1: no more.
+// 16 bytes, read from shared memory as one int4.
+struct __align__(16) GroupedUnit {
+  int row0, end, e, nb;
+  __device__ int n() const { return (end - row0 + 31) & ~31; }  // MMA N
+};
+
+// The units of one role, in order.  Every lane of the role's warp calls
+// next() (or one lane alone, for a role of one lane: ALONE).
+template <bool ALONE>
+class GroupedUnits {
+ public:
+  __device__ GroupedUnits(const GroupedUnit *ring, uint32_t full, uint32_t empty,
+                          const GroupedParams &p, volatile int *abort_flag)
+      : ring_(ring), full_(full), empty_(empty), p_(p), abort_(abort_flag) {}
+  // False at the end, or when a wait gave up (ok then false).
+  __device__ bool next(GroupedUnit &u, bool &ok) {
+    const uint32_t block = i_ >> 5;
+    if ((i_ & 31u) == 0u) {
+      ok = wait_bar(full_ + 8u * (block & 1u), (block >> 1) & 1u, p_.timeout_ns, abort_, p_.err,
+                    WAIT_SCHED_FULL);
+      if (!ALONE) ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return false;
+    }
+    const int4 v = *reinterpret_cast<const int4 *>(ring_ + (i_ & 63u));
+    u.row0 = v.x, u.end = v.y, u.e = v.z, u.nb = v.w;
+    if ((i_ & 31u) == 31u) {  // the block has been read
+      if (!ALONE) __syncwarp();
+      if (ALONE || (threadIdx.x & 31u) == 0u) ptx::mbar_arrive(empty_ + 8u * (block & 1u));
+    }
+    ++i_;
+    return u.row0 >= 0;
+  }
+
+ private:
+  const GroupedUnit *ring_;
+  uint32_t full_, empty_, i_ = 0;
+  const GroupedParams &p_;
+  volatile int *abort_;
 };
 
 template <class C>
@@ -134,6 +178,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   auto acce_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + 2 + b); };
   const uint32_t drain_bar = bars + 8u * (2 * C::STAGES + 4);
   auto row_bar = [&](int s) { return bars + 8u * (2 * C::STAGES + 5 + s); };
+  const uint32_t unitf_bar = bars + 8u * (3 * C::STAGES + 5);  // two each
+  const uint32_t unite_bar = bars + 8u * (3 * C::STAGES + 7);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + C::NUM_BARS * 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *off = reinterpret_cast<int *>(smem + C::TAB_OFF);  // [E + 1] group bounds
@@ -156,6 +202,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       ptx::mbar_init(acce_bar(b), 2 * C::EPI_WARPS);
     }
     ptx::mbar_init(drain_bar, 1);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(unitf_bar + 8u * b, 1);
+      ptx::mbar_init(unite_bar + 8u * b, C::UNIT_READERS);
+    }
     *abort_flag = 0;
     ptx::fence_barrier_init();
     ptx::prefetch_tmap(&tmW1);
@@ -172,9 +222,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
 
-  // Group bounds and row-tile counts.  The bounds are clamped to [0, P] and
-  // made monotone, so that no value of `offsets` reaches past Y.
-  if (warp == 0) {
+  GroupedUnit *ring = reinterpret_cast<GroupedUnit *>(smem + C::UNIT_OFF);
+
+  if (warp == C::UNIT_WARP) {
+    // ------------------------------------------------------------ unit finder
+    // Group bounds and row-tile counts.  The bounds are clamped to [0, P] and
+    // made monotone, so that no value of `offsets` reaches past Y.
     int top = 0, sum = 0;
     for (int e0 = 0; e0 <= p.E; e0 += 32) {
       const int e = e0 + lane;
@@ -201,44 +254,49 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       top = __shfl_sync(0xffffffffu, v, 31);
       sum = __shfl_sync(0xffffffffu, t, 31);
     }
-  }
-  __syncthreads();
-  const int64_t num_units = int64_t(tiles[p.E]) * p.num_n_blk;
-
-  auto unit_at = [&](int64_t u) {
-    GroupedUnit r;
-    // the expert whose row tiles hold tile u / num_n_blk
-    const int tt = static_cast<int>(u / p.num_n_blk);
-    int lo = 0, hi = p.E;  // tiles[lo] <= tt < tiles[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tiles[mid] <= tt) lo = mid; else hi = mid;
+    __syncwarp();
+    const int64_t num_units = int64_t(tiles[p.E]) * p.num_n_blk;
+    for (uint32_t block = 0;; ++block) {
+      const bool ok = wait_bar(unite_bar + 8u * (block & 1u), ((block >> 1) & 1u) ^ 1u,
+                               p.timeout_ns, abort_flag, p.err, WAIT_SCHED_EMPTY);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int64_t u = cid + (int64_t(block) * 32 + lane) * ncl;
+      GroupedUnit r = {-1, -1, 0, 0};
+      if (u < num_units) {
+        // the expert whose row tiles hold tile u / num_n_blk
+        const int tt = static_cast<int>(u / p.num_n_blk);
+        int lo = 0, hi = p.E;  // tiles[lo] <= tt < tiles[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (tiles[mid] <= tt) lo = mid; else hi = mid;
+        }
+        const int mt = tiles[lo + 1] - tiles[lo];
+        const int64_t local = u - int64_t(tiles[lo]) * p.num_n_blk;
+        const int64_t per_group = int64_t(C::GROUP) * p.num_n_blk;
+        const int first = static_cast<int>(local / per_group) * C::GROUP;
+        const int span = min(C::GROUP, mt - first);
+        const int64_t w = local % per_group;
+        const int cnt = off[lo + 1] - off[lo];
+        // even split in steps of 32 rows; no tile is empty: cnt > (mt - 1) * NT
+        const int step = ((cnt + mt - 1) / mt + 31) & ~31;
+        r.e = lo;
+        r.nb = static_cast<int>(w / span);
+        r.row0 = off[lo] + (first + static_cast<int>(w % span)) * step;
+        r.end = min(r.row0 + step, off[lo + 1]);
+      }
+      *reinterpret_cast<int4 *>(ring + 32 * (block & 1u) + lane) = make_int4(r.row0, r.end, r.e, r.nb);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(unitf_bar + 8u * (block & 1u));
+      if (__any_sync(0xffffffffu, r.row0 < 0)) break;
     }
-    const int mt = tiles[lo + 1] - tiles[lo];
-    const int local = static_cast<int>(u - int64_t(tiles[lo]) * p.num_n_blk);
-    const int per_group = C::GROUP * p.num_n_blk;
-    const int g = local / per_group;
-    const int first = g * C::GROUP;
-    const int span = min(C::GROUP, mt - first);
-    const int w = local - g * per_group;
-    const int cnt = off[lo + 1] - off[lo];
-    // even split in steps of 32 rows; no tile is empty: cnt > (mt - 1) * NT
-    const int step = ((cnt + mt - 1) / mt + 31) & ~31;
-    r.e = lo;
-    r.nb = w / span;
-    r.row0 = off[lo] + (first + w % span) * step;
-    r.end = min(r.row0 + step, off[lo + 1]);
-    r.n = (r.end - r.row0 + 31) & ~31;
-    return r;
-  };
-
-  if (warp == C::PRODUCER_WARP) {
+  } else if (warp == C::PRODUCER_WARP) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
     uint32_t stage = 0, phase = 0, issued = 0;
     bool ok = true;
     if (lane == 0) {
-      for (int64_t u = cid; ok && u < num_units; u += ncl) {
-        const GroupedUnit un = unit_at(u);
+      GroupedUnits<true> units(ring, unitf_bar, unite_bar, p, abort_flag);
+      GroupedUnit un;
+      while (ok && units.next(un, ok)) {
         const int col0 = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS;
         for (int kb = 0; kb < p.num_k_blk; ++kb) {
           if (!wait_bar(empty_bar(stage), phase ^ 1u, p.timeout_ns, abort_flag, p.err,
@@ -283,9 +341,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     constexpr int PASSES = C::NT / 2 / STEP;
     uint32_t stage = 0, phase = 0;
     bool ok = true;
-    for (int64_t u = cid; ok && u < num_units; u += ncl) {
-      const GroupedUnit un = unit_at(u);
-      const int half = un.n >> 1;
+    GroupedUnits<false> units(ring, unitf_bar, unite_bar, p, abort_flag);
+    GroupedUnit un;
+    while (units.next(un, ok)) {
+      const int half = un.n() >> 1;
       const int passes = half / STEP;
       const __nv_bfloat16 *src[PASSES];
 #pragma unroll
@@ -313,6 +372,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           phase ^= 1u;
         }
       }
+      if (!__all_sync(0xffffffffu, ok)) break;
     }
     ptx::cp_async_wait_all();
     __syncwarp();
@@ -323,7 +383,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // reads them through the async proxy, so the fence stands between.
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      for (int64_t u = cid; ok && u < num_units; u += ncl)
+      GroupedUnits<true> units(ring, unitf_bar, unite_bar, p, abort_flag);
+      GroupedUnit un;
+      while (ok && units.next(un, ok))
         for (int kb = 0; kb < p.num_k_blk; ++kb) {
           if (!wait_bar(row_bar(stage), phase, p.timeout_ns, abort_flag, p.err, WAIT_ROWS)) {
             ok = false;
@@ -341,9 +403,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (lane == 0 && rank == 0) {
       uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
       bool ok = true;
-      for (int64_t u = cid; ok && u < num_units; u += ncl) {
-        const GroupedUnit un = unit_at(u);
-        const uint32_t idesc = ptx::idesc_bf16(C::MMA_M, un.n, true, false);
+      GroupedUnits<true> units(ring, unitf_bar, unite_bar, p, abort_flag);
+      GroupedUnit un;
+      while (ok && units.next(un, ok)) {
+        const uint32_t idesc = ptx::idesc_bf16(C::MMA_M, un.n(), true, false);
         if (!wait_bar(acce_bar(abuf), aphase ^ 1u, p.timeout_ns, abort_flag, p.err,
                       WAIT_MMA_ACC_EMPTY))
           break;
@@ -404,16 +467,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     float *give = reinterpret_cast<float *>(smem + C::STG_OFF + (warp ^ 2) * C::STG_BYTES);
     const int pair_bar = 1 + 2 * h + (q & 1);
     uint32_t abuf = 0, aphase = 0;
-    for (int64_t u = cid; u < num_units; u += ncl) {
-      const GroupedUnit un = unit_at(u);
-      bool ok = wait_bar(accf_bar(abuf), aphase, p.timeout_ns, abort_flag, p.err,
+    bool ok = true;
+    GroupedUnits<false> units(ring, unitf_bar, unite_bar, p, abort_flag);
+    GroupedUnit un;
+    bool gave_up = false;
+    while (true) {
+      if (!units.next(un, ok)) {
+        gave_up = !ok;
+        break;
+      }
+      ok = wait_bar(accf_bar(abuf), aphase, p.timeout_ns, abort_flag, p.err,
                          WAIT_EPI_ACC_FULL);
       ok = __all_sync(0xffffffffu, ok);
       if (C::FUSED) ok = bar_all(pair_bar, 64, ok);  // both warps go on, or neither
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * C::ACC_COLS;
-      const int nchunk = un.n / CH;
+      const int nchunk = un.n() / CH;
       // the lane's column of 8 in the row segments that the warp stores
       const int scol = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS + wcol + (lane & 3) * 8;
       const uint32_t release = ptx::mapa_shared(acce_bar(abuf), 0);
@@ -479,6 +549,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         aphase ^= 1u;
       }
     }
+    // A warp that gave up while looking for a unit still meets its partner,
+    // which may be waiting for the pair's decision on one.
+    if (C::FUSED && gave_up) bar_all(pair_bar, 64, false);
   }
 
   // Both CTAs have passed their last use of the pair's resources before either
