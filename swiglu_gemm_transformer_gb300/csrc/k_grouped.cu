@@ -13,7 +13,7 @@ namespace {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct GroupedLaunch {
-  CUtensorMap w1, w2;
+  CUtensorMap a, a2, w1, w2;
   GroupedParams p;
   int64_t units;  // most units the call can have
   int device;
@@ -54,7 +54,7 @@ cudaError_t launch_grouped(GroupedLaunch &gl) {
   const int64_t clusters = std::min<int64_t>(gl.units, max_clusters[gl.device & 63]);
   cfg.gridDim = dim3(unsigned(2 * clusters), 1, 1);
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, gl.w1, gl.w2, gl.p);
+  return cudaLaunchKernelEx(&cfg, kern, gl.a, gl.a2, gl.w1, gl.w2, gl.p);
 }
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
@@ -96,13 +96,20 @@ int run_grouped(const void *A, const void *W1, const void *W2, bool fused, const
     return cudaMemsetAsync(Y, 0, y_bytes, gl.stream) == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
   if (cudaGetDevice(&gl.device) != cudaSuccess) return SWIGLU_ERR_CUDA;
 
+  // Tiles of up to 256 rows read each weight once per 256 rows; tiles of up to
+  // 64 rows leave shared memory for more weight boxes in flight, which is
+  // what counts when a group has a few rows and the weights' stream is the cost.
+  const int nt = P > 48 * E ? 256 : 64;
+  const uint64_t adim[2] = {uint64_t(K), uint64_t(T)}, astr[1] = {uint64_t(K) * 2};
+  const uint32_t abox[2] = {64, rows ? 1u : 32u}, abox2[2] = {64, uint32_t(nt / 2)};
   const uint64_t wdim[3] = {uint64_t(N), uint64_t(K), uint64_t(E)};
   const uint64_t wstr[2] = {uint64_t(N) * 2, uint64_t(N) * K * 2};
   const uint32_t wbox[3] = {64, 64, 1};
-  rc = encode_bf16_map(&gl.w1, W1, 3, wdim, wstr, wbox);
+  rc = encode_bf16_map(&gl.a, A, 2, adim, astr, abox);
+  if (!rows && rc == SWIGLU_OK) rc = encode_bf16_map(&gl.a2, A, 2, adim, astr, abox2);
+  if (rc == SWIGLU_OK) rc = encode_bf16_map(&gl.w1, W1, 3, wdim, wstr, wbox);
   if (rc == SWIGLU_OK) rc = encode_bf16_map(&gl.w2, fused ? W2 : W1, 3, wdim, wstr, wbox);
   if (rc != SWIGLU_OK) return rc;
-  p.A = static_cast<const __nv_bfloat16 *>(A);
   p.offsets = offsets;
   p.rows = rows;
   p.Y = static_cast<__nv_bfloat16 *>(Y);
@@ -110,13 +117,8 @@ int run_grouped(const void *A, const void *W1, const void *W2, bool fused, const
   p.P = int32_t(P);
   p.E = int32_t(E);
   p.N = int32_t(N);
-  p.K = int32_t(K);
   p.num_k_blk = int32_t(ceil_div(K, 64));
   p.num_n_blk = int32_t(ceil_div(N, fused ? 128 : 256));
-  // Tiles of up to 256 rows read each weight once per 256 rows; tiles of up to
-  // 64 rows leave shared memory for more weight boxes in flight, which is
-  // what counts when a group has a few rows and the weights' stream is the cost.
-  const int nt = P > 48 * E ? 256 : 64;
   gl.units = (std::min(E, P) + P / nt) * p.num_n_blk;
   cudaError_t e;
   if (fused)

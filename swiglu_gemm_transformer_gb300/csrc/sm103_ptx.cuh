@@ -405,22 +405,33 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Asynchronous 16-byte copy global -> shared by this thread; zeros where
-// `valid` is false (the address is then not read).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
+// Four rows r0..r3 of a 2-D tensor, columns from c0 on (a one-row box), into
+// four consecutive rows of this CTA's shared memory (TMA gather4); completion
+// as above.
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap *m,
+                                                 uint32_t bar_cluster, int32_t c0, int32_t r0,
+                                                 int32_t r1, int32_t r2, int32_t r3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
+      ".mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(r0), "r"(r1), "r"(r2),
+      "r"(r3)
+      : "memory");
 }
 
-// One of the barrier's expected arrivals, made when every earlier cp.async of
-// this thread has landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
+// True in one thread of a converged warp.  A role run by one thread takes its
+// branch on this rather than on a lane number: the compiler then knows that
+// one thread is active, and issues the instructions that want uniform
+// operands (TMA, tcgen05.mma) directly instead of in a loop over the lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // Whole warp, in BOTH CTAs of the pair: allocate `ncols` TMEM columns in each.

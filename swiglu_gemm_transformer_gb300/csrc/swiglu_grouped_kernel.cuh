@@ -20,17 +20,20 @@
 //     for up to NT rows;
 //   * FUSED with two MMAs of M = 128 (gate, up) would put both values of an
 //     output into one TMEM lane, but reads the rows' tile from shared memory
-//     twice and is bound by that (1.31 against 1.57 PFLOP/s of the linear
-//     form at 64 experts x 1024 rows, K = 2048); so the gate lanes (0-63) and
+//     twice (measured 1.31 PFLOP/s where the linear form ran 1.57: 64 experts x
+//     1024 rows, K = 2048); so the gate lanes (0-63) and
 //     up lanes (64-127) trade half their values through shared memory;
 //   * weights are loaded MN-major straight from the row-major [E, K, N]
 //     tensors through 3-D tensor maps, whose K extent ends at each expert's
 //     last row, so a ragged K step never multiplies the next expert's
 //     weights;
-//   * four warps of each CTA copy its half of the tile's rows with cp.async,
-//     through `rows` or directly.  TMA gather4 for the same rows took about 75
-//     cycles per four rows however it was issued and bound the kernel (1118
-//     against ... us at 64 experts x 1024 rows, K = 2048, N = 1024);
+//   * each CTA loads its half of the tile's rows with TMA: gathered rows four
+//     at a time (gather4), a full dense half in one box, a part of one in boxes
+//     of 32 rows.  Several warps issue them, one thread each, chosen with
+//     elect.sync: issued by lane 0 of one warp they took about 50 ns apiece
+//     (gate/up with rows at 64 experts x 1024 rows, K = 2048, N = 1024: 1118 us;
+//     rows copied with cp.async instead 374 us; eight warps like this 326 us, four
+//     366 us, sixteen 320 us but a third fewer registers a thread);
 //   * accumulators are double-buffered in TMEM (256 columns each).
 // Unit schedule: every CTA reads `offsets`, counts the row tiles of each
 // expert, and the pairs take the units (expert, row tile, column tile) in
@@ -55,11 +58,10 @@ namespace swiglu {
 constexpr int kMaxExperts = 1024;
 
 struct GroupedParams {
-  const __nv_bfloat16 *A;  // [T, K]
   const int32_t *offsets;  // [E + 1]
   const int32_t *rows;     // [P] or null
   __nv_bfloat16 *Y;        // [P, N]
-  int32_t T, P, E, N, K;   // rows of A, rows of Y, experts, output columns, inner size
+  int32_t T, P, E, N;      // rows of A, rows of Y, experts, output columns
   int32_t num_k_blk, num_n_blk;
   uint64_t timeout_ns;
   uint32_t *err;
@@ -88,16 +90,17 @@ struct GroupedCfg {
   static constexpr int TAB_BYTES = 2 * (kMaxExperts + 1) * 4;
   static constexpr int UNIT_OFF = (TAB_OFF + TAB_BYTES + 15) / 16 * 16;  // two blocks of 32 units
   static constexpr int BAR_OFF = UNIT_OFF + 2 * 32 * 16;
-  static constexpr int NUM_BARS = 3 * STAGES + 9;
+  static constexpr int NUM_BARS = 2 * STAGES + 9;
   static constexpr int SMEM_BYTES = BAR_OFF + NUM_BARS * 8 + 16 + 1024;
   static constexpr int PRODUCER_WARP = EPI_WARPS;
   static constexpr int MMA_WARP = EPI_WARPS + 1;
   static constexpr int ROW_WARP = EPI_WARPS + 2;  // first of the warps that load rows
-  static constexpr int ROW_WARPS = 4;
+  static constexpr int ROW_WARPS = 8;
   static constexpr int UNIT_WARP = ROW_WARP + ROW_WARPS;
   static constexpr int THREADS = 32 * (UNIT_WARP + 1);
   // warps that read the units: epilogue, row loaders, producer, MMA
   static constexpr int UNIT_READERS = EPI_WARPS + ROW_WARPS + 2;
+  static_assert(NT / 8 % ROW_WARPS == 0, "gathers split evenly");
   static constexpr int MMA_M = 256;
   static constexpr int ACC_COLS = 256; // TMEM columns of one accumulator buffer
   static constexpr int GROUP = 8;
@@ -163,7 +166,9 @@ class GroupedUnits {
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
-    swiglu_grouped_kernel(const __grid_constant__ CUtensorMap tmW1,
+    swiglu_grouped_kernel(const __grid_constant__ CUtensorMap tmA,   // dense: boxes of 32 rows; gathered: one row
+                          const __grid_constant__ CUtensorMap tmA2,  // dense: boxes of NT / 2 rows
+                          const __grid_constant__ CUtensorMap tmW1,
                           const __grid_constant__ CUtensorMap tmW2,  // FUSED only
                           const GroupedParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -177,9 +182,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   auto accf_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + b); };
   auto acce_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + 2 + b); };
   const uint32_t drain_bar = bars + 8u * (2 * C::STAGES + 4);
-  auto row_bar = [&](int s) { return bars + 8u * (2 * C::STAGES + 5 + s); };
-  const uint32_t unitf_bar = bars + 8u * (3 * C::STAGES + 5);  // two each
-  const uint32_t unite_bar = bars + 8u * (3 * C::STAGES + 7);
+  const uint32_t unitf_bar = bars + 8u * (2 * C::STAGES + 5);  // two each
+  const uint32_t unite_bar = bars + 8u * (2 * C::STAGES + 7);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + C::NUM_BARS * 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *off = reinterpret_cast<int *>(smem + C::TAB_OFF);  // [E + 1] group bounds
@@ -191,11 +195,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const int cid = static_cast<int>(ptx::cluster_id_x());
   const int ncl = static_cast<int>(ptx::num_clusters_x());
 
+  const bool gather = p.rows != nullptr;
   if (warp == C::PRODUCER_WARP && lane == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(full_bar(s), 2);  // the expected bytes of the weights, the peer's rows
+      ptx::mbar_init(full_bar(s), 1);
       ptx::mbar_init(empty_bar(s), 1);
-      ptx::mbar_init(row_bar(s), 32 * C::ROW_WARPS);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(accf_bar(b), 1);
@@ -204,10 +208,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     ptx::mbar_init(drain_bar, 1);
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(unitf_bar + 8u * b, 1);
-      ptx::mbar_init(unite_bar + 8u * b, C::UNIT_READERS);
+      // (the odd CTA issues no MMAs: its MMA warp reads no units)
+      ptx::mbar_init(unite_bar + 8u * b, C::UNIT_READERS - (rank == 0 ? 0 : 1));
     }
     *abort_flag = 0;
     ptx::fence_barrier_init();
+    ptx::prefetch_tmap(&tmA);
+    if (!gather) ptx::prefetch_tmap(&tmA2);
     ptx::prefetch_tmap(&tmW1);
     if (C::FUSED) ptx::prefetch_tmap(&tmW2);
   }
@@ -290,14 +297,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (__any_sync(0xffffffffu, r.row0 < 0)) break;
     }
   } else if (warp == C::PRODUCER_WARP) {
-    // ------------------------------------------------------------ TMA producer (both CTAs)
-    uint32_t stage = 0, phase = 0, issued = 0;
-    bool ok = true;
-    if (lane == 0) {
+    // ------------------------------------------------------------ weights (both CTAs)
+    if (ptx::elect_one()) {
+      uint32_t stage = 0, phase = 0, issued = 0;
+      bool ok = true;
       GroupedUnits<true> units(ring, unitf_bar, unite_bar, p, abort_flag);
       GroupedUnit un;
       while (ok && units.next(un, ok)) {
         const int col0 = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS;
+        const int half = un.n() >> 1;
+        const uint32_t row_bytes = (gather ? half : (half + 31) & ~31) * C::BK * 2;
         for (int kb = 0; kb < p.num_k_blk; ++kb) {
           if (!wait_bar(empty_bar(stage), phase ^ 1u, p.timeout_ns, abort_flag, p.err,
                         WAIT_PRODUCER_EMPTY)) {
@@ -306,7 +315,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           const uint32_t sw = base + stage * C::STAGE_BYTES;
           const uint32_t fb = ptx::mapa_shared(full_bar(stage), 0);
-          if (rank == 0) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * C::W_BYTES);
+          // the bytes of both CTAs, weights and rows
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * (C::W_BYTES + row_bytes));
           ptx::tma_load_3d_pair(sw, &tmW1, fb, col0, kb * C::BK, un.e);
           if (C::FUSED)
             ptx::tma_load_3d_pair(sw + C::ATOM_BYTES, &tmW2, fb, col0, kb * C::BK, un.e);
@@ -331,76 +341,63 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= C::ROW_WARP) {
-    // ------------------------------------------------------------ row loaders (both CTAs)
-    // Thread i copies 16-byte piece i % 8 of rows i / 8 + 16 j of this CTA's
-    // half into the 128-byte swizzle (piece c of row r at c ^ (r % 8)).
-    const int tid = (warp - C::ROW_WARP) * 32 + lane;
-    const int piece = tid & 7, r = tid >> 3;
-    const uint32_t dst = base + C::W_BYTES + r * 128 + ((piece ^ (r & 7)) << 4);
-    constexpr int STEP = 4 * C::ROW_WARPS;   // rows per pass of the four warps
-    constexpr int PASSES = C::NT / 2 / STEP;
-    uint32_t stage = 0, phase = 0;
-    bool ok = true;
-    GroupedUnits<false> units(ring, unitf_bar, unite_bar, p, abort_flag);
-    GroupedUnit un;
-    while (units.next(un, ok)) {
-      const int half = un.n() >> 1;
-      const int passes = half / STEP;
-      const __nv_bfloat16 *src[PASSES];
-#pragma unroll
-      for (int j = 0; j < PASSES; ++j) {
-        // rows past the tile's end repeat its last one; their products are not stored
-        const int at = min(un.row0 + static_cast<int>(rank) * half + r + j * STEP, un.end - 1);
-        const int t = p.rows != nullptr && j < passes ? __ldg(p.rows + at) : at;
-        src[j] = p.A + int64_t(min(max(t, 0), p.T - 1)) * p.K + piece * 8;
-      }
-      for (int kb = 0; kb < p.num_k_blk; ++kb) {
-        if (!wait_bar(empty_bar(stage), phase ^ 1u, p.timeout_ns, abort_flag, p.err,
-                      WAIT_PRODUCER_EMPTY)) {
-          ok = false;
-          break;
-        }
-        const bool in = kb * C::BK + piece * 8 < p.K;  // K is a multiple of 8
-#pragma unroll
-        for (int j = 0; j < PASSES; ++j)
-          if (j < passes)
-            ptx::cp_async16(dst + stage * C::STAGE_BYTES + j * STEP * 128,
-                            src[j] + (in ? kb * C::BK : 0), in);
-        ptx::cp_async_arrive(row_bar(stage));
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      if (!__all_sync(0xffffffffu, ok)) break;
-    }
-    ptx::cp_async_wait_all();
-    __syncwarp();
-  } else if (warp == C::MMA_WARP) {
-    if (lane == 0 && rank != 0) {
-      // ---------------------------------------------------------- the odd CTA's rows
-      // Tells the leader that this CTA's rows of a stage have landed: the MMA
-      // reads them through the async proxy, so the fence stands between.
+    // ------------------------------------------------------------ rows (both CTAs)
+    if (ptx::elect_one()) {
+      const int w = warp - C::ROW_WARP;
+      constexpr int PER = C::NT / 8 / C::ROW_WARPS;  // gathers of a warp per stage
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       GroupedUnits<true> units(ring, unitf_bar, unite_bar, p, abort_flag);
       GroupedUnit un;
-      while (ok && units.next(un, ok))
+      while (ok && units.next(un, ok)) {
+        const int half = un.n() >> 1;
+        const int row0 = un.row0 + static_cast<int>(rank) * half;
+        // Rows past the tile's end: gathered, its last row again; dense, other
+        // tiles' rows or zeros.  Their products are not stored.
+        int idx[PER][4];
+        if (gather) {
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = min(row0 + 4 * (w + j * C::ROW_WARPS) + i, un.end - 1);
+              idx[j][i] = min(max(__ldg(p.rows + at), 0), p.T - 1);
+            }
+        }
         for (int kb = 0; kb < p.num_k_blk; ++kb) {
-          if (!wait_bar(row_bar(stage), phase, p.timeout_ns, abort_flag, p.err, WAIT_ROWS)) {
+          if (!wait_bar(empty_bar(stage), phase ^ 1u, p.timeout_ns, abort_flag, p.err,
+                        WAIT_PRODUCER_EMPTY)) {
             ok = false;
             break;
           }
-          ptx::fence_proxy_async_smem();
-          ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(full_bar(stage), 0));
+          const uint32_t sa = base + stage * C::STAGE_BYTES + C::W_BYTES;
+          const uint32_t fb = ptx::mapa_shared(full_bar(stage), 0);
+          if (gather) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+              const int g = w + j * C::ROW_WARPS;
+              if (4 * g < half)
+                ptx::tma_gather4_pair(sa + g * 512, &tmA, fb, kb * C::BK, idx[j][0], idx[j][1],
+                                      idx[j][2], idx[j][3]);
+            }
+          } else if (half == C::NT / 2) {
+            if (w == 0) ptx::tma_load_2d_pair(sa, &tmA2, fb, kb * C::BK, row0);
+          } else {
+            for (int i = 32 * w; i < half; i += 32 * C::ROW_WARPS)
+              ptx::tma_load_2d_pair(sa + i * 128, &tmA, fb, kb * C::BK, row0 + i);
+          }
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
+      }
+      if (!ok) spin_ns(100000);  // aborted: copies already in flight into this CTA land
     }
+    __syncwarp();
+  } else if (warp == C::MMA_WARP) {
     // ------------------------------------------------------------ MMA issuer (leader only)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && ptx::elect_one()) {
       uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
       bool ok = true;
       GroupedUnits<true> units(ring, unitf_bar, unite_bar, p, abort_flag);
@@ -413,13 +410,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + abuf * C::ACC_COLS;
         for (int kb = 0; kb < p.num_k_blk; ++kb) {
-          if (!wait_bar(row_bar(stage), phase, p.timeout_ns, abort_flag, p.err, WAIT_ROWS) ||
-              !wait_bar_cluster(full_bar(stage), phase, p.timeout_ns, abort_flag, p.err,
-                                WAIT_MMA_FULL)) {
+          if (!wait_bar(full_bar(stage), phase, p.timeout_ns, abort_flag, p.err, WAIT_MMA_FULL)) {
             ok = false;
             break;
           }
-          ptx::fence_proxy_async_smem();
           ptx::tc_fence_after();
           const uint32_t sw = base + stage * C::STAGE_BYTES;
           const uint32_t sa = sw + C::W_BYTES;

@@ -20,7 +20,6 @@ enum : uint32_t {
   WAIT_DRAIN = 5,
   WAIT_SELFTEST = 6,
   WAIT_SCHED_FULL = 9,   // a pair kernel role waiting for the next unit's response
-  WAIT_ROWS = 11,        // the grouped kernel waiting for a stage's rows
   WAIT_SCHED_EMPTY = 10, // the pair's scheduler waiting for a response slot
 };
 
@@ -79,17 +78,6 @@ __device__ __forceinline__ static bool wait_bar(uint32_t bar, uint32_t parity, u
                                                 uint32_t where) {
   if (ptx::mbar_try_wait(bar, parity)) return true;
   return wait_slow(bar, parity, limit_ns, abort_flag, err, where);
-}
-
-// wait_bar with cluster-scope acquire, for what a thread of the other CTA
-// released.
-__device__ __forceinline__ static bool wait_bar_cluster(uint32_t bar, uint32_t parity,
-                                                        uint64_t limit_ns,
-                                                        volatile int *abort_flag, uint32_t *err,
-                                                        uint32_t where) {
-  while (!ptx::mbar_try_wait_cluster(bar, parity))
-    if (!wait_slow(bar, parity, limit_ns, abort_flag, err, where)) return false;
-  return true;
 }
 
 // Bounded wait that records nothing (used while draining after an abort).
