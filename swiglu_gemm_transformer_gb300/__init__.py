@@ -85,6 +85,8 @@ class SwigluError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded C library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -119,11 +121,11 @@ def _check(fn: str, rc: int):
 
 def _stream(stream):
     import torch
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _on_tensor_device(fn):
@@ -133,14 +135,19 @@ def _on_tensor_device(fn):
     @functools.wraps(fn)
     def call(*args, **kw):
         import torch
-        ts = [a for a in list(args) + list(kw.values()) if isinstance(a, torch.Tensor)]
-        devs = {t.device for t in ts}
-        if len(devs) > 1:
-            raise ValueError(f"{fn.__name__}: tensors on several devices: {sorted(map(str, devs))}")
-        if ts and ts[0].is_cuda:
-            with torch.cuda.device(ts[0].device):
-                return fn(*args, **kw)
-        return fn(*args, **kw)
+        dev = None  # device number of the tensors (-1: CPU)
+        for a in (*args, *kw.values()):
+            if isinstance(a, torch.Tensor):
+                d = a.get_device()
+                if dev is None:
+                    dev = d
+                elif d != dev:
+                    devs = {str(t.device) for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)}
+                    raise ValueError(f"{fn.__name__}: tensors on several devices: {sorted(devs)}")
+        if dev is None or dev < 0 or dev == torch._C._cuda_getDevice():
+            return fn(*args, **kw)
+        with torch.cuda.device(dev):
+            return fn(*args, **kw)
     return call
 
 
