@@ -236,9 +236,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // Group bounds and row-tile counts.  The bounds are clamped to [0, P] and
     // made monotone, so that no value of `offsets` reaches past Y.
     int top = 0, sum = 0;
+    constexpr int AHEAD = 4;  // loads in flight: each is a trip to memory
+    int raw[AHEAD];
     for (int e0 = 0; e0 <= p.E; e0 += 32) {
-      const int e = e0 + lane;
-      int v = e <= p.E ? min(max(__ldg(p.offsets + e), 0), p.P) : 0;
+      const int e = e0 + lane, slot = (e0 / 32) % AHEAD;
+      if (slot == 0) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          raw[i] = e + 32 * i <= p.E ? __ldg(p.offsets + e + 32 * i) : 0;
+      }
+      int v = raw[0];
+#pragma unroll
+      for (int i = 1; i < AHEAD; ++i) v = slot == i ? raw[i] : v;
+      v = e <= p.E ? min(max(v, 0), p.P) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int w = __shfl_up_sync(0xffffffffu, v, o);
