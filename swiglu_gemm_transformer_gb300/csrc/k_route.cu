@@ -7,23 +7,26 @@
 //     weights[t,j] = scale * p, or scale * p / (sum of the chosen p)
 //     rows, slots  = the entries (t, j) in the order (expert, t k + j)
 //
-// One warp per token: lane l holds the logits of experts l, l + 32, ..., as
-// 32-bit keys whose unsigned order is the floats' order (0 = no expert: a
-// masked logit of -inf or a lane past E).  One round per choice: a warp
-// maximum of the keys, then a warp minimum of the expert numbers that hold
-// it, so ties need no second pass.
+// LPT lanes per token (4 to 32: at least k, and eight experts a lane while that
+// is enough): lane l holds the logits of experts l, l + LPT, ... as 32-bit keys
+// whose unsigned order is the floats' order.  A key of 0 is no expert: a masked
+// logit of -inf, or a lane past E.  A choice is one maximum over the group's
+// lanes (log2(LPT) shuffles) of the key with the complement of the expert's
+// number below it, so that among equal logits the lowest number wins.  What
+// counts is the length of this chain (k rounds of it, each on the one before),
+// so nothing in it branches.
 //
 // The order is a counting sort that keeps entries in sequence, without
 // atomics, so its result does not depend on timing: each warp counts its own
 // tokens' entries by expert (equal experts within 32 entries are found with
 // match_any), the warps' counts are summed in order, and each warp walks its
-// entries again and numbers them.
+// entries again and numbers them within the block.
 //
-// Up to kOneTokens tokens one block does all of it in one launch.  Beyond
-// that a first kernel chooses and counts per block of tokens (counts go to
-// the workspace) and a second one, overlapped by programmatic dependent
-// launch, sums the counts of the blocks before its own and numbers its
-// entries.
+// Up to kBlockTokens tokens one block does all of it in one launch.  Beyond
+// that a first kernel does so per block of tokens (each entry's number within
+// its block goes to slots, the block's counts to the workspace), and a second
+// one, overlapped by programmatic dependent launch, sums the counts of the
+// blocks before its own and adds them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -40,10 +43,8 @@ namespace {
 
 constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
-constexpr int kWarps = 16;               // warps per block
-constexpr int kThreads = 32 * kWarps;
-constexpr int kBlockTokens = 128;        // tokens per block, several blocks
-constexpr int kOneTokens = 128;          // tokens of the one-block form
+constexpr int kBlockTokens = 128;        // tokens per block
+constexpr int kCounters = 16384;         // warps of a block x experts
 constexpr unsigned kAll = 0xffffffffu;
 
 struct RouteParams {
@@ -57,109 +58,108 @@ struct RouteParams {
   float scale;
 };
 
-// Unsigned key with the order of the floats; -inf -> 0 (masked), NaN above
+// Unsigned number with the order of the floats; -inf -> 0 (masked), NaN above
 // +inf (it is chosen first and its weight comes out NaN, so it stays visible).
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x == -INFINITY) return 0u;
-  if (x != x) return 0xffffffffu;
-  if (x == 0.0f) return 0x80000000u;  // both zeros
-  const uint32_t b = __float_as_uint(x);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));  // -0 becomes +0
+  const uint32_t k = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+  return x != x ? 0xffffffffu : k == 0x007fffffu ? 0u : k;
 }
 
 __device__ __forceinline__ float key_value(uint32_t key) {
-  if (key == 0xffffffffu) return NAN;
-  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+  const uint32_t b = key ^ ((key & 0x80000000u) ? 0x80000000u : 0xffffffffu);
+  return key == 0u ? -INFINITY : __uint_as_float(b);  // all ones -> a NaN
 }
 
-__device__ __forceinline__ float warp_total(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
-}
-
-// One token by one warp; the chosen experts go to `ids16` (shared; 0xffff =
-// none) and to global memory.
-template <int EPL, bool FP32>
-__device__ __forceinline__ void choose(const RouteParams &p, int t, int lane, uint16_t *ids16) {
+// The token t of this lane's group of LPT >= k lanes (or none: t >= end), its
+// chosen experts to ids16 (shared; 0xffff = none) and global memory.  All
+// lanes of the warp call it together.
+template <int LPT, int EPL, bool FP32>
+__device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane,
+                                       uint16_t *ids16) {
+  using Pick = unsigned long long;  // key above ~expert; 0 in the upper half: none
+  const int l = lane & (LPT - 1);
+  const bool live = t < end;
+  float x[EPL];
   uint32_t key[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = 0u;
-    if (e < p.E) {
-      const int64_t at = int64_t(t) * p.E + e;
-      key[i] = order_key(FP32 ? __ldg(static_cast<const float *>(p.logits) + at)
-                              : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[at]));
+    const int e = l + LPT * i;
+    x[i] = -INFINITY;
+    if (live && e < p.E) {
+      const int64_t at = t * p.E + e;
+      x[i] = FP32 ? __ldg(static_cast<const float *>(p.logits) + at)
+                  : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[at]);
     }
   }
-  uint32_t best = 0u;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) best = max(best, key[i]);
-  const uint32_t top = __reduce_max_sync(kAll, best);
-  const float m = key_value(top);
-  float sum = 0.0f;
-  if (!p.renormalize && top != 0u) {
+  for (int i = 0; i < EPL; ++i) key[i] = order_key(x[i]);
+  // this lane's largest key, the first that holds it
+  auto best = [&]() {
+    uint32_t b[EPL];
+    int w[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (key[i] != 0u) sum += expf(key_value(key[i]) - m);
-    sum = warp_total(sum);
-  }
-  int my_id = -1;       // lane j keeps choice j
-  float my_e = 0.0f;
-  for (int j = 0; j < p.k; ++j) {
-    const uint32_t mx = j == 0 ? top : __reduce_max_sync(kAll, best);
-    if (mx == 0u) break;
-    uint32_t at = 0xffffffffu;
-    if (best == mx) {
+    for (int i = 0; i < EPL; ++i) b[i] = key[i], w[i] = i;
 #pragma unroll
-      for (int i = EPL - 1; i >= 0; --i)
-        if (key[i] == mx) at = lane + 32 * i;
-    }
-    const uint32_t e = __reduce_min_sync(kAll, at);
-    if (lane == j) {
-      my_id = static_cast<int>(e);
-      my_e = expf(key_value(mx) - m);
-    }
-    if (at == e) {  // the owner takes it out
-      best = 0u;
+    for (int st = 1; st < EPL; st <<= 1)
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        if (lane + 32 * i == static_cast<int>(e)) key[i] = 0u;
-        best = max(best, key[i]);
+      for (int i = 0; i + st < EPL; i += 2 * st) {
+        const bool up = b[i + st] > b[i];
+        b[i] = up ? b[i + st] : b[i];
+        w[i] = up ? w[i + st] : w[i];
       }
+    return (Pick(b[0]) << 32) | ~static_cast<uint32_t>(l + LPT * w[0]);
+  };
+  auto group_max = [](Pick v) {
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) {
+      const Pick u = __shfl_xor_sync(kAll, v, o);
+      v = u > v ? u : v;
     }
+    return v;
+  };
+  Pick mx = group_max(best());
+  const float m = key_value(static_cast<uint32_t>(mx >> 32));
+  float sum = 0.0f;
+  if (!p.renormalize) {
+    // a masked logit adds exp(-inf) = 0 (where all are, the sum is not used)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sum += expf(x[i] - m);
   }
-  if (p.renormalize) sum = warp_total(my_e);
-  if (lane < p.k) {
-    const int64_t at = int64_t(t) * p.k + lane;
-    p.ids[at] = my_id;
-    p.weights[at] = my_id < 0 ? 0.0f : p.scale * (my_e / sum);
-    ids16[lane] = my_id < 0 ? uint16_t(0xffff) : uint16_t(my_id);
+  uint32_t my_key = 0u;  // lane j of the group keeps choice j
+  int my_id = -1;
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t top = static_cast<uint32_t>(mx >> 32);
+    const int e = top != 0u ? static_cast<int>(~static_cast<uint32_t>(mx)) : -1;
+    my_key = l == j ? top : my_key;
+    my_id = l == j ? e : my_id;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = l + LPT * i == e ? 0u : key[i];
+    mx = group_max(best());
+  }
+  const float w = my_id < 0 ? 0.0f : expf(key_value(my_key) - m);
+  sum = p.renormalize ? w : sum;
+#pragma unroll
+  for (int o = LPT / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  if (live && l < p.k) {
+    p.ids[t * p.k + l] = my_id;
+    p.weights[t * p.k + l] = my_id < 0 ? 0.0f : p.scale * (w / sum);
+    ids16[l] = static_cast<uint16_t>(my_id);  // -1 -> 0xffff
   }
 }
 
-// Walks this warp's entries [i0, i1) of the block, 32 at a time.  NUMBER =
-// false: counts them into cnt[expert]; true: cnt[expert] holds the number of
-// entries of the block before this warp's, and each entry gets its place.
-template <bool NUMBER>
-__device__ __forceinline__ void walk(const RouteParams &p, const uint16_t *ids16, int i0, int i1,
-                                     uint16_t *cnt, const int32_t *base, int t0, int lane) {
+// Walks this warp's entries [i0, i1) of the block, 32 at a time, adding them to
+// cnt[expert]; number(i, e, before) gets each entry's expert and the entries
+// counted before it (e = 0xffff: none).
+template <class F>
+__device__ __forceinline__ void walk(const uint16_t *ids16, int i0, int i1, uint16_t *cnt, int lane,
+                                     F number) {
   for (int b = i0; b < i1; b += 32) {
     const int i = b + lane;
     const unsigned e = i < i1 ? ids16[i] : 0xffffu;
     const unsigned same = __match_any_sync(kAll, e);
     const unsigned before = same & ((1u << lane) - 1u);
-    if (NUMBER && i < i1) {
-      const int64_t entry = int64_t(t0) * p.k + i;
-      if (e != 0xffffu) {
-        const int pos = base[e] + cnt[e] + __popc(before);
-        p.slots[entry] = pos;
-        p.rows[pos] = static_cast<int32_t>(entry / p.k);
-      } else {
-        p.slots[entry] = -1;
-      }
-    }
+    if (i < i1) number(i, e, e != 0xffffu ? cnt[e] + __popc(before) : 0);
     __syncwarp();
     if (e != 0xffffu && before == 0u) cnt[e] += static_cast<uint16_t>(__popc(same));
     __syncwarp();
@@ -167,138 +167,111 @@ __device__ __forceinline__ void walk(const RouteParams &p, const uint16_t *ids16
 }
 
 struct RouteSmem {
-  uint16_t cnt[kWarps][kMaxE];
+  uint16_t cnt[kCounters];  // [warp][E]
   int32_t base[kMaxE];
   uint16_t ids[kBlockTokens * kMaxK];
-  int32_t carry[33];
+  int32_t carry[32];
 };
 
-// Replaces v (one value per thread; thread i < n holds element i) by the sum
-// of the elements before it; `total` gets the sum.  All threads.
-__device__ __forceinline__ int block_exclusive_scan(int v, int32_t *carry, int &total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
+// Exclusive scan of base[0, E) in place; returns the total.  All threads.
+__device__ __forceinline__ int scan_experts(RouteSmem &sm, int E, int32_t *offsets) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int carried = 0;
+  for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+    const int e = e0 + threadIdx.x;
+    const int v = e < E ? sm.base[e] : 0;
+    int s = v;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int w = __shfl_up_sync(kAll, s, o);
-    if (lane >= o) s += w;
-  }
-  if (lane == 31) carry[warp] = s;
-  __syncthreads();
-  if (warp == 0) {
-    int c = lane < kWarps ? carry[lane] : 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(kAll, s, o);
+      if (lane >= o) s += w;
+    }
+    if (lane == 31) sm.carry[warp] = s;
+    __syncthreads();
+    int c = lane < warps ? sm.carry[lane] : 0;  // every warp scans the warps' sums
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int w = __shfl_up_sync(kAll, c, o);
       if (lane >= o) c += w;
     }
-    carry[lane] = c;
-  }
-  __syncthreads();
-  const int before = warp > 0 ? carry[warp - 1] : 0;
-  total = carry[kWarps - 1];
-  __syncthreads();
-  return before + s - v;
-}
-
-// cnt[w][e] -> entries of the block's warps before w; returns the block's
-// count of each of this thread's experts through `counted(e, n)`.
-template <class F>
-__device__ __forceinline__ void scan_warps(RouteSmem &sm, int E, F counted) {
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    int run = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const int c = sm.cnt[w][e];
-      sm.cnt[w][e] = static_cast<uint16_t>(run);
-      run += c;
-    }
-    counted(e, run);
-  }
-}
-
-__device__ __forceinline__ void clear_counts(RouteSmem &sm, int E) {
-  for (int i = threadIdx.x; i < kWarps * E; i += kThreads) sm.cnt[i / E][i % E] = 0;
-}
-
-// base[e] (the count of expert e) -> first place of expert e, for all E
-// experts; returns the number of routed entries.
-__device__ __forceinline__ int scan_experts(RouteSmem &sm, int E, int32_t *offsets) {
-  int carried = 0;
-  for (int e0 = 0; e0 < E; e0 += kThreads) {
-    const int e = e0 + threadIdx.x;
-    int total;
-    const int before = block_exclusive_scan(e < E ? sm.base[e] : 0, sm.carry, total);
+    const int before = __shfl_sync(kAll, c, max(warp - 1, 0));
+    const int first = carried + (warp > 0 ? before : 0) + s - v;
     if (e < E) {
-      sm.base[e] = carried + before;
-      if (offsets) offsets[e] = carried + before;
+      sm.base[e] = first;
+      if (offsets) offsets[e] = first;
     }
-    carried += total;
+    carried += __shfl_sync(kAll, c, 31);
+    __syncthreads();
   }
   if (offsets && threadIdx.x == 0) offsets[E] = carried;
   return carried;
 }
 
-// Everything in one block.
-template <int EPL, bool FP32>
-__global__ void __launch_bounds__(kThreads) route_one_kernel(const RouteParams p) {
+// One block of tokens; ONE: the whole call, otherwise the first pass of it.
+template <int LPT, int EPL, bool FP32, bool ONE>
+__global__ void __launch_bounds__(EPL > 8 ? 512 : 1024, 1) route_choose_kernel(const RouteParams p) {
   __shared__ RouteSmem sm;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  uint16_t *cnt = sm.cnt + warp * p.E;
   ptx::grid_launch_dependents();
-  clear_counts(sm, p.E);
+  for (int e = lane; e < p.E; e += 32) cnt[e] = 0;
   ptx::grid_dependency_wait();
-  const int per = (p.T + kWarps - 1) / kWarps;
-  const int t0 = min(warp * per, p.T), t1 = min(t0 + per, p.T);
-  for (int t = t0; t < t1; ++t) choose<EPL, FP32>(p, t, lane, sm.ids + t * p.k);
-  __syncthreads();
-  walk<false>(p, sm.ids, t0 * p.k, t1 * p.k, sm.cnt[warp], nullptr, 0, lane);
-  __syncthreads();
-  scan_warps(sm, p.E, [&](int e, int n) { sm.base[e] = n; });
-  __syncthreads();
-  const int routed = scan_experts(sm, p.E, p.offsets);
-  __syncthreads();
-  walk<true>(p, sm.ids, t0 * p.k, t1 * p.k, sm.cnt[warp], sm.base, 0, lane);
-  for (int i = routed + threadIdx.x; i < p.T * p.k; i += kThreads) p.rows[i] = -1;
-}
-
-// Several blocks, first pass: choose, and count the block's entries.
-template <int EPL, bool FP32>
-__global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParams p) {
-  __shared__ RouteSmem sm;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  ptx::grid_launch_dependents();
-  clear_counts(sm, p.E);
-  ptx::grid_dependency_wait();
-  const int b0 = blockIdx.x * kBlockTokens, nt = min(kBlockTokens, p.T - b0);
-  const int per = (nt + kWarps - 1) / kWarps;
+  const int64_t b0 = int64_t(blockIdx.x) * kBlockTokens;
+  const int nt = static_cast<int>(min(int64_t(kBlockTokens), p.T - b0));
+  // each warp takes a run of tokens, 32 / LPT at a time
+  constexpr int SIDE = 32 / LPT;
+  const int per = (nt + warps * SIDE - 1) / (warps * SIDE) * SIDE;
   const int t0 = min(warp * per, nt), t1 = min(t0 + per, nt);
-  for (int t = t0; t < t1; ++t) choose<EPL, FP32>(p, b0 + t, lane, sm.ids + t * p.k);
+  for (int t = t0; t < t1; t += SIDE)
+    choose<LPT, EPL, FP32>(p, b0 + t + lane / LPT, b0 + t1, lane, sm.ids + (t + lane / LPT) * p.k);
+  __syncwarp();
+  walk(sm.ids, t0 * p.k, t1 * p.k, cnt, lane, [](int, unsigned, int) {});
   __syncthreads();
-  walk<false>(p, sm.ids, t0 * p.k, t1 * p.k, sm.cnt[warp], nullptr, 0, lane);
+  // the warps' counts of each expert, in order
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    int run = 0;
+    for (int w = 0; w < warps; ++w) {
+      const int c = sm.cnt[w * p.E + e];
+      sm.cnt[w * p.E + e] = static_cast<uint16_t>(run);
+      run += c;
+    }
+    if (ONE)
+      sm.base[e] = run;
+    else
+      p.counts[int64_t(blockIdx.x) * p.E + e] = run;
+  }
   __syncthreads();
-  scan_warps(sm, p.E, [&](int e, int n) { p.counts[int64_t(blockIdx.x) * p.E + e] = n; });
+  const int routed = ONE ? scan_experts(sm, p.E, p.offsets) : 0;
+  walk(sm.ids, t0 * p.k, t1 * p.k, cnt, lane, [&](int i, unsigned e, int before) {
+    const int64_t entry = b0 * p.k + i;
+    if (ONE && e != 0xffffu) {
+      before += sm.base[e];
+      p.rows[before] = i / p.k;  // ONE: b0 = 0
+    }
+    p.slots[entry] = e == 0xffffu ? -1 : before;
+  });
+  if (ONE)
+    for (int i = routed + threadIdx.x; i < p.T * p.k; i += blockDim.x) p.rows[i] = -1;
 }
 
-// Several blocks, second pass: places of the block's entries.
-__global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteParams p) {
+// Several blocks, second pass: the block's entries get their places.
+__global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) {
   __shared__ RouteSmem sm;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.x;
   ptx::grid_launch_dependents();
-  clear_counts(sm, p.E);
   int32_t *mine = reinterpret_cast<int32_t *>(sm.ids);  // [E] entries of the blocks before this one
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
     sm.base[e] = 0;
     mine[e] = 0;
   }
   ptx::grid_dependency_wait();
   __syncthreads();
-  // Counts of every block: thread (g, e) sums blocks g, g + G, ... (integer
-  // sums in shared memory: their order does not matter).
-  const int G = max(1, kThreads / p.E);
-  for (int e0 = 0; e0 < p.E; e0 += kThreads) {
-    const int e = e0 + (p.E >= kThreads ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) % p.E);
-    const int g = p.E >= kThreads ? 0 : threadIdx.x / p.E;
+  // Thread (g, e) sums blocks g, g + G, ... of expert e (integer sums in
+  // shared memory: their order does not matter).
+  const int G = max(1, static_cast<int>(blockDim.x) / p.E);
+  for (int e0 = 0; e0 < p.E; e0 += blockDim.x) {
+    const int e = e0 + static_cast<int>(threadIdx.x) % p.E;  // E > blockDim.x: e0 + threadIdx.x
+    const int g = threadIdx.x / p.E;
     if (e < p.E && g < G) {
       int all = 0, before = 0;
 #pragma unroll 8
@@ -313,46 +286,49 @@ __global__ void __launch_bounds__(kThreads) route_order_kernel(const RouteParams
   }
   __syncthreads();
   const int routed = scan_experts(sm, p.E, b == 0 ? p.offsets : nullptr);
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) sm.base[e] += mine[e];
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kThreads) sm.base[e] += mine[e];
-  __syncthreads();
-  const int b0 = b * kBlockTokens, nt = min(kBlockTokens, p.T - b0);
-  for (int i = threadIdx.x; i < nt * p.k; i += kThreads)
-    sm.ids[i] = static_cast<uint16_t>(__ldg(p.ids + int64_t(b0) * p.k + i));  // -1 -> 0xffff
-  __syncthreads();
-  const int per = (nt + kWarps - 1) / kWarps;
-  const int t0 = min(warp * per, nt), t1 = min(t0 + per, nt);
-  walk<false>(p, sm.ids, t0 * p.k, t1 * p.k, sm.cnt[warp], nullptr, b0, lane);
-  __syncthreads();
-  scan_warps(sm, p.E, [](int, int) {});
-  __syncthreads();
-  walk<true>(p, sm.ids, t0 * p.k, t1 * p.k, sm.cnt[warp], sm.base, b0, lane);
-  const int64_t entries = int64_t(p.T) * p.k;
-  for (int64_t i = routed + int64_t(b) * kThreads + threadIdx.x; i < entries;
-       i += int64_t(p.blocks) * kThreads)
+  const int64_t b0 = int64_t(b) * kBlockTokens, entries = int64_t(p.T) * p.k;
+  const int64_t end = min(b0 + kBlockTokens, int64_t(p.T)) * p.k;
+  for (int64_t i = b0 * p.k + threadIdx.x; i < end; i += blockDim.x) {
+    const int e = __ldg(p.ids + i);
+    if (e >= 0) {
+      const int pos = sm.base[e] + p.slots[i];
+      p.slots[i] = pos;
+      p.rows[pos] = static_cast<int32_t>(i) / p.k;  // T * k < 2^31
+    }
+  }
+  for (int64_t i = routed + int64_t(b) * blockDim.x + threadIdx.x; i < entries;
+       i += int64_t(p.blocks) * blockDim.x)
     p.rows[i] = -1;
 }
 
-cudaError_t launch_pdl(void (*kern)(RouteParams), int grid, const RouteParams &p, cudaStream_t s) {
+cudaError_t launch_pdl(void (*kern)(RouteParams), int grid, int threads, const RouteParams &p,
+                       cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int EPL>
+template <int LPT, int EPL>
 cudaError_t launch_route(bool fp32, const RouteParams &p, cudaStream_t s) {
-  if (p.T <= kOneTokens)
-    return launch_pdl(fp32 ? route_one_kernel<EPL, true> : route_one_kernel<EPL, false>, 1, p, s);
-  cudaError_t e = launch_pdl(fp32 ? route_choose_kernel<EPL, true> : route_choose_kernel<EPL, false>,
-                             p.blocks, p, s);
-  return e != cudaSuccess ? e : launch_pdl(route_order_kernel, p.blocks, p, s);
+  // warps: as many as there are groups of tokens, threads and counters for
+  const int groups = (std::min(p.T, kBlockTokens) + 32 / LPT - 1) / (32 / LPT);
+  const int warps = std::min({EPL > 8 ? 16 : 32, kCounters / p.E, groups});
+  if (p.blocks == 1)
+    return launch_pdl(fp32 ? route_choose_kernel<LPT, EPL, true, true>
+                           : route_choose_kernel<LPT, EPL, false, true>, 1, 32 * warps, p, s);
+  const cudaError_t e = launch_pdl(fp32 ? route_choose_kernel<LPT, EPL, true, false>
+                                        : route_choose_kernel<LPT, EPL, false, false>,
+                                   p.blocks, 32 * warps, p, s);
+  return e != cudaSuccess ? e : launch_pdl(route_place_kernel, p.blocks, 1024, p, s);
 }
 
 }  // namespace
@@ -360,7 +336,7 @@ cudaError_t launch_route(bool fp32, const RouteParams &p, cudaStream_t s) {
 
 extern "C" uint64_t swiglu_moe_route_workspace_size(int64_t T, int64_t E, int64_t k) {
   using namespace swiglu;
-  if (T <= kOneTokens || E < 1 || k < 1) return 0;
+  if (T <= kBlockTokens || E < 1 || k < 1) return 0;
   return uint64_t((T + kBlockTokens - 1) / kBlockTokens) * E * 4;
 }
 
@@ -414,11 +390,12 @@ extern "C" int swiglu_moe_route(const void *logits, int32_t logits_fp32, int32_t
   p.renormalize = renormalize;
   p.scale = scale;
   const bool f = logits_fp32 != 0;
-  const cudaError_t e = E <= 32    ? launch_route<1>(f, p, s)
-                        : E <= 64  ? launch_route<2>(f, p, s)
-                        : E <= 128 ? launch_route<4>(f, p, s)
-                        : E <= 256 ? launch_route<8>(f, p, s)
-                        : E <= 512 ? launch_route<16>(f, p, s)
-                                   : launch_route<32>(f, p, s);
+  const int64_t lanes = std::max((E + 7) / 8, k);  // per token
+  const cudaError_t e = lanes <= 4    ? launch_route<4, 8>(f, p, s)
+                        : lanes <= 8  ? launch_route<8, 8>(f, p, s)
+                        : lanes <= 16 ? launch_route<16, 8>(f, p, s)
+                        : E <= 256    ? launch_route<32, 8>(f, p, s)
+                        : E <= 512    ? launch_route<32, 16>(f, p, s)
+                                      : launch_route<32, 32>(f, p, s);
   return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
 }
