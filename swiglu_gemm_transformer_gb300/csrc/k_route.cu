@@ -22,11 +22,15 @@
 // match_any), the warps' counts are summed in order, and each warp walks its
 // entries again and numbers them within the block.
 //
-// Up to kBlockTokens tokens one block does all of it in one launch.  Beyond
-// that a first kernel does so per block of tokens (each entry's number within
-// its block goes to slots, the block's counts to the workspace), and a second
-// one, overlapped by programmatic dependent launch, sums the counts of the
-// blocks before its own and adds them.
+// Up to kOneTokens tokens are one launch of one cluster, 32 tokens a block: one
+// SM issues the choices of 128 tokens in about 6 us, so a few tokens are spread
+// over several; the blocks read each other's counts through distributed shared
+// memory (128 tokens: 5.4 us, in one block 9.1 us).  Beyond that a first kernel
+// numbers the entries within each block of 32 to 128 tokens (in slots) and writes
+// the block's counts to the workspace, and a second one, overlapped by
+// programmatic dependent launch, sums the counts of the blocks before its own
+// and adds them (16384 tokens: 12.6 us; in clusters of eight blocks of 32
+// tokens 15.2 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -43,7 +47,9 @@ namespace {
 
 constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
-constexpr int kBlockTokens = 128;        // tokens per block
+constexpr int kOneTokens = 256;          // tokens of the one-launch form,
+constexpr int kOneBlockTokens = 32;      // per block of its cluster (at most eight)
+constexpr int kBlockTokens = 128;        // most tokens per block otherwise
 constexpr int kCounters = 16384;         // warps of a block x experts
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -52,8 +58,8 @@ struct RouteParams {
   int32_t *ids;
   float *weights;
   int32_t *offsets, *rows, *slots;
-  int32_t *counts;  // [blocks][E], several blocks only
-  int32_t T, E, k, blocks;
+  int32_t *counts;  // [blocks][E], two launches only
+  int32_t T, E, k, blocks, block_tokens;
   int32_t renormalize;
   float scale;
 };
@@ -168,7 +174,8 @@ __device__ __forceinline__ void walk(const uint16_t *ids16, int i0, int i1, uint
 
 struct RouteSmem {
   uint16_t cnt[kCounters];  // [warp][E]
-  int32_t base[kMaxE];
+  int32_t base[kMaxE];      // first place of each expert's entries
+  int32_t total[kMaxE];     // entries of this block (read by the cluster's other blocks), or of the blocks before
   uint16_t ids[kBlockTokens * kMaxK];
   int32_t carry[32];
 };
@@ -207,17 +214,20 @@ __device__ __forceinline__ int scan_experts(RouteSmem &sm, int E, int32_t *offse
   return carried;
 }
 
-// One block of tokens; ONE: the whole call, otherwise the first pass of it.
+// One block of tokens; ONE: a block of the only cluster, which does the whole
+// call, otherwise the first pass of it.
 template <int LPT, int EPL, bool FP32, bool ONE>
-__global__ void __launch_bounds__(EPL > 8 ? 512 : 1024, 1) route_choose_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(1024, 1) route_choose_kernel(const RouteParams p) {
   __shared__ RouteSmem sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int rank = blockIdx.x, ranks = ONE ? gridDim.x : 1;
+  const int tokens = ONE ? kOneBlockTokens : p.block_tokens;
   uint16_t *cnt = sm.cnt + warp * p.E;
   ptx::grid_launch_dependents();
   for (int e = lane; e < p.E; e += 32) cnt[e] = 0;
   ptx::grid_dependency_wait();
-  const int64_t b0 = int64_t(blockIdx.x) * kBlockTokens;
-  const int nt = static_cast<int>(min(int64_t(kBlockTokens), p.T - b0));
+  const int64_t b0 = int64_t(blockIdx.x) * tokens;
+  const int nt = static_cast<int>(max(int64_t(0), min(int64_t(tokens), p.T - b0)));
   // each warp takes a run of tokens, 32 / LPT at a time
   constexpr int SIDE = 32 / LPT;
   const int per = (nt + warps * SIDE - 1) / (warps * SIDE) * SIDE;
@@ -236,21 +246,39 @@ __global__ void __launch_bounds__(EPL > 8 ? 512 : 1024, 1) route_choose_kernel(c
       run += c;
     }
     if (ONE)
-      sm.base[e] = run;
+      sm.total[e] = sm.base[e] = run;
     else
       p.counts[int64_t(blockIdx.x) * p.E + e] = run;
   }
-  __syncthreads();
-  const int routed = ONE ? scan_experts(sm, p.E, p.offsets) : 0;
+  if (ONE && ranks > 1) {
+    // the cluster's counts, and those of the blocks before this one
+    ptx::cluster_sync();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+      int all = 0, before = 0;
+      for (int r = 0; r < ranks; ++r) {
+        const int c = static_cast<int>(
+            ptx::ld_shared_cluster_u32(ptx::mapa_shared(ptx::smem_u32(&sm.total[e]), r)));
+        all += c;
+        before += r < rank ? c : 0;
+      }
+      sm.base[e] = all;
+      for (int w = 0; w < warps; ++w) sm.cnt[w * p.E + e] += static_cast<uint16_t>(before);
+    }
+    // the other blocks have read this one's counts: it may end
+    ptx::cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  const int routed = ONE ? scan_experts(sm, p.E, rank == 0 ? p.offsets : nullptr) : 0;
   walk(sm.ids, t0 * p.k, t1 * p.k, cnt, lane, [&](int i, unsigned e, int before) {
     const int64_t entry = b0 * p.k + i;
     if (ONE && e != 0xffffu) {
       before += sm.base[e];
-      p.rows[before] = i / p.k;  // ONE: b0 = 0
+      p.rows[before] = static_cast<int32_t>(entry) / p.k;
     }
     p.slots[entry] = e == 0xffffu ? -1 : before;
   });
-  if (ONE)
+  if (ONE && rank == 0)
     for (int i = routed + threadIdx.x; i < p.T * p.k; i += blockDim.x) p.rows[i] = -1;
 }
 
@@ -259,7 +287,7 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
   __shared__ RouteSmem sm;
   const int b = blockIdx.x;
   ptx::grid_launch_dependents();
-  int32_t *mine = reinterpret_cast<int32_t *>(sm.ids);  // [E] entries of the blocks before this one
+  int32_t *mine = sm.total;  // [E] entries of the blocks before this one
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
     sm.base[e] = 0;
     mine[e] = 0;
@@ -288,8 +316,8 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
   const int routed = scan_experts(sm, p.E, b == 0 ? p.offsets : nullptr);
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) sm.base[e] += mine[e];
   __syncthreads();
-  const int64_t b0 = int64_t(b) * kBlockTokens, entries = int64_t(p.T) * p.k;
-  const int64_t end = min(b0 + kBlockTokens, int64_t(p.T)) * p.k;
+  const int64_t b0 = int64_t(b) * p.block_tokens, entries = int64_t(p.T) * p.k;
+  const int64_t end = min(b0 + p.block_tokens, int64_t(p.T)) * p.k;
   for (int64_t i = b0 * p.k + threadIdx.x; i < end; i += blockDim.x) {
     const int e = __ldg(p.ids + i);
     if (e >= 0) {
@@ -303,32 +331,43 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
     p.rows[i] = -1;
 }
 
-cudaError_t launch_pdl(void (*kern)(RouteParams), int grid, int threads, const RouteParams &p,
-                       cudaStream_t s) {
+cudaError_t launch_pdl(void (*kern)(RouteParams), int grid, int cluster, int threads,
+                       const RouteParams &p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// Tokens per block of the two-launch form: 32 while that makes at most about one
+// block per SM (4096 tokens: 11.3 us, with 128 a block 12.7 us; 1024: 7.8 and 12.0), then 64 and 128.
+int block_tokens(int64_t T) { return T <= 32 * 152 ? 32 : T <= 64 * 152 ? 64 : kBlockTokens; }
+
 template <int LPT, int EPL>
 cudaError_t launch_route(bool fp32, const RouteParams &p, cudaStream_t s) {
-  // warps: as many as there are groups of tokens, threads and counters for
-  const int groups = (std::min(p.T, kBlockTokens) + 32 / LPT - 1) / (32 / LPT);
-  const int warps = std::min({EPL > 8 ? 16 : 32, kCounters / p.E, groups});
-  if (p.blocks == 1)
+  // warps: as many as there are groups of tokens and counters for
+  auto warps = [&](int tokens) { return std::min({32, kCounters / p.E, (tokens + 32 / LPT - 1) / (32 / LPT)}); };
+  if (p.T <= kOneTokens) {
+    int blocks = 1;  // a power of two
+    while (blocks * kOneBlockTokens < p.T) blocks *= 2;
     return launch_pdl(fp32 ? route_choose_kernel<LPT, EPL, true, true>
-                           : route_choose_kernel<LPT, EPL, false, true>, 1, 32 * warps, p, s);
+                           : route_choose_kernel<LPT, EPL, false, true>,
+                      blocks, blocks, 32 * warps(std::min(p.T, kOneBlockTokens)), p, s);
+  }
   const cudaError_t e = launch_pdl(fp32 ? route_choose_kernel<LPT, EPL, true, false>
                                         : route_choose_kernel<LPT, EPL, false, false>,
-                                   p.blocks, 32 * warps, p, s);
-  return e != cudaSuccess ? e : launch_pdl(route_place_kernel, p.blocks, 1024, p, s);
+                                   p.blocks, 1, 32 * warps(p.block_tokens), p, s);
+  return e != cudaSuccess ? e : launch_pdl(route_place_kernel, p.blocks, 1, 1024, p, s);
 }
 
 }  // namespace
@@ -336,8 +375,9 @@ cudaError_t launch_route(bool fp32, const RouteParams &p, cudaStream_t s) {
 
 extern "C" uint64_t swiglu_moe_route_workspace_size(int64_t T, int64_t E, int64_t k) {
   using namespace swiglu;
-  if (T <= kBlockTokens || E < 1 || k < 1) return 0;
-  return uint64_t((T + kBlockTokens - 1) / kBlockTokens) * E * 4;
+  if (T <= kOneTokens || E < 1 || k < 1) return 0;
+  const int n = block_tokens(T);
+  return uint64_t((T + n - 1) / n) * E * 4;
 }
 
 extern "C" int swiglu_moe_route(const void *logits, int32_t logits_fp32, int32_t renormalize,
@@ -386,7 +426,8 @@ extern "C" int swiglu_moe_route(const void *logits, int32_t logits_fp32, int32_t
   p.T = int32_t(T);
   p.E = int32_t(E);
   p.k = int32_t(k);
-  p.blocks = int32_t((T + kBlockTokens - 1) / kBlockTokens);
+  p.block_tokens = block_tokens(T);
+  p.blocks = int32_t((T + p.block_tokens - 1) / p.block_tokens);
   p.renormalize = renormalize;
   p.scale = scale;
   const bool f = logits_fp32 != 0;
