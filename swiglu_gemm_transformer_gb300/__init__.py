@@ -14,11 +14,14 @@ from __future__ import annotations
 import collections
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libswiglu_gb300.so")
+TORCH_LIB_PATH = os.path.join(_HERE, "_swiglu_torch.so")
 
 OK, ERR_INVALID_ARG, ERR_MISALIGNED, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT = range(6)
 VARIANT_AUTO, VARIANT_1SM_N128, VARIANT_1SM_N64, VARIANT_2SM_N128, VARIANT_1SM_N32 = range(5)
@@ -74,6 +77,7 @@ _CT = {"p": ctypes.c_void_p, "l": ctypes.c_int64, "f": ctypes.c_float, "i": ctyp
 
 _lock = threading.Lock()
 _lib = None
+_torch_mod = None
 
 
 class SwigluError(RuntimeError):
@@ -589,17 +593,26 @@ def swiglu_mlp_noalloc(A, W1, W2, W3, R, Z, *, stream=None):
 MoeRoute = collections.namedtuple("MoeRoute", "ids weights offsets rows slots")
 
 
-def _out_like(t, name, shape, dtype, device):
-    import torch
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, dtype, ndim=len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}")
-    return t
+def _native():
+    """The PyTorch module of the sparse block's calls (csrc/torch_binding.cpp)."""
+    global _torch_mod
+    if _torch_mod is not None:
+        return _torch_mod
+    with _lock:
+        if _torch_mod is None:
+            import torch  # noqa: F401  (the module uses its libraries)
+            if not os.path.exists(TORCH_LIB_PATH):
+                raise RuntimeError(
+                    f"{TORCH_LIB_PATH} is missing: build the library first "
+                    "(python -c 'import __graft_entry__ as g; g.build()')")
+            loader = importlib.machinery.ExtensionFileLoader("_swiglu_torch", TORCH_LIB_PATH)
+            spec = importlib.util.spec_from_file_location("_swiglu_torch", TORCH_LIB_PATH, loader=loader)
+            mod = importlib.util.module_from_spec(spec)
+            loader.exec_module(mod)
+            _torch_mod = mod
+    return _torch_mod
 
 
-@_on_tensor_device
 def swiglu_moe_route(logits, k: int, *, renormalize: bool = False, scale: float = 1.0, ids=None,
                      weights=None, offsets=None, rows=None, slots=None, workspace=None, stream=None):
     """Top-k routing of tokens to experts from their logits [T,E] (bf16 or fp32).
@@ -608,81 +621,28 @@ def swiglu_moe_route(logits, k: int, *, renormalize: bool = False, scale: float 
     slots [T,k]): the chosen experts (-1: none left, every other logit -inf)
     with their softmax weights, and the order of the (token, choice) entries
     by expert that swiglu_fused_grouped reads."""
-    import torch
-    if isinstance(logits, torch.Tensor) and logits.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
-    _need(logits, "logits")
-    T, E = logits.shape
-    k = int(k)
-    if not 1 <= k <= E:
-        raise ValueError(f"k must be in [1, {E}], got {k}")
-    dev, i32 = logits.device, torch.int32
-    ids = _out_like(ids, "ids", (T, k), i32, dev)
-    weights = _out_like(weights, "weights", (T, k), torch.float32, dev)
-    offsets = _out_like(offsets, "offsets", (E + 1,), i32, dev)
-    rows = _out_like(rows, "rows", (T * k,), i32, dev)
-    slots = _out_like(slots, "slots", (T, k), i32, dev)
-    ws, nbytes = _workspace(lib().swiglu_moe_route_workspace_size(T, E, k), dev, workspace)
-    rc = lib().swiglu_moe_route(logits.data_ptr(), int(logits.dtype == torch.float32),
-                                1 if renormalize else 0, float(scale), ids.data_ptr(),
-                                weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
-                                slots.data_ptr(), T, E, k,
-                                ws.data_ptr() if ws is not None else None, nbytes, _stream(stream))
-    _check("swiglu_moe_route", rc)
-    return MoeRoute(ids, weights, offsets, rows, slots)
+    return MoeRoute(*_native().moe_route(logits, k, renormalize, scale, ids, weights, offsets, rows, slots,
+                                         workspace, stream))
 
 
-def _grouped(A, Ws, names, offsets, rows, Y):
-    import torch
-    bf = torch.bfloat16
-    _need(A, "A", bf)
-    for W, n in zip(Ws, names):
-        _need(W, n, bf, ndim=3)
-        if W.shape != Ws[0].shape:
-            raise ValueError("W1 and W2 must match in shape")
-    T, K = A.shape
-    E, Kw, N = Ws[0].shape
-    if Kw != K:
-        raise ValueError(f"shape mismatch: A {tuple(A.shape)}, {names[0]} {tuple(Ws[0].shape)}")
-    _need(offsets, "offsets", torch.int32, ndim=1)
-    if offsets.numel() != E + 1:
-        raise ValueError(f"offsets must have {E + 1} elements")
-    if rows is not None:
-        _need(rows, "rows", torch.int32, ndim=1)
-    P = T if rows is None else rows.numel()
-    Y = _out_like(Y, "the output", (P, N), bf, A.device)
-    return Y, (T, P, E, N, K)
-
-
-@_on_tensor_device
 def swiglu_fused_grouped(A, W1, W2, offsets, rows=None, Y=None, *, stream=None):
     """Y[p] = SiLU(a @ W1[e]) * (a @ W2[e]), a = A[rows[p]] (A[p] without rows),
     for the places p in [offsets[e], offsets[e+1]) of expert e; W1/W2 [E,K,N].
 
     Places that belong to no expert are left as they are (uninitialised where
     Y is allocated here)."""
-    Y, dims = _grouped(A, (W1, W2), ("W1", "W2"), offsets, rows, Y)
-    rc = lib().swiglu_fused_grouped(A.data_ptr(), W1.data_ptr(), W2.data_ptr(), offsets.data_ptr(),
-                                    rows.data_ptr() if rows is not None else None, Y.data_ptr(),
-                                    *dims, _stream(stream))
-    _check("swiglu_fused_grouped", rc)
-    return Y
+    if W2 is None:
+        raise TypeError("W2 must be a torch.Tensor")
+    return _native().grouped(A, W1, W2, offsets, rows, Y, stream)
 
 
-@_on_tensor_device
 def swiglu_linear_grouped(X, W, offsets, rows=None, Z=None, *, stream=None):
     """Z[p] = x @ W[e], x = X[rows[p]] (X[p] without rows), for the places p in
     [offsets[e], offsets[e+1]) of expert e; W [E,K,N].  Places that belong to no
     expert are left as they are."""
-    Z, dims = _grouped(X, (W,), ("W",), offsets, rows, Z)
-    rc = lib().swiglu_linear_grouped(X.data_ptr(), W.data_ptr(), offsets.data_ptr(),
-                                     rows.data_ptr() if rows is not None else None, Z.data_ptr(),
-                                     *dims, _stream(stream))
-    _check("swiglu_linear_grouped", rc)
-    return Z
+    return _native().grouped(X, W, None, offsets, rows, Z, stream)
 
 
-@_on_tensor_device
 def swiglu_residual_norm(Z, R, *, slots=None, weights=None, post_norm: bool = True, gamma_post=None,
                          gate=None, residual_scale: float = 1.0, gamma_pre=None, eps: float = 1e-6,
                          Rout=None, H=None, stream=None):
@@ -696,53 +656,8 @@ def swiglu_residual_norm(Z, R, *, slots=None, weights=None, post_norm: bool = Tr
     bf16 [D] or [T,D] (rows may be strided, or broadcast with stride 0);
     gammas bf16 [D] or None for ones; post_norm=False leaves z as it is.
     Rout may be R."""
-    import torch
-    bf = torch.bfloat16
-    _need(Z, "Z", bf)
-    if isinstance(R, torch.Tensor) and R.dtype not in (bf, torch.float32):
-        raise TypeError(f"R must be bfloat16 or float32, got {R.dtype}")
-    _need(R, "R")
-    T, D = R.shape
-    P = Z.shape[0]
-    k = 0
-    if Z.shape[1] != D:
-        raise ValueError(f"shape mismatch: Z {tuple(Z.shape)}, R {tuple(R.shape)}")
-    if (slots is None) != (weights is None):
-        raise ValueError("slots and weights go together")
-    if slots is None:
-        if P != T:
-            raise ValueError("without slots, Z must be [T, D]")
-    else:
-        _need(slots, "slots", torch.int32), _need(weights, "weights", torch.float32)
-        k = slots.shape[1]
-        if tuple(slots.shape) != (T, k) or tuple(weights.shape) != (T, k):
-            raise ValueError("slots and weights must be [T, k]")
-    for g, n in ((gamma_post, "gamma_post"), (gamma_pre, "gamma_pre")):
-        if g is not None:
-            _need(g, n, bf, ndim=1)
-            if g.numel() != D:
-                raise ValueError(f"{n} must have {D} elements")
-    if gamma_post is not None and not post_norm:
-        raise ValueError("gamma_post without post_norm")
-    stride = 0
-    if gate is not None:
-        if not isinstance(gate, torch.Tensor) or not gate.is_cuda or gate.dtype != bf:
-            raise TypeError("gate must be a bfloat16 CUDA tensor")
-        if tuple(gate.shape) not in ((D,), (T, D)) or (D > 1 and gate.stride(-1) != 1):
-            raise ValueError("gate must be [D] or [T, D] with contiguous rows")
-        stride = gate.stride(0) if gate.dim() == 2 and T > 1 else 0
-    Rout = _out_like(Rout, "Rout", (T, D), R.dtype, R.device)
-    H = _out_like(H, "H", (T, D), bf, R.device)
-
-    def ptr(t):
-        return t.data_ptr() if t is not None else None
-    rc = lib().swiglu_residual_norm(Z.data_ptr(), ptr(slots), ptr(weights), R.data_ptr(),
-                                    int(R.dtype == torch.float32), 1 if post_norm else 0,
-                                    ptr(gamma_post), ptr(gate), stride, float(residual_scale),
-                                    ptr(gamma_pre), float(eps), Rout.data_ptr(), H.data_ptr(),
-                                    T, P, k, D, _stream(stream))
-    _check("swiglu_residual_norm", rc)
-    return Rout, H
+    return _native().residual_norm(Z, R, slots, weights, post_norm, gamma_post, gate, residual_scale,
+                                   gamma_pre, eps, Rout, H, stream)
 
 
 def swiglu_select_variant(M: int, N: int, K: int, interleaved: bool = False) -> int:
