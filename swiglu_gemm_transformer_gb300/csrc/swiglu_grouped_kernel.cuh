@@ -34,7 +34,7 @@
 //     (gate/up with rows at 64 experts x 1024 rows, K = 2048, N = 1024: 1118 us;
 //     rows copied with cp.async instead 374 us; eight warps like this 326 us, four
 //     366 us, sixteen 320 us but a third fewer registers a thread);
-//   * accumulators are double-buffered in TMEM (256 columns each).
+//   * accumulators are double-buffered in TMEM (NT columns each).
 // Unit schedule: every CTA reads `offsets`, counts the row tiles of each
 // expert, and the pairs take the units (expert, row tile, column tile) in
 // turn; the rows of an expert are split evenly over its row tiles, in steps
@@ -102,9 +102,9 @@ struct GroupedCfg {
   static constexpr int UNIT_READERS = EPI_WARPS + ROW_WARPS + 2;
   static_assert(NT / 8 % ROW_WARPS == 0, "gathers split evenly");
   static constexpr int MMA_M = 256;
-  static constexpr int ACC_COLS = 256; // TMEM columns of one accumulator buffer
+  static constexpr int ACC_COLS = NT;  // TMEM columns of one accumulator buffer
   static constexpr int GROUP = 8;
-  static_assert(NT % 32 == 0 && NT <= 256, "rows of a tile");
+  static_assert(NT == 128 || NT == 256, "rows of a tile");
   static_assert(STAGES >= 4, "pipeline depth");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };

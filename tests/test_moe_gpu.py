@@ -104,7 +104,8 @@ def check_route(sg, logits, k, renorm=False, scale=1.0, **kw):
 @pytest.mark.parametrize("fp32", [False, True])
 @pytest.mark.parametrize("shape", [(1, 64, 8), (1, 1, 1), (3, 4, 4), (16, 8, 2), (17, 33, 3), (127, 60, 6), (128, 64, 8),
                                    (129, 64, 8), (1000, 128, 4), (300, 256, 8), (257, 500, 7), (130, 1024, 32),
-                                   (77, 1024, 32), (2049, 16, 1)], ids=lambda s: "x".join(map(str, s)))
+                                   (77, 1024, 32), (2049, 16, 1), (33, 64, 8), (256, 64, 8), (257, 8, 8), (4865, 32, 2),
+                                   (9729, 12, 3), (40, 600, 9)], ids=lambda s: "x".join(map(str, s)))
 def test_route(sg, shape, fp32):
     T, E, k = shape
     x = torch.randn(T, E, generator=_gen("route", *shape)) * 2
@@ -120,7 +121,7 @@ def test_route_ties_go_to_the_lowest_expert(sg, T):
     check_route(sg, x, 8, renorm=True)
 
 
-@pytest.mark.parametrize("T", [9, 400])
+@pytest.mark.parametrize("T", [9, 400, 5000])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_masked(sg, T, renorm):
     x = torch.randn(T, 40, generator=_gen("mask", T))
@@ -253,7 +254,7 @@ FORMS = pytest.mark.parametrize("fused", [True, False], ids=["fused", "linear"])
 @FORMS
 @pytest.mark.parametrize("gather", [True, False], ids=["rows", "dense"])
 @pytest.mark.parametrize("sizes", [[1], [5, 0, 3], [0, 0, 1, 0], [31, 32, 33], [64, 65, 1, 0, 63], [255, 256, 257, 0, 2],
-                                   [700, 0, 0, 1, 513]], ids=lambda s: "-".join(map(str, s)))
+                                   [700, 0, 0, 1, 513], [127, 128, 129, 97]], ids=lambda s: "-".join(map(str, s)))
 @pytest.mark.parametrize("NK", [(8, 8), (72, 136), (264, 200), (512, 64)], ids=lambda s: "x".join(map(str, s)))
 def test_grouped(sg, fused, gather, sizes, NK):
     check_grouped(sg, fused, sizes, *NK, T=53 if gather else None)
@@ -471,6 +472,25 @@ def test_norm_rows_and_joins(sg, T, k):
     check_norm(sg, T, 512, k=k, r32=bool(k & 1), gate="rows")
 
 
+# more rows than the direct kernel takes: the ring in shared memory
+@pytest.mark.parametrize("r32", [False, True], ids=["r16", "r32"])
+@pytest.mark.parametrize("D,k", [(8, 0), (256, 1), (512, 0), (520, 3), (1024, 8), (2048, 8), (2056, 2), (4096, 0), (8192, 2),
+                                 (8200, 0), (16384, 0), (264, 30), (264, 33)])
+def test_norm_many_rows(sg, D, k, r32):
+    def edit(Z, R, slots, weights):
+        if slots is not None:
+            slots[5] = -1
+            slots[7, 0] = Z.shape[0] + 3
+    check_norm(sg, 701, D, k=k, r32=r32, gate="rows" if D % 16 == 0 else "vector", edit=edit)
+
+
+@pytest.mark.parametrize("gate", [None, "vector", "rows", "strided", "expanded"])
+@pytest.mark.parametrize("post", [True, False])
+def test_norm_many_rows_forms(sg, gate, post):
+    check_norm(sg, 1300, 904, k=2, gate=gate, post=post, gammas=False)
+    check_norm(sg, 1300, 904, gate=gate, post=post, r32=True, inplace=True)
+
+
 @pytest.mark.parametrize("gate", [None, "vector", "rows", "strided", "expanded"])
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("gammas", [True, False])
@@ -512,14 +532,16 @@ def test_norm_nan_stays_in_its_row(sg):
     assert torch.isnan(H[2]).all() and not torch.isnan(H[[0, 1, 3]]).any() and not torch.isnan(Ro[[0, 1, 3]]).any()
 
 
-def test_norm_without_the_second_norm(sg):
+@pytest.mark.parametrize("T", [9, 2000])
+@pytest.mark.parametrize("post", [1, 0])
+def test_norm_without_the_second_norm(sg, T, post):
     """H = NULL: only R' is made (the last block of a model)."""
-    Z = torch.randn(9, 128, generator=_gen("h0")).to(BF).to(DEV)
-    R = torch.randn(9, 128, generator=_gen("h1")).to(BF).to(DEV)
-    want, _ = sg.swiglu_residual_norm(Z, R)
+    Z = torch.randn(T, 1024, generator=_gen("h0")).to(BF).to(DEV)
+    R = torch.randn(T, 1024, generator=_gen("h1")).to(BF).to(DEV)
+    want, _ = sg.swiglu_residual_norm(Z, R, post_norm=bool(post))
     out = torch.empty_like(R)
-    rc = sg.lib().swiglu_residual_norm(Z.data_ptr(), None, None, R.data_ptr(), 0, 1, None, None, 0, 1.0, None, 1e-6,
-                                       out.data_ptr(), None, 9, 9, 0, 128, torch.cuda.current_stream().cuda_stream)
+    rc = sg.lib().swiglu_residual_norm(Z.data_ptr(), None, None, R.data_ptr(), 0, post, None, None, 0, 1.0, None, 1e-6,
+                                       out.data_ptr(), None, T, T, 0, 1024, torch.cuda.current_stream().cuda_stream)
     assert rc == sg.OK
     _status(sg)
     assert torch.equal(out, want)
