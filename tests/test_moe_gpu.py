@@ -637,3 +637,72 @@ def test_block_in_a_graph_matches_64_bits(sg):
                                   None, 1e-6)
         assert ((state["ro"].double().cpu() - rr).abs() <= dr + 2.0**-8 * rr.abs() + 1e-38).all()
         assert ((state["h"].double().cpu() - hh).abs() <= dh + 2.0**-8 * hh.abs() + 1e-38).all()
+
+
+def test_example_block(sg):
+    """The example's blocks against their plain form, and single tokens against the prompt.
+
+    A block rounds Y and Z to BF16 (2^-9 each) and may round an element the
+    other way than the plain form (2^-8 of it); as a norm over many elements
+    such flips stay far below 2^-8.  Single tokens run the products in other
+    tiles, with the sums in the same order over K: equal but for the router's
+    logits, whose product may sum in another order and flip a rounding."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    worst, off = mod.main(hidden=264, inner=136, experts=8, top_k=2, layers=2, prompt=81)
+    assert worst < 2.0**-8 and off < 2.0**-6
+
+
+# ---- sizes past 32 bits ---------------------------------------------------------------
+
+
+def test_grouped_output_past_32_bits(sg):
+    P, N, K = 70016, 32768, 64          # 2.3e9 outputs
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    X = torch.randn(P, K, generator=gen, device=DEV).to(BF)
+    W = (torch.randn(2, K, N, generator=gen, device=DEV) / 8).to(BF)
+    off = torch.tensor([0, 40000, P], dtype=torch.int32, device=DEV)
+    Z = sg.swiglu_linear_grouped(X, W, off)
+    _status(sg)
+    for a, b, e in ((0, 3, 0), (39998, 40000, 0), (40000, 40002, 1), (65530, 65545, 1), (P - 3, P, 1)):
+        ref, tol = grouped_ref(X[a:b].cpu(), [W[e:e + 1].cpu()], [0, b - a], None)
+        assert ((Z[a:b].double().cpu() - ref).abs() <= tol).all(), (a, b)
+
+
+def test_grouped_weights_past_32_bits(sg):
+    E, K, N = 40, 2048, 28672           # 2.3e9 weights a matrix
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    W = torch.empty(E, K, N, dtype=BF, device=DEV)
+    for e in range(E):
+        W[e] = torch.randn(K, N, generator=gen, device=DEV) / 45
+    X = torch.randn(6, K, generator=gen, device=DEV).to(BF)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[36:] = 2
+    off[38:] = 5
+    off[40:] = 6
+    Z = sg.swiglu_linear_grouped(X, W, off.to(DEV))
+    _status(sg)
+    for a, b, e in ((0, 2, 35), (2, 5, 37), (5, 6, 39)):
+        ref, tol = grouped_ref(X[a:b].cpu(), [W[e:e + 1].cpu()], [0, b - a], None)
+        assert ((Z[a:b].double().cpu() - ref).abs() <= tol).all(), e
+
+
+def test_norm_past_32_bits(sg):
+    T, D = 270000, 8192                 # 2.2e9 elements
+    R = torch.zeros(T, D, dtype=BF, device=DEV)
+    Z = torch.zeros(T, D, dtype=BF, device=DEV)
+    at = [0, 1, 131071, 262143, 262144, T - 1]
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    for t in at:
+        R[t] = torch.randn(D, generator=gen, device=DEV)
+        Z[t] = torch.randn(D, generator=gen, device=DEV)
+    want = sg.swiglu_residual_norm(Z[at].contiguous(), R[at].contiguous())
+    Ro, H = sg.swiglu_residual_norm(Z, R, Rout=R)
+    _status(sg)
+    assert torch.equal(Ro[at], want[0])
+    assert ((H[at].float() - want[1].float()).abs() <= 2.0**-7 * want[1].float().abs()).all()
+    assert int((H != 0).any(1).sum()) == len(at)
