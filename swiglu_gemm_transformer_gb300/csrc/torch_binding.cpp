@@ -211,7 +211,8 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
     Tensor Y = c.output(a[5], "the output", ScalarType::BFloat16, {P, N});
     void *s = c.stream(a[6]);
-    const int32_t *r = rows ? ptr<int32_t>(*rows) : nullptr;
+    // (an empty tensor has no address: any other stands for "rows are given")
+    const int32_t *r = !rows ? nullptr : P > 0 ? ptr<int32_t>(*rows) : ptr<int32_t>(offsets);
     c.check(unlocked([&] {
       return fused ? swiglu_fused_grouped(A.data_ptr(), W1.data_ptr(), W2.data_ptr(), ptr<int32_t>(offsets),
                                           r, Y.data_ptr(), T, P, E, N, K, s)
@@ -273,7 +274,8 @@ PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Tensor Rout = c.output(a[10], "Rout", R.scalar_type(), {T, D});
     Tensor H = c.output(a[11], "H", bf, {T, D});
     void *s = c.stream(a[12]);
-    auto at = [](const Tensor *t) { return t ? t->data_ptr() : nullptr; };
+    // (slots without columns have no address: any other stands for "slots are given")
+    auto at = [&](const Tensor *t) { return !t ? nullptr : t->numel() > 0 ? t->data_ptr() : R.data_ptr(); };
     c.check(unlocked([&] {
       return swiglu_residual_norm(Z.data_ptr(), static_cast<const int32_t *>(at(slots)),
                                   static_cast<const float *>(at(weights)), R.data_ptr(),

@@ -547,6 +547,24 @@ def test_norm_without_the_second_norm(sg, T, post):
     assert torch.equal(out, want)
 
 
+def test_no_rows_and_no_choices(sg):
+    # rows that name nothing at all, of a matrix with rows
+    A = torch.ones(5, 16, dtype=BF, device=DEV)
+    W = torch.ones(2, 16, 24, dtype=BF, device=DEV)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    assert sg.swiglu_linear_grouped(A, W, off, none).shape == (0, 24)
+    assert sg.swiglu_fused_grouped(A, W, W, off, none).shape == (0, 24)
+    # k = 0: nothing joins, R' = s R
+    for T in (3, 900):
+        R = torch.randn(T, 64, generator=_gen("k0")).to(BF).to(DEV)
+        slots = torch.zeros(T, 0, dtype=torch.int32, device=DEV)
+        Ro, _ = sg.swiglu_residual_norm(A.new_ones(7, 64), R, slots=slots, weights=torch.zeros(T, 0, device=DEV),
+                                        residual_scale=0.5)
+        _status(sg)
+        assert torch.equal(Ro, (0.5 * R.float()).to(BF))
+
+
 def test_norm_empty(sg):
     Z = torch.empty(0, 64, dtype=BF, device=DEV)
     Ro, H = sg.swiglu_residual_norm(Z, Z)
