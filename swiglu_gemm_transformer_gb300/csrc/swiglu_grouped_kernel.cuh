@@ -98,8 +98,6 @@ struct GroupedCfg {
   static constexpr int ROW_WARPS = 8;
   static constexpr int UNIT_WARP = ROW_WARP + ROW_WARPS;
   static constexpr int THREADS = 32 * (UNIT_WARP + 1);
-  // warps that read the units: epilogue, row loaders, producer, MMA
-  static constexpr int UNIT_READERS = EPI_WARPS + ROW_WARPS + 2;
   static_assert(NT / 8 % ROW_WARPS == 0, "gathers split evenly");
   static constexpr int MMA_M = 256;
   static constexpr int ACC_COLS = NT;  // TMEM columns of one accumulator buffer
@@ -198,7 +196,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const bool gather = p.rows != nullptr;
   if (warp == C::PRODUCER_WARP && lane == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(full_bar(s), gather ? 1 + 2 * C::ROW_WARPS : 1);
       ptx::mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -208,8 +206,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     ptx::mbar_init(drain_bar, 1);
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(unitf_bar + 8u * b, 1);
-      // (the odd CTA issues no MMAs: its MMA warp reads no units)
-      ptx::mbar_init(unite_bar + 8u * b, C::UNIT_READERS - (rank == 0 ? 0 : 1));
+      // readers of the units: epilogue warps, warps that copy rows, the weights'
+      // thread and, in the leader, the MMA's
+      ptx::mbar_init(unite_bar + 8u * b,
+                     C::EPI_WARPS + (gather ? C::ROW_WARPS : 1) + 1 + (rank == 0 ? 1 : 0));
     }
     *abort_flag = 0;
     ptx::fence_barrier_init();
@@ -352,8 +352,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __syncwarp();
   } else if (warp >= C::ROW_WARP) {
     // ------------------------------------------------------------ rows (both CTAs)
-    if (ptx::elect_one()) {
-      const int w = warp - C::ROW_WARP;
+    // Dense rows are copied by the first of these warps alone, gathered rows by
+    // all of them.  A tile of a few gathered rows leaves some without a copy,
+    // and a thread that only waited for the stages could miss a phase; so
+    // every thread that gathers also arrives on the stage's "full" barrier.
+    const int w = warp - C::ROW_WARP;
+    if ((gather || w == 0) && ptx::elect_one()) {
       constexpr int PER = C::NT / 8 / C::ROW_WARPS;  // gathers of a warp per stage
       uint32_t stage = 0, phase = 0;
       bool ok = true;
@@ -383,6 +387,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint32_t sa = base + stage * C::STAGE_BYTES + C::W_BYTES;
           const uint32_t fb = ptx::mapa_shared(full_bar(stage), 0);
           if (gather) {
+            ptx::mbar_arrive_cluster_relaxed(fb);
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
               const int g = w + j * C::ROW_WARPS;
@@ -391,9 +396,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                       idx[j][2], idx[j][3]);
             }
           } else if (half == C::NT / 2) {
-            if (w == 0) ptx::tma_load_2d_pair(sa, &tmA2, fb, kb * C::BK, row0);
+            ptx::tma_load_2d_pair(sa, &tmA2, fb, kb * C::BK, row0);
           } else {
-            for (int i = 32 * w; i < half; i += 32 * C::ROW_WARPS)
+            for (int i = 0; i < half; i += 32)
               ptx::tma_load_2d_pair(sa + i * 128, &tmA, fb, kb * C::BK, row0 + i);
           }
           if (++stage == C::STAGES) {
