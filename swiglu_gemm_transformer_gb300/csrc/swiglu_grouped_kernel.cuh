@@ -126,6 +126,17 @@ __device__ __forceinline__ static bool bar_all(int id, int threads, bool ok) {
 struct __align__(16) GroupedUnit {
   int row0, end, e, nb;
   __device__ int n() const { return (end - row0 + 31) & ~31; }  // MMA N
+  // Rows of the CTA `rank`'s half that belong to the tile.
+  __device__ int rows_of(int rank) const {
+    const int half = n() >> 1;
+    return min(max(end - row0 - rank * half, 0), half);
+  }
+  // Bytes of a CTA's copies of them per stage: whole groups of four gathered
+  // rows, whole boxes of dense ones.
+  __device__ uint32_t row_bytes(int rank, bool gather) const {
+    const int grain = gather ? 4 : 32;
+    return ((rows_of(rank) + grain - 1) & ~(grain - 1)) * 128;
+  }
 };
 
 // The units of one role, in order.  Every lane of the role's warp calls
@@ -196,7 +207,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const bool gather = p.rows != nullptr;
   if (warp == C::PRODUCER_WARP && lane == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(full_bar(s), gather ? 1 + 2 * C::ROW_WARPS : 1);
+      ptx::mbar_init(full_bar(s), 1 + 2 * (gather ? C::ROW_WARPS : 1));
       ptx::mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -315,8 +326,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       GroupedUnit un;
       while (ok && units.next(un, ok)) {
         const int col0 = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS;
-        const int half = un.n() >> 1;
-        const uint32_t row_bytes = (gather ? half : (half + 31) & ~31) * C::BK * 2;
+        const uint32_t row_bytes = un.row_bytes(0, gather) + un.row_bytes(1, gather);
         for (int kb = 0; kb < p.num_k_blk; ++kb) {
           if (!wait_bar(empty_bar(stage), phase ^ 1u, p.timeout_ns, abort_flag, p.err,
                         WAIT_PRODUCER_EMPTY)) {
@@ -326,7 +336,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint32_t sw = base + stage * C::STAGE_BYTES;
           const uint32_t fb = ptx::mapa_shared(full_bar(stage), 0);
           // the bytes of both CTAs, weights and rows
-          if (rank == 0) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * (C::W_BYTES + row_bytes));
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * C::W_BYTES + row_bytes);
           ptx::tma_load_3d_pair(sw, &tmW1, fb, col0, kb * C::BK, un.e);
           if (C::FUSED)
             ptx::tma_load_3d_pair(sw + C::ATOM_BYTES, &tmW2, fb, col0, kb * C::BK, un.e);
@@ -353,9 +363,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else if (warp >= C::ROW_WARP) {
     // ------------------------------------------------------------ rows (both CTAs)
     // Dense rows are copied by the first of these warps alone, gathered rows by
-    // all of them.  A tile of a few gathered rows leaves some without a copy,
-    // and a thread that only waited for the stages could miss a phase; so
-    // every thread that gathers also arrives on the stage's "full" barrier.
+    // all of them; the rows of the MMA's N past the tile's end are not copied
+    // (their products, of whatever the stage held before, are not stored).  A
+    // tile of few rows leaves some threads without a copy, and a thread that
+    // only waited for the stages could miss a phase; so each of them also
+    // arrives on the stage's "full" barrier.
     const int w = warp - C::ROW_WARP;
     if ((gather || w == 0) && ptx::elect_one()) {
       constexpr int PER = C::NT / 8 / C::ROW_WARPS;  // gathers of a warp per stage
@@ -364,10 +376,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       GroupedUnits<true> units(ring, unitf_bar, unite_bar, p, abort_flag);
       GroupedUnit un;
       while (ok && units.next(un, ok)) {
-        const int half = un.n() >> 1;
-        const int row0 = un.row0 + static_cast<int>(rank) * half;
-        // Rows past the tile's end: gathered, its last row again; dense, other
-        // tiles' rows or zeros.  Their products are not stored.
+        const int row0 = un.row0 + static_cast<int>(rank) * (un.n() >> 1);
+        const int rows = un.rows_of(rank);
+        // the last group of four repeats the tile's last row
         int idx[PER][4];
         if (gather) {
 #pragma unroll
@@ -386,19 +397,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           const uint32_t sa = base + stage * C::STAGE_BYTES + C::W_BYTES;
           const uint32_t fb = ptx::mapa_shared(full_bar(stage), 0);
+          ptx::mbar_arrive_cluster_relaxed(fb);
           if (gather) {
-            ptx::mbar_arrive_cluster_relaxed(fb);
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
               const int g = w + j * C::ROW_WARPS;
-              if (4 * g < half)
+              if (4 * g < rows)
                 ptx::tma_gather4_pair(sa + g * 512, &tmA, fb, kb * C::BK, idx[j][0], idx[j][1],
                                       idx[j][2], idx[j][3]);
             }
-          } else if (half == C::NT / 2) {
+          } else if (rows > C::NT / 2 - 32) {
             ptx::tma_load_2d_pair(sa, &tmA2, fb, kb * C::BK, row0);
           } else {
-            for (int i = 0; i < half; i += 32)
+            for (int i = 0; i < rows; i += 32)
               ptx::tma_load_2d_pair(sa + i * 128, &tmA, fb, kb * C::BK, row0 + i);
           }
           if (++stage == C::STAGES) {
