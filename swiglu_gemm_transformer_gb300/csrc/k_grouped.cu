@@ -39,20 +39,25 @@ cudaError_t launch_grouped(GroupedLaunch &gl) {
   cfg.stream = gl.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;  // the occupancy query takes the cluster shape only
+  if (C::SPLIT) attr[0].val.clusterDim.x = 2 * gl.p.pairs;
   if (once.needed(gl.device, gl.ctx_gen)) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(2 * 64, 1, 1);
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-    if (e != cudaSuccess) return e;
-    if (n < 1) return cudaErrorInvalidConfiguration;
-    max_clusters[gl.device & 63] = n;
+    if (!C::SPLIT) {
+      cfg.gridDim = dim3(2 * 64, 1, 1);
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorInvalidConfiguration;
+      max_clusters[gl.device & 63] = n;
+    }
     once.done(gl.device, gl.ctx_gen);
   }
-  const int64_t clusters = std::min<int64_t>(gl.units, max_clusters[gl.device & 63]);
-  cfg.gridDim = dim3(unsigned(2 * clusters), 1, 1);
+  // SPLIT: a cluster per unit; else a persistent grid of pairs
+  const int64_t clusters =
+      C::SPLIT ? gl.units : std::min<int64_t>(gl.units, max_clusters[gl.device & 63]);
+  cfg.gridDim = dim3(unsigned(clusters) * attr[0].val.clusterDim.x, 1, 1);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, gl.a, gl.a2, gl.w1, gl.w2, gl.p);
 }
@@ -96,6 +101,20 @@ int run_grouped(const void *A, const void *W1, const void *W2, bool fused, const
     return cudaMemsetAsync(Y, 0, y_bytes, gl.stream) == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
   if (cudaGetDevice(&gl.device) != cudaSuccess) return SWIGLU_ERR_CUDA;
 
+  p.num_k_blk = int32_t(ceil_div(K, 64));
+  p.num_n_blk = int32_t(ceil_div(N, fused ? 128 : 256));
+  auto units = [&](int rows_per_tile) {
+    return (std::min(E, P) + P / rows_per_tile) * p.num_n_blk;
+  };
+  // Few units and enough K to share: several pairs to a unit.  A cluster of four
+  // or eight CTAs fits the GPU 36 or 15 times.  One token, in a graph: down of 2
+  // of 8 experts of the 0.5B shape (4864 x 896) 17.0 -> 8.9 us, of the 7B shape
+  // (18944 x 3584) 56 -> 43, gate/up of 2 of 64 experts (2048 x 1024) 11.1 -> 9.8;
+  // at 17 K steps as fast as without.  With 100 rows an expert the sums to add
+  // cost more: 16 K steps 9.0 us without and 11.1 with.
+  const int64_t few = units(128);
+  const int least = P > 32 * E ? 32 : 16;  // K steps
+  const int pairs = few > 36 || p.num_k_blk < least ? 1 : few > 15 ? 2 : 4;
   // Tiles of up to 256 rows read each weight once per 256 rows; tiles of up to
   // 128 rows leave shared memory for two more stages, which is what counts
   // where a group has few rows and the weights' stream is the cost.  Gate/up of
@@ -103,7 +122,7 @@ int run_grouped(const void *A, const void *W1, const void *W2, bool fused, const
   // of 128 and 88.1 in tiles of 256, 128 rows 90.9 and 93.4, 192 rows 115 and
   // 99; ragged groups of 127 rows on average 33 and 32 (8 experts, K = 896,
   // N = 4864).
-  const int nt = P > 96 * E ? 256 : 128;
+  const int nt = pairs == 1 && P > 96 * E ? 256 : 128;
   const uint64_t adim[2] = {uint64_t(K), uint64_t(T)}, astr[1] = {uint64_t(K) * 2};
   const uint32_t abox[2] = {64, rows ? 1u : 32u}, abox2[2] = {64, uint32_t(nt / 2)};
   const uint64_t wdim[3] = {uint64_t(N), uint64_t(K), uint64_t(E)};
@@ -121,11 +140,14 @@ int run_grouped(const void *A, const void *W1, const void *W2, bool fused, const
   p.P = int32_t(P);
   p.E = int32_t(E);
   p.N = int32_t(N);
-  p.num_k_blk = int32_t(ceil_div(K, 64));
-  p.num_n_blk = int32_t(ceil_div(N, fused ? 128 : 256));
-  gl.units = (std::min(E, P) + P / nt) * p.num_n_blk;
+  gl.units = units(nt);
+  p.pairs = pairs;
+  p.kb_per_pair = int32_t(ceil_div(p.num_k_blk, pairs));
   cudaError_t e;
-  if (fused)
+  if (pairs > 1)
+    e = fused ? launch_grouped<GroupedCfg<true, 128, true>>(gl)
+              : launch_grouped<GroupedCfg<false, 128, true>>(gl);
+  else if (fused)
     e = nt == 256 ? launch_grouped<GroupedCfg<true, 256>>(gl) : launch_grouped<GroupedCfg<true, 128>>(gl);
   else
     e = nt == 256 ? launch_grouped<GroupedCfg<false, 256>>(gl) : launch_grouped<GroupedCfg<false, 128>>(gl);

@@ -43,6 +43,11 @@
 // 32 at a time (one per lane), and hands them to the other roles through a
 // ring in shared memory: found by each role for itself, a unit cost about
 // 2 us between two main loops.
+// SPLIT: for calls of so few units that most SMs would stand idle.  A K step of
+// 64 takes a pair about 0.16 us however few rows it has (the MMA's time for 256
+// weight rows), so a cluster of several pairs shares one unit: each takes a
+// slice of K, and the first pair adds the others' FP32 sums, in order, from its
+// shared memory (the ring, idle by then).  At most one unit per cluster.
 // Every wait is bounded as in the other kernels.
 #pragma once
 
@@ -63,14 +68,17 @@ struct GroupedParams {
   __nv_bfloat16 *Y;        // [P, N]
   int32_t T, P, E, N;      // rows of A, rows of Y, experts, output columns
   int32_t num_k_blk, num_n_blk;
+  int32_t pairs, kb_per_pair;  // SPLIT: pairs of a cluster, K steps of each
   uint64_t timeout_ns;
   uint32_t *err;
 };
 
 // NT: most rows of one tile (MMA N).
-template <bool FUSED_, int NT_>
+template <bool FUSED_, int NT_, bool SPLIT_ = false>
 struct GroupedCfg {
   static constexpr bool FUSED = FUSED_;
+  static constexpr bool SPLIT = SPLIT_;
+  static constexpr int MAX_PAIRS = 4;            // SPLIT: pairs of a cluster
   static constexpr int NT = NT_;
   static constexpr int BK = 64;
   static constexpr int COLS = FUSED ? 64 : 128;  // output columns per CTA
@@ -103,6 +111,7 @@ struct GroupedCfg {
   static constexpr int ACC_COLS = NT;  // TMEM columns of one accumulator buffer
   static constexpr int GROUP = 8;
   static_assert(NT == 128 || NT == 256, "rows of a tile");
+  static_assert(!SPLIT || (MAX_PAIRS - 1) * NT * 128 * 4 <= STAGES * STAGE_BYTES, "sums fit the ring");
   static_assert(STAGES >= 4, "pipeline depth");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -200,7 +209,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = ptx::cluster_ctarank();  // 0 = the pair's leader
+  const uint32_t crank = ptx::cluster_ctarank();
+  const uint32_t lead = C::SPLIT ? crank & ~1u : 0u;  // cluster rank of this pair's leader
+  const uint32_t rank = crank - lead;                 // 0 = the pair's leader
+  const uint16_t both = static_cast<uint16_t>(0x3u << lead);  // the pair's CTAs, as a mask
+  const int kb0 = C::SPLIT ? static_cast<int>(lead >> 1) * p.kb_per_pair : 0;
+  const int kb1 = C::SPLIT ? min(p.num_k_blk, kb0 + p.kb_per_pair) : p.num_k_blk;
   const int cid = static_cast<int>(ptx::cluster_id_x());
   const int ncl = static_cast<int>(ptx::num_clusters_x());
 
@@ -241,6 +255,96 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   ptx::grid_dependency_wait();
 
   GroupedUnit *ring = reinterpret_cast<GroupedUnit *>(smem + C::UNIT_OFF);
+  GroupedUnit mine = {-1, -1, 0, 0};  // epilogue: the tile at hand
+  bool have = false;                  // SPLIT: its sums are complete
+
+  // ---- epilogue (warps 0-7, both CTAs) ----
+  // Warp q (mod 4) reads TMEM lanes [32q, 32q + 32), the tile's rows in the
+  // columns.  Linear: lane i is output column 32q + i; FUSED: warps q = 0, 1
+  // hold the gate and q = 2, 3 the up values of output columns 32 (q % 2) + i.
+  // Per 32 rows (FUSED) or 16 rows (linear) of the tile; warps 0-3 take the
+  // even chunks, warps 4-7 the odd ones.
+  const int q = warp & 3, h = (warp >> 2) & 1;
+  constexpr int CH = C::FUSED ? 32 : 16;
+  const bool gate = q < 2;
+  const int wcol = C::FUSED ? 32 * (q & 1) : 32 * q;
+  uint8_t *stg = smem + C::STG_OFF + warp * C::STG_BYTES;
+  // FUSED: warps q and q ^ 2 trade values; the gate warp finishes a chunk's
+  // first 16 rows, the up warp the last 16 (named barrier of their 64 threads)
+  float *give = reinterpret_cast<float *>(smem + C::STG_OFF + (warp ^ 2) * C::STG_BYTES);
+  const int pair_bar = 1 + 2 * h + (q & 1);
+  // Finishes and stores one tile, whose accumulator starts at `tacc`; arrives on
+  // `release` (cluster address) once the warp has read it.
+  auto finish = [&](const GroupedUnit &un, uint32_t tacc, uint32_t release) {
+    const int nchunk = un.n() / CH;
+    // the lane's column of 8 in the row segments that the warp stores
+    const int scol = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS + wcol + (lane & 3) * 8;
+    if (h >= nchunk) {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster_relaxed(release);
+    }
+#pragma unroll 1
+    for (int c = h; c < nchunk; c += 2) {
+      uint32_t v[CH];
+      if constexpr (C::FUSED) ptx::tmem_ld32(tacc + c * CH, v);
+      else ptx::tmem_ld16(tacc + c * CH, v);
+      ptx::tmem_wait_ld();
+      ptx::reg_fence(v);
+      if constexpr (C::SPLIT) {
+        const float *more = reinterpret_cast<const float *>(smem) + c * CH * 128 + q * 32 + lane;
+        for (int s = 1; s < p.pairs; ++s, more += C::NT * 128)
+#pragma unroll
+          for (int i = 0; i < CH; ++i)
+            v[i] = __float_as_uint(__uint_as_float(v[i]) + more[i * 128]);
+      }
+      if (c + 2 >= nchunk) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(release);
+      }
+      float y[16];
+      if constexpr (C::FUSED) {
+        if (c != h) asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          give[i * 32 + lane] = __uint_as_float(gate ? v[16 + i] : v[i]);
+        asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
+        const float *got = reinterpret_cast<const float *>(stg);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = got[i * 32 + lane];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          y[i] = gate ? silu_mul(__uint_as_float(v[i]), y[i])
+                      : silu_mul(y[i], __uint_as_float(v[16 + i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[i]);
+      }
+      __nv_bfloat16 *sp = reinterpret_cast<__nv_bfloat16 *>(stg) + lane;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sp[i * (C::STG_PITCH / 2)] = __float2bfloat16_rn(y[i]);
+      __syncwarp();
+      const int row0 = un.row0 + c * CH + (C::FUSED && !gate ? 16 : 0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = j * 8 + (lane >> 2);
+        const int row = row0 + t;
+        if (row < un.end && scol < p.N) {
+          uint4 out = *reinterpret_cast<const uint4 *>(stg + t * C::STG_PITCH + (lane & 3) * 16);
+          if (p.rows != nullptr) {
+            // a row number that names no row of A gives zeros
+            const int src = __ldg(p.rows + row);
+            if (src < 0 || src >= p.T) out = make_uint4(0, 0, 0, 0);
+          }
+          *reinterpret_cast<uint4 *>(p.Y + int64_t(row) * p.N + scol) = out;
+        }
+      }
+      __syncwarp();
+    }
+  };
+
 
   if (warp == C::UNIT_WARP) {
     // ------------------------------------------------------------ unit finder
@@ -327,14 +431,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       while (ok && units.next(un, ok)) {
         const int col0 = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS;
         const uint32_t row_bytes = un.row_bytes(0, gather) + un.row_bytes(1, gather);
-        for (int kb = 0; kb < p.num_k_blk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bar(empty_bar(stage), phase ^ 1u, p.timeout_ns, abort_flag, p.err,
                         WAIT_PRODUCER_EMPTY)) {
             ok = false;
             break;
           }
           const uint32_t sw = base + stage * C::STAGE_BYTES;
-          const uint32_t fb = ptx::mapa_shared(full_bar(stage), 0);
+          const uint32_t fb = ptx::mapa_shared(full_bar(stage), lead);
           // the bytes of both CTAs, weights and rows
           if (rank == 0) ptx::mbar_arrive_expect_tx(full_bar(stage), 2 * C::W_BYTES + row_bytes);
           ptx::tma_load_3d_pair(sw, &tmW1, fb, col0, kb * C::BK, un.e);
@@ -389,14 +493,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               idx[j][i] = min(max(__ldg(p.rows + at), 0), p.T - 1);
             }
         }
-        for (int kb = 0; kb < p.num_k_blk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bar(empty_bar(stage), phase ^ 1u, p.timeout_ns, abort_flag, p.err,
                         WAIT_PRODUCER_EMPTY)) {
             ok = false;
             break;
           }
           const uint32_t sa = base + stage * C::STAGE_BYTES + C::W_BYTES;
-          const uint32_t fb = ptx::mapa_shared(full_bar(stage), 0);
+          const uint32_t fb = ptx::mapa_shared(full_bar(stage), lead);
           ptx::mbar_arrive_cluster_relaxed(fb);
           if (gather) {
 #pragma unroll
@@ -435,7 +539,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + abuf * C::ACC_COLS;
-        for (int kb = 0; kb < p.num_k_blk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bar(full_bar(stage), phase, p.timeout_ns, abort_flag, p.err, WAIT_MMA_FULL)) {
             ok = false;
             break;
@@ -448,122 +552,50 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // Weights (MMA A): MN-major 64-column boxes ATOM_BYTES apart, 8-row
             // K groups 1024 bytes apart, 16 K rows = 2048 bytes.  Rows (MMA
             // B): K-major, 128-byte swizzle, 32 bytes of K per MMA.
-            const uint32_t acc = kb != 0 || kk != 0 ? 1u : 0u;
+            const uint32_t acc = kb != kb0 || kk != 0 ? 1u : 0u;
             const uint64_t wdesc = ptx::smem_desc(sw + kk * 2048, C::ATOM_BYTES, 1024, ptx::SW_128B);
             const uint64_t rdesc = ptx::smem_desc(sa + kk * 32, 16, 1024, ptx::SW_128B);
             ptx::mma_f16_pair(d, wdesc, rdesc, idesc, acc);
           }
-          ptx::mma_commit_pair_mc(empty_bar(stage), 0x3);
+          ptx::mma_commit_pair_mc(empty_bar(stage), both);
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        ptx::mma_commit_pair_mc(accf_bar(abuf), 0x3);
+        ptx::mma_commit_pair_mc(accf_bar(abuf), both);
         if (++abuf == 2) {
           abuf = 0;
           aphase ^= 1u;
         }
       }
-      ptx::mma_commit_pair_mc(drain_bar, 0x1);
+      ptx::mma_commit_pair_mc(drain_bar, static_cast<uint16_t>(0x1u << lead));
       wait_quiet(drain_bar, 0, p.timeout_ns);
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ epilogue (warps 0-7, both CTAs)
-    // Warp q (mod 4) reads TMEM lanes [32q, 32q + 32), the tile's rows in the
-    // columns.  Linear: lane i is output column 32q + i; FUSED: warps q = 0, 1
-    // hold the gate and q = 2, 3 the up values of output columns 32 (q % 2) + i.
-    // Per 32 rows (FUSED) or 16 rows (linear) of the tile; warps 0-3 take the
-    // even chunks, warps 4-7 the odd ones.
-    const int q = warp & 3, h = warp >> 2;
-    constexpr int CH = C::FUSED ? 32 : 16;
-    const bool gate = q < 2;
-    const int wcol = C::FUSED ? 32 * (q & 1) : 32 * q;
-    uint8_t *stg = smem + C::STG_OFF + warp * C::STG_BYTES;
-    // FUSED: warps q and q ^ 2 trade values; the gate warp finishes a chunk's
-    // first 16 rows, the up warp the last 16 (named barrier of their 64 threads)
-    float *give = reinterpret_cast<float *>(smem + C::STG_OFF + (warp ^ 2) * C::STG_BYTES);
-    const int pair_bar = 1 + 2 * h + (q & 1);
+    // ------------------------------------------------------------ epilogue
     uint32_t abuf = 0, aphase = 0;
     bool ok = true;
     GroupedUnits<false> units(ring, unitf_bar, unite_bar, p, abort_flag);
-    GroupedUnit un;
     bool gave_up = false;
     while (true) {
-      if (!units.next(un, ok)) {
+      if (!units.next(mine, ok)) {
         gave_up = !ok;
         break;
       }
-      ok = wait_bar(accf_bar(abuf), aphase, p.timeout_ns, abort_flag, p.err,
-                         WAIT_EPI_ACC_FULL);
+      ok = wait_bar(accf_bar(abuf), aphase, p.timeout_ns, abort_flag, p.err, WAIT_EPI_ACC_FULL);
       ok = __all_sync(0xffffffffu, ok);
+      if (C::SPLIT) {  // the only unit: its sums meet after the roles
+        have = ok;
+        break;
+      }
       if (C::FUSED) ok = bar_all(pair_bar, 64, ok);  // both warps go on, or neither
       if (!ok) break;
       ptx::tc_fence_after();
-      const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * C::ACC_COLS;
-      const int nchunk = un.n() / CH;
-      // the lane's column of 8 in the row segments that the warp stores
-      const int scol = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS + wcol + (lane & 3) * 8;
-      const uint32_t release = ptx::mapa_shared(acce_bar(abuf), 0);
-      if (h >= nchunk) {
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(release);
-      }
-#pragma unroll 1
-      for (int c = h; c < nchunk; c += 2) {
-        uint32_t v[CH];
-        if constexpr (C::FUSED) ptx::tmem_ld32(tacc + c * CH, v);
-        else ptx::tmem_ld16(tacc + c * CH, v);
-        ptx::tmem_wait_ld();
-        ptx::reg_fence(v);
-        if (c + 2 >= nchunk) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster_relaxed(release);
-        }
-        float y[16];
-        if constexpr (C::FUSED) {
-          if (c != h) asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            give[i * 32 + lane] = __uint_as_float(gate ? v[16 + i] : v[i]);
-          asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory");
-          const float *got = reinterpret_cast<const float *>(stg);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = got[i * 32 + lane];
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            y[i] = gate ? silu_mul(__uint_as_float(v[i]), y[i])
-                        : silu_mul(y[i], __uint_as_float(v[16 + i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[i]);
-        }
-        __nv_bfloat16 *sp = reinterpret_cast<__nv_bfloat16 *>(stg) + lane;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sp[i * (C::STG_PITCH / 2)] = __float2bfloat16_rn(y[i]);
-        __syncwarp();
-        const int row0 = un.row0 + c * CH + (C::FUSED && !gate ? 16 : 0);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = j * 8 + (lane >> 2);
-          const int row = row0 + t;
-          if (row < un.end && scol < p.N) {
-            uint4 out = *reinterpret_cast<const uint4 *>(stg + t * C::STG_PITCH + (lane & 3) * 16);
-            if (p.rows != nullptr) {
-              // a row number that names no row of A gives zeros
-              const int src = __ldg(p.rows + row);
-              if (src < 0 || src >= p.T) out = make_uint4(0, 0, 0, 0);
-            }
-            *reinterpret_cast<uint4 *>(p.Y + int64_t(row) * p.N + scol) = out;
-          }
-        }
-        __syncwarp();
-      }
+      finish(mine, tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * C::ACC_COLS,
+             ptx::mapa_shared(acce_bar(abuf), lead));
       if (++abuf == 2) {
         abuf = 0;
         aphase ^= 1u;
@@ -571,7 +603,39 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     // A warp that gave up while looking for a unit still meets its partner,
     // which may be waiting for the pair's decision on one.
-    if (C::FUSED && gave_up) bar_all(pair_bar, 64, false);
+    if (C::FUSED && !C::SPLIT && gave_up) bar_all(pair_bar, 64, false);
+  }
+
+  if constexpr (C::SPLIT) {
+    // The pairs' sums: every copy into the first pair's ring and every MMA that
+    // reads it has completed, the others' epilogue warps write theirs there,
+    // and the first pair finishes the tile.
+    ptx::tc_fence_before();
+    __syncwarp();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    if (have && lead != 0) {
+      const uint32_t to = ptx::mapa_shared(base, rank) +
+                          ((lead / 2 - 1) * C::NT * 128 + q * 32 + lane) * 4;
+      const int nchunk = mine.n() / CH;
+#pragma unroll 1
+      for (int c = h; c < nchunk; c += 2) {
+        uint32_t v[CH];
+        if constexpr (C::FUSED) ptx::tmem_ld32(tacc + c * CH, v);
+        else ptx::tmem_ld16(tacc + c * CH, v);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence(v);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) ptx::st_shared_cluster_u32(to + (c * CH + i) * 512, v[i]);
+      }
+    }
+    __syncwarp();
+    ptx::cluster_sync();
+    if (warp < C::EPI_WARPS && lead == 0) {
+      if (C::FUSED) have = bar_all(pair_bar, 64, have);
+      if (have) finish(mine, tacc, ptx::mapa_shared(acce_bar(0), lead));
+    }
   }
 
   // Both CTAs have passed their last use of the pair's resources before either

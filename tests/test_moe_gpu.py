@@ -292,6 +292,16 @@ def test_grouped_long_k_wraps_the_ring(sg, fused):
 
 
 @FORMS
+@pytest.mark.parametrize("gather", [True, False], ids=["rows", "dense"])
+@pytest.mark.parametrize("sizes", [[1, 0], [0, 2, 0, 1], [5, 33, 0, 70], [128, 1], [300], [17, 0, 0, 0, 0, 0, 0, 0, 0, 1]],
+                         ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("NK", [(8, 1024), (72, 1032), (264, 1096), (520, 2056), (2600, 1120)], ids=lambda s: "x".join(map(str, s)))
+def test_grouped_few_units_share_k(sg, fused, gather, sizes, NK):
+    """So few tiles that several pairs share each one's K."""
+    check_grouped(sg, fused, sizes, *NK, T=29 if gather else None)
+
+
+@FORMS
 def test_grouped_next_expert_and_other_rows_never_leak(sg, fused):
     """NaN in an expert without rows, and in rows of A that no place names, stay out
     (a ragged K step must not reach into the next expert's matrix)."""
