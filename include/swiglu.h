@@ -407,7 +407,9 @@ int swiglu_moe_route(const void *logits, int32_t logits_fp32, int32_t renormaliz
  *     swiglu_fused_grouped :  Y[p] = SiLU(a W1[e]) (.) (a W2[e])
  *     swiglu_linear_grouped:  Z[p] = a W[e]
  * with a = A[rows[p]], or A[p] where rows is NULL (then T must equal P).
- * BF16 in, FP32 accumulate, one rounding to BF16.
+ * BF16 in, FP32 accumulate, one rounding to BF16.  Sums run over K in order,
+ * or, where a call has few tiles, over two or four slices of K whose sums are
+ * added in order: equal calls give equal bits.
  *   A       : device, BF16 [T,K]  (read)
  *   W1, W2, W : device, BF16 [E,K,N]  (read)
  *   offsets : device, int32 [E+1]  (read at kernel time); values are clamped

@@ -63,7 +63,7 @@ def _torch_command(target: str):
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
             *(f"-I{p}" for p in inc), TORCH_SRC, "-o", target, "-L", os.path.join(home, "lib"), "-L", PKG,
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-l:" + os.path.basename(LIB),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-l:" + os.path.basename(LIB),
             "-Wl,-rpath,$ORIGIN"]
 
 

@@ -293,6 +293,11 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
     mine[e] = 0;
   }
   ptx::grid_dependency_wait();
+  const int64_t b0 = int64_t(b) * p.block_tokens, entries = int64_t(p.T) * p.k;
+  const int64_t end = min(b0 + p.block_tokens, int64_t(p.T)) * p.k;
+  // the thread's first entry, on its way while the counts are summed
+  int64_t i = b0 * p.k + threadIdx.x;
+  int e_next = i < end ? __ldg(p.ids + i) : -1, s_next = i < end ? p.slots[i] : 0;
   __syncthreads();
   // Thread (g, e) sums blocks g, g + G, ... of expert e (integer sums in
   // shared memory: their order does not matter).
@@ -316,19 +321,21 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
   const int routed = scan_experts(sm, p.E, b == 0 ? p.offsets : nullptr);
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) sm.base[e] += mine[e];
   __syncthreads();
-  const int64_t b0 = int64_t(b) * p.block_tokens, entries = int64_t(p.T) * p.k;
-  const int64_t end = min(b0 + p.block_tokens, int64_t(p.T)) * p.k;
-  for (int64_t i = b0 * p.k + threadIdx.x; i < end; i += blockDim.x) {
-    const int e = __ldg(p.ids + i);
-    if (e >= 0) {
-      const int pos = sm.base[e] + p.slots[i];
+  while (i < end) {
+    if (e_next >= 0) {
+      const int pos = sm.base[e_next] + s_next;
       p.slots[i] = pos;
       p.rows[pos] = static_cast<int32_t>(i) / p.k;  // T * k < 2^31
     }
+    i += blockDim.x;
+    if (i < end) {
+      e_next = __ldg(p.ids + i);
+      s_next = p.slots[i];
+    }
   }
-  for (int64_t i = routed + int64_t(b) * blockDim.x + threadIdx.x; i < entries;
-       i += int64_t(p.blocks) * blockDim.x)
-    p.rows[i] = -1;
+  for (int64_t n = routed + int64_t(b) * blockDim.x + threadIdx.x; n < entries;
+       n += int64_t(p.blocks) * blockDim.x)
+    p.rows[n] = -1;
 }
 
 cudaError_t launch_pdl(void (*kern)(RouteParams), int grid, int cluster, int threads,
@@ -349,9 +356,13 @@ cudaError_t launch_pdl(void (*kern)(RouteParams), int grid, int cluster, int thr
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// Tokens per block of the two-launch form: 32 while that makes at most about one
-// block per SM (4096 tokens: 11.3 us, with 128 a block 12.7 us; 1024: 7.8 and 12.0), then 64 and 128.
-int block_tokens(int64_t T) { return T <= 32 * 152 ? 32 : T <= 64 * 152 ? 64 : kBlockTokens; }
+// Tokens per block of the two-launch form: as many blocks as SMs (GB300's 152),
+// 32 to 128 tokens each, whole groups of eight (4096 tokens in blocks of 32: 11.3
+// us, of 128: 12.7; 1024 tokens 7.8 and 12.0).
+int block_tokens(int64_t T) {
+  const int64_t n = ((T + 151) / 152 + 7) / 8 * 8;
+  return static_cast<int>(std::min<int64_t>(std::max<int64_t>(n, 32), kBlockTokens));
+}
 
 template <int LPT, int EPL>
 cudaError_t launch_route(bool fp32, const RouteParams &p, cudaStream_t s) {
