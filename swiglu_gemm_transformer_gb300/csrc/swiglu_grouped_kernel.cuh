@@ -33,7 +33,7 @@
 //     elect.sync: issued by lane 0 of one warp they took about 50 ns apiece
 //     (gate/up with rows at 64 experts x 1024 rows, K = 2048, N = 1024: 1118 us;
 //     rows copied with cp.async instead 374 us; eight warps like this 326 us, four
-//     366 us, sixteen 320 us but a third fewer registers a thread);
+//     366 us, sixteen 320 us);
 //   * accumulators are double-buffered in TMEM (NT columns each).
 // Unit schedule: every CTA reads `offsets`, counts the row tiles of each
 // expert, and the pairs take the units (expert, row tile, column tile) in
@@ -103,7 +103,10 @@ struct GroupedCfg {
   static constexpr int PRODUCER_WARP = EPI_WARPS;
   static constexpr int MMA_WARP = EPI_WARPS + 1;
   static constexpr int ROW_WARP = EPI_WARPS + 2;  // first of the warps that load rows
-  static constexpr int ROW_WARPS = 8;
+  // 16 where a stage takes 32 gathers per CTA (64 experts x 1024 rows, K = 2048:
+  // 340 us, with 8 warps 347), 8 where it takes 16 (one token's 8 experts: 11.2
+  // us, with 16 warps 12.0); the linear form's rows are dense
+  static constexpr int ROW_WARPS = FUSED && NT == 256 ? 16 : 8;
   static constexpr int UNIT_WARP = ROW_WARP + ROW_WARPS;
   static constexpr int THREADS = 32 * (UNIT_WARP + 1);
   static_assert(NT / 8 % ROW_WARPS == 0, "gathers split evenly");
