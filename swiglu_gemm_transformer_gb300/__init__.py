@@ -620,7 +620,10 @@ def swiglu_moe_route(logits, k: int, *, renormalize: bool = False, scale: float 
     Returns MoeRoute(ids [T,k], weights [T,k], offsets [E+1], rows [T*k],
     slots [T,k]): the chosen experts (-1: none left, every other logit -inf)
     with their softmax weights, and the order of the (token, choice) entries
-    by expert that swiglu_fused_grouped reads."""
+    by expert that swiglu_fused_grouped reads.
+
+    `stream`, here and in the block's other calls: everything that the call
+    allocates belongs to it, as under torch.cuda.stream(stream)."""
     return MoeRoute(*_native().moe_route(logits, k, renormalize, scale, ids, weights, offsets, rows, slots,
                                          workspace, stream))
 

@@ -86,16 +86,24 @@ struct Call {
     }
     return t;
   }
-  // The stream argument: None (the current one), a handle, or an object with one.
-  void *stream(PyObject *o) {
-    if (o == Py_None)
-      return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
+  // Makes the stream argument's stream the current one: None (it is already), a
+  // handle, or an object with one.  Outputs and workspaces come from the
+  // allocator's pool of the current stream, so memory that work of another
+  // stream still uses is not handed to this call, nor this call's to others.
+  cudaStream_t enter(PyObject *o, c10::cuda::OptionalCUDAStreamGuard &guard) const {
+    const auto dev = static_cast<c10::DeviceIndex>(device);
+    const cudaStream_t current = c10::cuda::getCurrentCUDAStream(dev).stream();
+    if (o == Py_None) return current;
     PyObject *h = PyLong_Check(o) ? (Py_INCREF(o), o) : PyObject_GetAttrString(o, "cuda_stream");
     if (!h) throw Refused();
     void *p = PyLong_AsVoidPtr(h);
     Py_DECREF(h);
     if (PyErr_Occurred()) throw Refused();
-    return p;
+    const auto s = static_cast<cudaStream_t>(p);
+    // (the handle of the legacy default stream has no pool of its own)
+    const cudaStream_t pool = s == cudaStreamLegacy ? nullptr : s;
+    if (pool != current) guard.reset_stream(c10::cuda::getStreamFromExternal(pool, dev));
+    return s;
   }
   // Raises SwigluError for a status other than SWIGLU_OK.
   void check(int status) const {
@@ -164,6 +172,8 @@ PyObject *moe_route(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (k < 1 || k > E)
       refuse(PyExc_ValueError, "k must be in [1, %lld], got %lld", (long long)E, (long long)k);
     const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
+    c10::cuda::OptionalCUDAStreamGuard pool;
+    void *s = c.enter(a[10], pool);
     Tensor out[5] = {c.output(a[4], "ids", ScalarType::Int, {T, k}),
                      c.output(a[5], "weights", ScalarType::Float, {T, k}),
                      c.output(a[6], "offsets", ScalarType::Int, {E + 1}),
@@ -179,7 +189,6 @@ PyObject *moe_route(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const bool fp32 = logits.scalar_type() == ScalarType::Float, renorm = truth(a[2]);
     const float scale = static_cast<float>(number(a[3]));
-    void *s = c.stream(a[10]);
     c.check(unlocked([&] {
       return swiglu_moe_route(logits.data_ptr(), fp32, renorm, scale, ptr<int32_t>(out[0]),
                               ptr<float>(out[1]), ptr<int32_t>(out[2]), ptr<int32_t>(out[3]),
@@ -211,8 +220,9 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Tensor *rows = a[4] != Py_None ? &c.tensor(a[4], "rows", ScalarType::Int, 1) : nullptr;
     const int64_t P = rows ? rows->numel() : T;
     const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
+    c10::cuda::OptionalCUDAStreamGuard pool;
+    void *s = c.enter(a[6], pool);
     Tensor Y = c.output(a[5], "the output", ScalarType::BFloat16, {P, N});
-    void *s = c.stream(a[6]);
     // (an empty tensor has no address: any other stands for "rows are given")
     const int32_t *r = !rows ? nullptr : P > 0 ? ptr<int32_t>(*rows) : ptr<int32_t>(offsets);
     c.check(unlocked([&] {
@@ -273,9 +283,10 @@ PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const float scale = static_cast<float>(number(a[7])), eps = static_cast<float>(number(a[9]));
     const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
+    c10::cuda::OptionalCUDAStreamGuard pool;
+    void *s = c.enter(a[12], pool);
     Tensor Rout = c.output(a[10], "Rout", R.scalar_type(), {T, D});
     Tensor H = c.output(a[11], "H", bf, {T, D});
-    void *s = c.stream(a[12]);
     // (slots without columns have no address: any other stands for "slots are given")
     auto at = [&](const Tensor *t) { return !t ? nullptr : t->numel() > 0 ? t->data_ptr() : R.data_ptr(); };
     c.check(unlocked([&] {

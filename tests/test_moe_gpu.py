@@ -181,6 +181,44 @@ def test_route_runs_again_into_the_same_buffers_and_on_another_stream(sg):
         assert (out.offsets.cpu().numpy() == offsets).all() and (out.slots.cpu().numpy() == slots).all()
 
 
+@pytest.mark.parametrize("stream", [lambda s: s, lambda s: s.cuda_stream], ids=["object", "handle"])
+def test_outputs_and_workspaces_belong_to_the_stream_of_the_call(sg, stream):
+    """Memory that the current stream has queued work for is not handed to a call
+    on another stream, nor the call's workspace to the current stream."""
+    T, E, k, N, K = 4096, 64, 8, 256, 128
+    s = torch.cuda.Stream()
+    gen = _gen("pools")
+    lg = torch.randn(T, E, generator=gen).to(DEV)
+    A, R = (torch.randn(T, K, generator=gen).to(DEV, BF) for _ in range(2))
+    W1, W2 = (torch.randn(E, K, N, generator=gen).div(11).to(DEV, BF) for _ in range(2))
+    W3 = torch.randn(E, N, K, generator=gen).div(16).to(DEV, BF)
+
+    def step(**kw):
+        r = sg.swiglu_moe_route(lg, k, renormalize=True, **kw)
+        y = sg.swiglu_fused_grouped(A, W1, W2, r.offsets, r.rows, **kw)
+        z = sg.swiglu_linear_grouped(y, W3, r.offsets, **kw)
+        return [*r, y, z, *sg.swiglu_residual_norm(z, R, slots=r.slots, weights=r.weights, **kw)]
+
+    want = [t.cpu() for t in step()]
+    sizes = [t.numel() * t.element_size() for t in want] + [sg.lib().swiglu_moe_route_workspace_size(T, E, k)]
+    torch.cuda.synchronize()
+    # the current stream still has to write to blocks that it has given back
+    torch.cuda._sleep(100_000_000)
+    for n in sizes * 2:
+        torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0x7F)
+    got = step(stream=stream(s))
+    # the side stream still works with the workspace when the current one asks for memory
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+    late = step(stream=stream(s))
+    for n in sizes * 2:
+        torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0x7F)
+    torch.cuda.synchronize()
+    _status(sg)
+    for w, a, b in zip(want, got, late):
+        assert torch.equal(w, a.cpu()) and torch.equal(w, b.cpu())
+
+
 # ---- grouped products -----------------------------------------------------------
 
 
