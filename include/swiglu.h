@@ -418,9 +418,9 @@ int swiglu_moe_route(const void *logits, int32_t logits_fp32, int32_t renormaliz
  *       outside [0, T) gives a row of zeros
  *   Y, Z    : device, BF16 [P,N]; the places before offsets[0] and from
  *       offsets[E] on are left as they are
- * Groups may be empty or of any size.  E <= 1024, K and N multiples of 8,
- * K * N < 2^39, pointers 16-byte aligned (offsets and rows 4-byte); Y must not
- * overlap an input.  K = 0 or T = 0 makes every product zero: Y is filled
+ * Groups may be empty or of any size.  E <= 1024, P and N below 2^31 - 256,
+ * K and N multiples of 8, K * N < 2^39, pointers 16-byte aligned (offsets and
+ * rows 4-byte); Y must not overlap an input.  K = 0 or T = 0 makes every product zero: Y is filled
  * with zeros.  P = 0 or N = 0 enqueues nothing.
  */
 int swiglu_fused_grouped(const void *A, const void *W1, const void *W2, const int32_t *offsets,

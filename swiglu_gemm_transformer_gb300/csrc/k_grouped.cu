@@ -63,6 +63,8 @@ cudaError_t launch_grouped(GroupedLaunch &gl) {
 }
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+// Places and columns: the last tile's bounds, up to 256 past them, are 32-bit too.
+constexpr int64_t kMaxTiled = kMaxDim - 256;
 
 // W2 == nullptr: the linear form.
 int run_grouped(const void *A, const void *W1, const void *W2, bool fused, const int32_t *offsets,
@@ -70,7 +72,7 @@ int run_grouped(const void *A, const void *W1, const void *W2, bool fused, const
                 int64_t K, void *stream) {
   if (T < 0 || P < 0 || E < 1 || N < 0 || K < 0) return SWIGLU_ERR_INVALID_ARG;
   if (!rows && T != P) return SWIGLU_ERR_INVALID_ARG;
-  if (T > kMaxDim || P > kMaxDim || N > kMaxDim || K > kMaxDim || E > kMaxExperts)
+  if (T > kMaxDim || P > kMaxTiled || N > kMaxTiled || K > kMaxDim || E > kMaxExperts)
     return SWIGLU_ERR_UNSUPPORTED;
   if (P == 0 || N == 0) return SWIGLU_OK;
   // one expert's matrix: the tensor map's largest stride is 2^40 bytes

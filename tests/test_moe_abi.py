@@ -70,6 +70,13 @@ def test_grouped_refusals(lib, fused, kw, want):
     assert _grouped(lib, fused, **kw) == want
 
 
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("kw", [dict(P=(1 << 31) - 1), dict(P=(1 << 31) - 256), dict(N=(1 << 31) - 8, K=8),
+                                dict(N=(1 << 31) - 256, K=8)])
+def test_grouped_refuses_sizes_whose_last_tile_passes_32_bits(lib, fused, kw):
+    assert _grouped(lib, fused, **kw) == UNS
+
+
 def test_grouped_needs_both_weights(lib):
     assert _grouped(lib, True, W2=None) == INV
     assert _grouped(lib, True, W2=C + 4) == MIS
