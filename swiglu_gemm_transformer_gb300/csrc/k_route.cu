@@ -50,7 +50,9 @@ constexpr int kMaxK = 32;
 constexpr int kOneTokens = 256;          // tokens of the one-launch form,
 constexpr int kOneBlockTokens = 32;      // per block of its cluster (at most eight)
 constexpr int kBlockTokens = 128;        // most tokens per block otherwise
-constexpr int kCounters = 16384;         // warps of a block x experts
+// Warps of a block x experts: 32 warps up to 510 experts, and RouteSmem is the 48 KB
+// that a kernel may hold without asking.
+constexpr int kCounters = 16320;
 constexpr unsigned kAll = 0xffffffffu;
 
 struct RouteParams {
@@ -179,6 +181,8 @@ struct RouteSmem {
   uint16_t ids[kBlockTokens * kMaxK];
   int32_t carry[32];
 };
+
+static_assert(sizeof(RouteSmem) <= 48 * 1024, "static shared memory");
 
 // Exclusive scan of base[0, E) in place; returns the total.  All threads.
 __device__ __forceinline__ int scan_experts(RouteSmem &sm, int E, int32_t *offsets) {
