@@ -55,6 +55,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "grouped_units.h"
 #include "sm103_ptx.cuh"
 #include "tc_common.cuh"
 
@@ -132,24 +133,6 @@ __device__ __forceinline__ static bool bar_all(int id, int threads, bool ok) {
       : "memory");
   return r != 0;
 }
-
-// One unit: rows [row0, end) of expert e, column tile nb; row0 = -1: no more.
-// 16 bytes, read from shared memory as one int4.
-struct __align__(16) GroupedUnit {
-  int row0, end, e, nb;
-  __device__ int n() const { return (end - row0 + 31) & ~31; }  // MMA N
-  // Rows of the CTA `rank`'s half that belong to the tile.
-  __device__ int rows_of(int rank) const {
-    const int half = n() >> 1;
-    return min(max(end - row0 - rank * half, 0), half);
-  }
-  // Bytes of a CTA's copies of them per stage: whole groups of four gathered
-  // rows, whole boxes of dense ones.
-  __device__ uint32_t row_bytes(int rank, bool gather) const {
-    const int grain = gather ? 4 : 32;
-    return ((rows_of(rank) + grain - 1) & ~(grain - 1)) * 128;
-  }
-};
 
 // The units of one role, in order.  Every lane of the role's warp calls
 // next() (or one lane alone, for a role of one lane: ALONE).
@@ -375,7 +358,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       v = max(v, top);
       const int prev = __shfl_up_sync(0xffffffffu, v, 1);
       // row tiles of expert e - 1
-      int t = e >= 1 && e <= p.E ? (v - (lane == 0 ? top : prev) + C::NT - 1) / C::NT : 0;
+      int t = e >= 1 && e <= p.E ? row_tiles<C::NT>(v - (lane == 0 ? top : prev)) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int w = __shfl_up_sync(0xffffffffu, t, o);
@@ -390,35 +373,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       sum = __shfl_sync(0xffffffffu, t, 31);
     }
     __syncwarp();
-    const int64_t num_units = int64_t(tiles[p.E]) * p.num_n_blk;
     for (uint32_t block = 0;; ++block) {
       const bool ok = wait_bar(unite_bar + 8u * (block & 1u), ((block >> 1) & 1u) ^ 1u,
                                p.timeout_ns, abort_flag, p.err, WAIT_SCHED_EMPTY);
       if (!__all_sync(0xffffffffu, ok)) break;
-      const int64_t u = cid + (int64_t(block) * 32 + lane) * ncl;
-      GroupedUnit r = {-1, -1, 0, 0};
-      if (u < num_units) {
-        // the expert whose row tiles hold tile u / num_n_blk
-        const int tt = static_cast<int>(u / p.num_n_blk);
-        int lo = 0, hi = p.E;  // tiles[lo] <= tt < tiles[hi]
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (tiles[mid] <= tt) lo = mid; else hi = mid;
-        }
-        const int mt = tiles[lo + 1] - tiles[lo];
-        const int64_t local = u - int64_t(tiles[lo]) * p.num_n_blk;
-        const int64_t per_group = int64_t(C::GROUP) * p.num_n_blk;
-        const int first = static_cast<int>(local / per_group) * C::GROUP;
-        const int span = min(C::GROUP, mt - first);
-        const int64_t w = local % per_group;
-        const int cnt = off[lo + 1] - off[lo];
-        // even split in steps of 32 rows; no tile is empty: cnt > (mt - 1) * NT
-        const int step = ((cnt + mt - 1) / mt + 31) & ~31;
-        r.e = lo;
-        r.nb = static_cast<int>(w / span);
-        r.row0 = off[lo] + (first + static_cast<int>(w % span)) * step;
-        r.end = min(r.row0 + step, off[lo + 1]);
-      }
+      const GroupedUnit r = grouped_unit<C::GROUP>(cid + (int64_t(block) * 32 + lane) * ncl, off,
+                                                   tiles, p.E, p.num_n_blk);
       *reinterpret_cast<int4 *>(ring + 32 * (block & 1u) + lane) = make_int4(r.row0, r.end, r.e, r.nb);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(unitf_bar + 8u * (block & 1u));
