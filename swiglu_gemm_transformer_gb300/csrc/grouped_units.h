@@ -78,4 +78,15 @@ SWIGLU_UNITS_FN GroupedUnit grouped_unit(int64_t u, const int *off, const int *t
   return r;
 }
 
+// The units of one of two warps that finish them together (they trade values
+// and meet at a barrier in between).  take() is true when this warp has the next
+// unit and its sums; false at the end of the units and where a wait gave up,
+// which may happen to one of the two alone.  So the warps meet once for every
+// take(), whatever it said: agree(ok) waits for the other warp and returns
+// whether both said true.  Neither can leave while the other still waits for it.
+template <class Take, class Agree, class Finish>
+SWIGLU_UNITS_FN void finish_together(Take take, Agree agree, Finish finish) {
+  while (agree(take())) finish();
+}
+
 }  // namespace swiglu

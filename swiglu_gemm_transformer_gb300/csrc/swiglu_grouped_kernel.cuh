@@ -540,33 +540,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     uint32_t abuf = 0, aphase = 0;
-    bool ok = true;
     GroupedUnits<false> units(ring, unitf_bar, unite_bar, p, abort_flag);
-    bool gave_up = false;
-    while (true) {
-      if (!units.next(mine, ok)) {
-        gave_up = !ok;
-        break;
-      }
+    // the next unit, its sums complete; false at the end, or when a wait gave up
+    auto take = [&] {
+      bool ok = true;
+      if (!units.next(mine, ok)) return false;
       ok = wait_bar(accf_bar(abuf), aphase, p.timeout_ns, abort_flag, p.err, WAIT_EPI_ACC_FULL);
-      ok = __all_sync(0xffffffffu, ok);
-      if (C::SPLIT) {  // the only unit: its sums meet after the roles
-        have = ok;
-        break;
-      }
-      if (C::FUSED) ok = bar_all(pair_bar, 64, ok);  // both warps go on, or neither
-      if (!ok) break;
-      ptx::tc_fence_after();
-      finish(mine, tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * C::ACC_COLS,
-             ptx::mapa_shared(acce_bar(abuf), lead));
-      if (++abuf == 2) {
-        abuf = 0;
-        aphase ^= 1u;
-      }
+      return __all_sync(0xffffffffu, ok) != 0;
+    };
+    if constexpr (C::SPLIT) {  // the only unit: its sums meet after the roles
+      have = take();
+    } else {
+      finish_together(
+          take, [&](bool ok) { return C::FUSED ? bar_all(pair_bar, 64, ok) : ok; },
+          [&] {
+            ptx::tc_fence_after();
+            finish(mine, tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * C::ACC_COLS,
+                   ptx::mapa_shared(acce_bar(abuf), lead));
+            if (++abuf == 2) {
+              abuf = 0;
+              aphase ^= 1u;
+            }
+          });
     }
-    // A warp that gave up while looking for a unit still meets its partner,
-    // which may be waiting for the pair's decision on one.
-    if (C::FUSED && !C::SPLIT && gave_up) bar_all(pair_bar, 64, false);
   }
 
   if constexpr (C::SPLIT) {

@@ -13,6 +13,11 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "swiglu_gemm_transformer_gb300", "csrc")
 
 SOURCE = r"""
+#include <chrono>
+#include <condition_variable>
+#include <mutex>
+#include <thread>
+
 #include "grouped_units.h"
 using namespace swiglu;
 extern "C" int t_row_tiles(int nt, int cnt) { return nt == 256 ? row_tiles<256>(cnt) : row_tiles<128>(cnt); }
@@ -27,6 +32,39 @@ extern "C" void t_units(int64_t u0, int count, const int *off, const int *tiles,
       out[5 + r] = u.rows_of(r), out[7 + r] = u.row_bytes(r, false), out[9 + r] = u.row_bytes(r, true);
   }
 }
+// Two warps that take n[0] and n[1] units before the end (or before a wait gives
+// up); done[w]: units that warp w finished.  Returns whether one of them was left
+// waiting for the other.
+extern "C" int t_together(const int *n, int *done) {
+  std::mutex m;
+  std::condition_variable cv;
+  int here = 0, round = 0, stuck = 0;
+  bool all = true, said = false;
+  auto agree = [&](bool ok) {
+    std::unique_lock<std::mutex> l(m);
+    all = all && ok;
+    if (++here == 2) {
+      said = all, here = 0, all = true, ++round;
+      cv.notify_all();
+      return said;
+    }
+    const int mine = round;
+    if (!cv.wait_for(l, std::chrono::seconds(2), [&] { return round != mine; })) {
+      stuck = 1;
+      return false;
+    }
+    return said;
+  };
+  auto warp = [&](int w) {
+    int taken = 0;
+    done[w] = 0;
+    finish_together([&] { return taken++ < n[w]; }, agree, [&] { ++done[w]; });
+  };
+  std::thread other(warp, 1);
+  warp(0);
+  other.join();
+  return stuck;
+}
 """
 
 
@@ -36,7 +74,7 @@ def lib(tmp_path_factory):
     src, out = d / "units.cpp", d / "units.so"
     src.write_text(SOURCE)
     # (wrapping sums, so that one past 32 bits shows as a wrong number)
-    subprocess.run(["g++", "-std=c++17", "-O1", "-fwrapv", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(out)], check=True)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-fwrapv", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(out)], check=True)
     m = ctypes.CDLL(str(out))
     m.t_units.argtypes = [ctypes.c_int64, ctypes.c_int] + [ctypes.c_void_p] * 2 + [ctypes.c_int] * 2 + [ctypes.c_void_p]
     m.t_units.restype = None
@@ -97,3 +135,12 @@ def test_units_take_every_place_and_column_once(lib, nt, num_n_blk, first, sizes
         seen[row0:end, nb] += 1
     assert (out[total:, 0] == -1).all()
     assert (seen[first:] == 1).all() and (seen[:first] == 0).all()
+
+
+@pytest.mark.parametrize("n", [(0, 0), (3, 3), (0, 1), (1, 0), (2, 5), (5, 2), (64, 63), (63, 64)])
+def test_two_warps_of_which_one_stops_early_both_end(lib, n):
+    """One warp of two may see the end of the units (or a wait of its own give
+    up) where the other does not; both leave, after the same units."""
+    want, done = (ctypes.c_int * 2)(*n), (ctypes.c_int * 2)()
+    assert lib.t_together(want, done) == 0
+    assert list(done) == [min(n)] * 2
