@@ -517,7 +517,9 @@ const char *swiglu_status_string(int32_t status);
 int swiglu_device_status(void *stream, uint32_t *detail);
 
 /* Time limit of every device-side wait, in nanoseconds (default 2e9, i.e. two
- * seconds; minimum 1e6).  Applies to launches enqueued after the call. */
+ * seconds; minimum 1e6).  A wait covers one tile's work at most, and one of the
+ * grouped products 32 tiles', for which its limit is 32 times this one.  Applies
+ * to launches enqueued after the call. */
 int swiglu_set_wait_timeout_ns(uint64_t ns);
 
 /*

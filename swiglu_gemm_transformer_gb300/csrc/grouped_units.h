@@ -34,6 +34,18 @@ struct alignas(16) GroupedUnit {
   }
 };
 
+// Units are found and handed on in blocks of this many (one per lane of a warp).
+constexpr int kUnitBlock = 32;
+
+// Time limit of the wait for a whole block of units to be taken: `limit_ns`, the
+// limit of one wait, for each of them.  (Every other wait lasts about one unit at
+// most: with K = 18944 a unit takes about 0.1 ms, a block 3 ms, and limits from
+// 1 ms on are allowed.)  A wait that stalls ends by its own limit all the same, and
+// its abort flag ends this one.
+SWIGLU_UNITS_FN uint64_t block_limit(uint64_t limit_ns) {
+  return limit_ns > UINT64_MAX / kUnitBlock ? UINT64_MAX : limit_ns * kUnitBlock;
+}
+
 // Sums of 32-bit places below stay below 2^31 for groups of up to 2^31 - 257
 // places (the entry points refuse more): a sum that passes it would give a
 // tile of a negative size.

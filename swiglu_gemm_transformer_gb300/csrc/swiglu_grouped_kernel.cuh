@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __syncwarp();
     for (uint32_t block = 0;; ++block) {
       const bool ok = wait_bar(unite_bar + 8u * (block & 1u), ((block >> 1) & 1u) ^ 1u,
-                               p.timeout_ns, abort_flag, p.err, WAIT_SCHED_EMPTY);
+                               block_limit(p.timeout_ns), abort_flag, p.err, WAIT_SCHED_EMPTY);
       if (!__all_sync(0xffffffffu, ok)) break;
       const GroupedUnit r = grouped_unit<C::GROUP>(cid + (int64_t(block) * 32 + lane) * ncl, off,
                                                    tiles, p.E, p.num_n_blk);

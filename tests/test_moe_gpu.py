@@ -339,6 +339,29 @@ def test_grouped_few_units_share_k(sg, fused, gather, sizes, NK):
     check_grouped(sg, fused, sizes, *NK, T=29 if gather else None)
 
 
+def test_grouped_many_long_units_within_a_short_limit(sg):
+    """The finder of the units waits for 32 of them at a time: about 2.7 ms here,
+    where one takes 0.08 ms, so a limit of 1.5 ms (a wait may take 1 ms or more) is
+    kept by every wait of its own and must not end this one."""
+    P, K, N = 85000, 16384, 4096        # 333 row tiles x 16 column tiles: 70 units a pair
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    X = torch.empty(P, K, dtype=BF, device=DEV)
+    for a in range(0, P, 5000):
+        X[a:a + 5000] = torch.randn(5000, K, generator=gen, device=DEV)
+    W = (torch.randn(1, K, N, generator=gen, device=DEV) / 128).to(BF)
+    off = torch.tensor([0, P], dtype=torch.int32, device=DEV)
+    _status(sg)
+    sg.swiglu_set_wait_timeout_ns(1_500_000)
+    try:
+        Z = sg.swiglu_linear_grouped(X, W, off)
+    finally:
+        sg.swiglu_set_wait_timeout_ns(2_000_000_000)
+    _status(sg)
+    for a, b in ((0, 3), (42000, 42002), (P - 3, P)):
+        ref, tol = grouped_ref(X[a:b].cpu(), [W.cpu()], [0, b - a], None)
+        assert ((Z[a:b].double().cpu() - ref).abs() <= tol).all(), (a, b)
+
+
 @FORMS
 def test_grouped_next_expert_and_other_rows_never_leak(sg, fused):
     """NaN in an expert without rows, and in rows of A that no place names, stay out

@@ -21,6 +21,7 @@ SOURCE = r"""
 #include "grouped_units.h"
 using namespace swiglu;
 extern "C" int t_row_tiles(int nt, int cnt) { return nt == 256 ? row_tiles<256>(cnt) : row_tiles<128>(cnt); }
+extern "C" uint64_t t_block_limit(uint64_t ns) { return block_limit(ns); }
 extern "C" int t_tile_rows(int cnt, int mt) { return tile_rows(cnt, mt); }
 // out: row0, end, expert, column tile, MMA N, rows of either CTA, bytes of either
 // (dense, then gathered) of the units u0 .. u0 + count - 1
@@ -78,6 +79,7 @@ def lib(tmp_path_factory):
     m = ctypes.CDLL(str(out))
     m.t_units.argtypes = [ctypes.c_int64, ctypes.c_int] + [ctypes.c_void_p] * 2 + [ctypes.c_int] * 2 + [ctypes.c_void_p]
     m.t_units.restype = None
+    m.t_block_limit.argtypes, m.t_block_limit.restype = [ctypes.c_uint64], ctypes.c_uint64
     return m
 
 
@@ -144,3 +146,8 @@ def test_two_warps_of_which_one_stops_early_both_end(lib, n):
     want, done = (ctypes.c_int * 2)(*n), (ctypes.c_int * 2)()
     assert lib.t_together(want, done) == 0
     assert list(done) == [min(n)] * 2
+
+
+@pytest.mark.parametrize("ns", [10**6, 2 * 10**9, (1 << 64) // 32 - 1, (1 << 64) // 32, (1 << 64) - 1])
+def test_limit_of_the_wait_for_a_block_of_units(lib, ns):
+    assert lib.t_block_limit(ns) == min(32 * ns, (1 << 64) - 1)
