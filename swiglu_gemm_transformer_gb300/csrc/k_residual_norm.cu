@@ -309,10 +309,16 @@ __global__ void __launch_bounds__(THREADS + 32, ring_most_blocks(THREADS, VPT))
         spin_ns(100000);  // aborted: copies already in flight land
         break;
       }
+      // lane 0 saw that the rows' warps have read the stage: now every lane may
+      // write it (shuffles and ballots order no memory)
+      __syncwarp();
       uint8_t *side = smem + l.side_off + stage * (kRingMaxK + 4) * 4;
       reinterpret_cast<float *>(side)[lane] = w;
       const uint32_t mask = __ballot_sync(0xffffffffu, slot >= 0);
       const uint32_t dst = ptx::smem_u32(smem) + stage * l.stage_bytes;
+      // the lanes' weights are written before lane 0's arrival hands them to the
+      // rows' warps, and the bytes are expected before the copies start
+      __syncwarp();
       if (lane == 0) {
         reinterpret_cast<uint32_t *>(side)[kRingMaxK] = mask;
         ptx::mbar_arrive_expect_tx(full(stage), l.z_bytes * __popc(mask) + l.r_bytes + l.g_bytes);

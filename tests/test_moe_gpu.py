@@ -555,6 +555,24 @@ def test_norm_many_rows(sg, D, k, r32):
     check_norm(sg, 701, D, k=k, r32=r32, gate="rows" if D % 16 == 0 else "vector", edit=edit)
 
 
+def test_norm_weights_of_every_choice_reach_their_row(sg):
+    """The shortest rows and the most choices of the ring form: a row's copies take
+    the least time that they can, and 30 lanes write a weight each.  Only one
+    choice of a row counts, a different one from row to row, and it is exact."""
+    T, D, k = 60000, 8, 30
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    Z = torch.randn(T, D, generator=gen, device=DEV).to(BF)
+    at = torch.randint(0, k, (T, 1), generator=gen, device=DEV)
+    slots = torch.randint(0, T, (T, k), generator=gen, device=DEV).int()
+    weights = torch.zeros(T, k, device=DEV).scatter_(1, at, 1.0 + at.float())
+    R = torch.zeros(T, D, device=DEV)
+    want = Z[slots.gather(1, at).long().squeeze(1)].float() * (1.0 + at.float())
+    for _ in range(20):
+        Ro, _ = sg.swiglu_residual_norm(Z, R, slots=slots, weights=weights, post_norm=False)
+        assert torch.equal(Ro, want)
+    _status(sg)
+
+
 @pytest.mark.parametrize("gate", [None, "vector", "rows", "strided", "expanded"])
 @pytest.mark.parametrize("post", [True, False])
 def test_norm_many_rows_forms(sg, gate, post):
