@@ -603,7 +603,7 @@ def _native():
             import torch  # noqa: F401  (the module uses its libraries)
             if not os.path.exists(TORCH_LIB_PATH):
                 raise RuntimeError(
-                    f"{TORCH_LIB_PATH} is missing: build the library first "
+                    f"{TORCH_LIB_PATH} is missing: build the library first, with a PyTorch that has CUDA "
                     "(python -c 'import __graft_entry__ as g; g.build()')")
             loader = importlib.machinery.ExtensionFileLoader("_swiglu_torch", TORCH_LIB_PATH)
             spec = importlib.util.spec_from_file_location("_swiglu_torch", TORCH_LIB_PATH, loader=loader)

@@ -4,7 +4,8 @@ Each translation unit under ``csrc/`` compiles in parallel to an object file
 under ``_build/``; the objects link into ``libswiglu_gb300.so`` beside this
 file (CUDA runtime linked statically, the driver reached through
 cudaGetDriverEntryPoint, so the library needs no libcuda at link time).  The
-PyTorch module ``_swiglu_torch.so`` links to it and to the running torch.
+PyTorch module ``_swiglu_torch.so`` links to it and to the running torch; where
+there is no PyTorch with CUDA, only the C library is built.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -72,8 +74,17 @@ def _torch_stamp() -> str:
     return torch.__version__
 
 
-def build_torch(force: bool = False) -> str:
-    """Build the PyTorch module; it links to the CUDA library, so that comes first."""
+def build_torch(force: bool = False):
+    """Build the PyTorch module; it links to the CUDA library, so that comes first.
+
+    Returns its path, or None where there is no PyTorch with CUDA."""
+    try:
+        import torch
+    except ModuleNotFoundError:
+        torch = None
+    if torch is None or torch.version.cuda is None:
+        print(f"no PyTorch with CUDA: {os.path.basename(TORCH_LIB)} is not built", file=sys.stderr)
+        return None
     stamp = os.path.join(BUILD, "torch_version")
     same = os.path.exists(stamp) and open(stamp).read() == _torch_stamp()
     if not force and same and not _stale(TORCH_LIB, [TORCH_SRC, os.path.join(INCLUDE, "swiglu.h")]):
@@ -125,5 +136,4 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True))
