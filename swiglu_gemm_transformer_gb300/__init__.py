@@ -647,8 +647,8 @@ def swiglu_linear_grouped(X, W, offsets, rows=None, Z=None, *, stream=None):
 
 
 def swiglu_residual_norm(Z, R, *, slots=None, weights=None, post_norm: bool = True, gamma_post=None,
-                         gate=None, residual_scale: float = 1.0, gamma_pre=None, eps: float = 1e-6,
-                         Rout=None, H=None, stream=None):
+                         gate=None, residual_scale: float = 1.0, pre_norm: bool = True, gamma_pre=None,
+                         eps: float = 1e-6, Rout=None, H=None, stream=None):
     """The end of a block and the norm before the next one; returns (R', H):
 
         z  = sum_j weights[t,j] * Z[slots[t,j]]   (Z[t] without slots)
@@ -657,9 +657,10 @@ def swiglu_residual_norm(Z, R, *, slots=None, weights=None, post_norm: bool = Tr
 
     Z bf16 [P,D]; R bf16 or fp32 [T,D]; slots/weights int32/fp32 [T,k]; gate
     bf16 [D] or [T,D] (rows may be strided, or broadcast with stride 0);
-    gammas bf16 [D] or None for ones; post_norm=False leaves z as it is.
-    Rout may be R."""
-    return _native().residual_norm(Z, R, slots, weights, post_norm, gamma_post, gate, residual_scale,
+    gammas bf16 [D] or None for ones; post_norm=False leaves z as it is;
+    pre_norm=False makes no H (a model's last block): it is None.  Rout may be
+    R."""
+    return _native().residual_norm(Z, R, slots, weights, post_norm, gamma_post, gate, residual_scale, pre_norm,
                                    gamma_pre, eps, Rout, H, stream)
 
 

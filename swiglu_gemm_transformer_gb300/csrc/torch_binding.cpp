@@ -235,10 +235,10 @@ PyObject *grouped(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// (Z, R, slots, weights, post_norm, gamma_post, gate, residual_scale, gamma_pre, eps, Rout, H, stream)
+// (Z, R, slots, weights, post_norm, gamma_post, gate, residual_scale, pre_norm, gamma_pre, eps, Rout, H, stream)
 PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    if (n != 13) refuse(PyExc_TypeError, "residual_norm takes 13 arguments");
+    if (n != 14) refuse(PyExc_TypeError, "residual_norm takes 14 arguments");
     Call c{"swiglu_residual_norm"};
     const auto bf = ScalarType::BFloat16;
     const Tensor &Z = c.tensor(a[0], "Z", bf, 2);
@@ -259,16 +259,18 @@ PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       if (slots->size(0) != T || weights->size(0) != T || weights->size(1) != k)
         refuse(PyExc_ValueError, "slots and weights must be [T, k]");
     }
-    const bool post = truth(a[4]);
+    const bool post = truth(a[4]), pre = truth(a[8]);
     const Tensor *gamma[2] = {nullptr, nullptr};
     for (int i = 0; i < 2; ++i) {
-      PyObject *o = a[i == 0 ? 5 : 8];
+      PyObject *o = a[i == 0 ? 5 : 9];
       if (o == Py_None) continue;
       const char *what = i == 0 ? "gamma_post" : "gamma_pre";
       gamma[i] = &c.tensor(o, what, bf, 1);
       if (gamma[i]->numel() != D) refuse(PyExc_ValueError, "%s must have %lld elements", what, (long long)D);
     }
     if (gamma[0] && !post) refuse(PyExc_ValueError, "gamma_post without post_norm");
+    if (gamma[1] && !pre) refuse(PyExc_ValueError, "gamma_pre without pre_norm");
+    if (a[12] != Py_None && !pre) refuse(PyExc_ValueError, "H without pre_norm");
     const Tensor *gate = nullptr;
     int64_t stride = 0;
     if (a[6] != Py_None) {
@@ -281,23 +283,25 @@ PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         refuse(PyExc_ValueError, "gate must be [D] or [T, D] with contiguous rows");
       stride = gate->dim() == 2 && T > 1 ? gate->stride(0) : 0;
     }
-    const float scale = static_cast<float>(number(a[7])), eps = static_cast<float>(number(a[9]));
+    const float scale = static_cast<float>(number(a[7])), eps = static_cast<float>(number(a[10]));
     const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
     c10::cuda::OptionalCUDAStreamGuard pool;
-    void *s = c.enter(a[12], pool);
-    Tensor Rout = c.output(a[10], "Rout", R.scalar_type(), {T, D});
-    Tensor H = c.output(a[11], "H", bf, {T, D});
+    void *s = c.enter(a[13], pool);
+    Tensor Rout = c.output(a[11], "Rout", R.scalar_type(), {T, D});
+    Tensor H;
+    if (pre) H = c.output(a[12], "H", bf, {T, D});
     // (slots without columns have no address: any other stands for "slots are given")
     auto at = [&](const Tensor *t) { return !t ? nullptr : t->numel() > 0 ? t->data_ptr() : R.data_ptr(); };
     c.check(unlocked([&] {
       return swiglu_residual_norm(Z.data_ptr(), static_cast<const int32_t *>(at(slots)),
                                   static_cast<const float *>(at(weights)), R.data_ptr(),
                                   R.scalar_type() == ScalarType::Float, post, at(gamma[0]), at(gate), stride,
-                                  scale, at(gamma[1]), eps, Rout.data_ptr(), H.data_ptr(), T, P, k, D, s);
+                                  scale, at(gamma[1]), eps, Rout.data_ptr(), pre ? H.data_ptr() : nullptr, T, P, k, D, s);
     }));
     PyObject *r = PyTuple_New(2);
     if (!r) throw Refused();
     PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(Rout)));
+    // (an undefined tensor is None)
     PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(H)));
     return r;
   });

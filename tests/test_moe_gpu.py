@@ -636,6 +636,25 @@ def test_norm_without_the_second_norm(sg, T, post):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("T", [0, 9, 2000])
+@pytest.mark.parametrize("post", [True, False])
+def test_norm_without_h_from_python(sg, T, post):
+    """pre_norm=False: R' as with it, and no H."""
+    gen = _gen("noh")
+    Z, R = (torch.randn(T, 520, generator=gen).to(BF).to(DEV) for _ in range(2))
+    gp = (1 + 0.2 * torch.randn(520, generator=gen)).to(BF).to(DEV) if post else None
+    want, _ = sg.swiglu_residual_norm(Z, R, post_norm=post, gamma_post=gp, residual_scale=0.5)
+    Ro, H = sg.swiglu_residual_norm(Z, R, post_norm=post, gamma_post=gp, residual_scale=0.5, pre_norm=False)
+    _status(sg)
+    assert H is None and torch.equal(Ro, want)
+    Ro, H = sg.swiglu_residual_norm(Z, R, post_norm=post, gamma_post=gp, residual_scale=0.5, pre_norm=False, Rout=R)
+    assert H is None and Ro is R and torch.equal(R, want)
+    with pytest.raises(ValueError, match="gamma_pre without pre_norm"):
+        sg.swiglu_residual_norm(Z, R, gamma_pre=want.new_ones(520), pre_norm=False)
+    with pytest.raises(ValueError, match="H without pre_norm"):
+        sg.swiglu_residual_norm(Z, R, H=torch.empty_like(Z), pre_norm=False)
+
+
 def test_no_rows_and_no_choices(sg):
     # rows that name nothing at all, of a matrix with rows
     A = torch.ones(5, 16, dtype=BF, device=DEV)
