@@ -339,6 +339,39 @@ def test_grouped_few_units_share_k(sg, fused, gather, sizes, NK):
     check_grouped(sg, fused, sizes, *NK, T=29 if gather else None)
 
 
+@FORMS
+@pytest.mark.parametrize("gather", [True, False], ids=["rows", "dense"])
+@pytest.mark.parametrize("E,rows_each,N,K", [(1024, 2, 1024, 24), (16, 1300, 8192, 40)], ids=["short", "long"])
+def test_grouped_ring_of_units_wraps(sg, fused, gather, E, rows_each, N, K):
+    """More than 64 units a pair (107, and 75 to 82), so that each half of the ring
+    of units is filled again, in tiles of up to 128 rows and of up to 256."""
+    gen = _gen("ringwrap", fused, gather, E)
+    N = N if fused else 2 * N
+    sizes = [int(v) for v in torch.randint(rows_each // 2, rows_each * 3 // 2 + 1, (E,), generator=gen)]
+    offsets = [0]
+    for n in sizes:
+        offsets.append(offsets[-1] + n)
+    P, T = offsets[-1], 400 if gather else offsets[-1]
+    A = torch.randn(T, K, generator=gen).to(BF)
+    Ws = [(torch.randn(E, K, N, generator=gen) / math.sqrt(K)).to(BF) for _ in range(2 if fused else 1)]
+    rows = torch.randint(0, T, (P,), generator=gen) if gather else None
+    off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    rd = None if rows is None else rows.int().to(DEV)
+    fn = sg.swiglu_fused_grouped if fused else sg.swiglu_linear_grouped
+    Y = fn(A.to(DEV), *[W.to(DEV) for W in Ws], off, rd, torch.full((P, N), math.nan, dtype=BF, device=DEV))
+    _status(sg)
+    assert not torch.isnan(Y).any()
+    got = Y.cpu()
+    for e in range(0, E, max(1, E // 100)):
+        a, b = offsets[e], offsets[e + 1]
+        if a == b:
+            continue
+        pick = torch.arange(a, b)[torch.randperm(b - a, generator=gen)[:24]]
+        x = A[pick if rows is None else rows[pick]]
+        ref, tol = grouped_ref(x, [W[e:e + 1] for W in Ws], [0, len(pick)], None)
+        assert ((got[pick].double() - ref).abs() <= tol).all(), e
+
+
 def test_grouped_many_long_units_within_a_short_limit(sg):
     """The finder of the units waits for 32 of them at a time: about 2.7 ms here,
     where one takes 0.08 ms, so a limit of 1.5 ms (a wait may take 1 ms or more) is
