@@ -391,7 +391,8 @@ int swiglu_mlp_noalloc(const void *A, const void *W1, const void *W2, const void
  *   ids, rows, slots : device, int32 [T,k], [T*k], [T,k]  (written)
  *   weights : device, FP32 [T,k]  (written);  offsets : device, int32 [E+1]
  *   workspace : device scratch of at least swiglu_moe_route_workspace_size()
- *       bytes (0 for a few tokens; may then be NULL), 4-byte aligned
+ *       bytes (0 for a few tokens; may then be NULL; 0 too for sizes that the
+ *       call refuses), 4-byte aligned
  * 1 <= k <= min(E, 32), E <= 1024, T * k < 2^31.  Every pointer aligned to its
  * element; no output overlaps another buffer.  T = 0 zeroes offsets.
  */

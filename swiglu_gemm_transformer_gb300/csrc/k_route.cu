@@ -368,6 +368,11 @@ int block_tokens(int64_t T) {
   return static_cast<int>(std::min<int64_t>(std::max<int64_t>(n, 32), kBlockTokens));
 }
 
+// Sizes that the call takes (places and offsets are 32-bit).
+bool supported(int64_t T, int64_t E, int64_t k) {
+  return E <= kMaxE && k <= kMaxK && T <= ((int64_t(1) << 31) - 1) / k;
+}
+
 template <int LPT, int EPL>
 cudaError_t launch_route(bool fp32, const RouteParams &p, cudaStream_t s) {
   // warps: as many as there are groups of tokens and counters for
@@ -390,7 +395,7 @@ cudaError_t launch_route(bool fp32, const RouteParams &p, cudaStream_t s) {
 
 extern "C" uint64_t swiglu_moe_route_workspace_size(int64_t T, int64_t E, int64_t k) {
   using namespace swiglu;
-  if (T <= kOneTokens || E < 1 || k < 1) return 0;
+  if (T <= kOneTokens || E < 1 || k < 1 || !supported(T, E, k)) return 0;
   const int n = block_tokens(T);
   return uint64_t((T + n - 1) / n) * E * 4;
 }
@@ -403,8 +408,7 @@ extern "C" int swiglu_moe_route(const void *logits, int32_t logits_fp32, int32_t
   if (T < 0 || E < 1 || k < 1 || k > E || (logits_fp32 != 0 && logits_fp32 != 1) ||
       (renormalize != 0 && renormalize != 1) || !std::isfinite(scale))
     return SWIGLU_ERR_INVALID_ARG;
-  const int64_t limit = (int64_t(1) << 31) - 1;
-  if (E > kMaxE || k > kMaxK || T > limit / k) return SWIGLU_ERR_UNSUPPORTED;
+  if (!supported(T, E, k)) return SWIGLU_ERR_UNSUPPORTED;
   if (!offsets || (T > 0 && (!logits || !ids || !weights || !rows || !slots)))
     return SWIGLU_ERR_INVALID_ARG;
   if (!ptr_aligned(logits, logits_fp32 ? 4 : 2) || !ptr_aligned(ids, 4) || !ptr_aligned(weights, 4) ||

@@ -25,6 +25,18 @@ def test_route_workspace_size(lib):
     assert lib.swiglu_moe_route_workspace_size(-5, 64, 8) == 0
 
 
+@pytest.mark.parametrize("T,E_,k", [((1 << 63) - 1, 1, 1), ((1 << 63) - 1, 1 << 62, 1), (1 << 40, 1024, 32), (1 << 26, 64, 33),
+                                    (4096, 1025, 8), (4096, 1 << 62, 8), (1 << 31, 8, 1)])
+def test_route_workspace_size_of_calls_that_are_refused(lib, T, E_, k):
+    assert lib.swiglu_moe_route_workspace_size(T, E_, k) == 0
+    assert _route(lib, T=T, E_=E_, k=k) == (INV if k > E_ else UNS)
+
+
+def test_route_workspace_size_of_the_most_tokens(lib):
+    T = (1 << 31) - 1
+    assert lib.swiglu_moe_route_workspace_size(T, 1024, 1) == -(-T // 128) * 1024 * 4
+
+
 def _route(lib, logits=A, fp32=0, renorm=0, scale=1.0, ids=B, weights=C, offsets=D, rows=E, slots=F,
            T=16, E_=64, k=8, ws=None, nbytes=0):
     return lib.swiglu_moe_route(logits, fp32, renorm, scale, ids, weights, offsets, rows, slots, T, E_, k,
