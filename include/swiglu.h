@@ -421,8 +421,9 @@ int swiglu_moe_route(const void *logits, int32_t logits_fp32, int32_t renormaliz
  *       offsets[E] on are left as they are
  * Groups may be empty or of any size.  E <= 1024, P and N below 2^31 - 256,
  * K and N multiples of 8, K * N < 2^39, pointers 16-byte aligned (offsets and
- * rows 4-byte); Y must not overlap an input.  K = 0 or T = 0 makes every product zero: Y is filled
- * with zeros.  P = 0 or N = 0 enqueues nothing.
+ * rows 4-byte); Y must not overlap an input.  K = 0 or T = 0 makes every product
+ * zero: all of Y is filled with zeros, places of no expert too.  P = 0 or N = 0
+ * enqueues nothing.
  */
 int swiglu_fused_grouped(const void *A, const void *W1, const void *W2, const int32_t *offsets,
                          const int32_t *rows, void *Y, int64_t T, int64_t P, int64_t E, int64_t N,

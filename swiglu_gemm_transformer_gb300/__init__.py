@@ -633,7 +633,7 @@ def swiglu_fused_grouped(A, W1, W2, offsets, rows=None, Y=None, *, stream=None):
     for the places p in [offsets[e], offsets[e+1]) of expert e; W1/W2 [E,K,N].
 
     Places that belong to no expert are left as they are (uninitialised where
-    Y is allocated here)."""
+    Y is allocated here); with K = 0 or no rows in A all of Y is zeros."""
     if W2 is None:
         raise TypeError("W2 must be a torch.Tensor")
     return _native().grouped(A, W1, W2, offsets, rows, Y, stream)
@@ -642,7 +642,7 @@ def swiglu_fused_grouped(A, W1, W2, offsets, rows=None, Y=None, *, stream=None):
 def swiglu_linear_grouped(X, W, offsets, rows=None, Z=None, *, stream=None):
     """Z[p] = x @ W[e], x = X[rows[p]] (X[p] without rows), for the places p in
     [offsets[e], offsets[e+1]) of expert e; W [E,K,N].  Places that belong to no
-    expert are left as they are."""
+    expert are left as they are; with K = 0 or no rows in X all of Z is zeros."""
     return _native().grouped(X, W, None, offsets, rows, Z, stream)
 
 

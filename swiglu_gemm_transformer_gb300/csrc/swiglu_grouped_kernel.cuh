@@ -32,8 +32,9 @@
 //     of 32 rows.  Several warps issue them, one thread each, chosen with
 //     elect.sync: issued by lane 0 of one warp they took about 50 ns apiece
 //     (gate/up with rows at 64 experts x 1024 rows, K = 2048, N = 1024: 1118 us;
-//     rows copied with cp.async instead 374 us; eight warps like this 326 us, four
-//     366 us, sixteen 320 us);
+//     rows copied with cp.async instead 374 us; four warps like this 366 us, eight
+//     320 us, sixteen 313 us, dense rows 298 us: bursts of ten calls.  Back to
+//     back, under the power cap, eight 371, sixteen 365, dense 346 us);
 //   * accumulators are double-buffered in TMEM (NT columns each).
 // Unit schedule: every CTA reads `offsets`, counts the row tiles of each
 // expert, and the pairs take the units (expert, row tile, column tile) in
@@ -104,9 +105,12 @@ struct GroupedCfg {
   static constexpr int PRODUCER_WARP = EPI_WARPS;
   static constexpr int MMA_WARP = EPI_WARPS + 1;
   static constexpr int ROW_WARP = EPI_WARPS + 2;  // first of the warps that load rows
-  // 16 where a stage takes 32 gathers per CTA (64 experts x 1024 rows, K = 2048:
-  // 340 us, with 8 warps 347), 8 where it takes 16 (one token's 8 experts: 11.2
-  // us, with 16 warps 12.0); the linear form's rows are dense
+  // 16 where a stage takes 32 gathers per CTA (8192 tokens, 8 of 64 experts, K =
+  // 2048, ragged groups: 335 us, with 8 warps 343, in bursts), 8 where it takes 16
+  // (one token's 8 experts 14.3 us, with 16 warps 14.6; weights in L2 10.9 and
+  // 11.6; 61 tokens 70.7 and 71.3).  The linear form always has 8: a block's down
+  // product has dense rows, and with `rows` it is 8 % slower (8192 tokens, 64
+  // experts, K = 1024, N = 2048: 212 us against 197).
   static constexpr int ROW_WARPS = FUSED && NT == 256 ? 16 : 8;
   static constexpr int UNIT_WARP = ROW_WARP + ROW_WARPS;
   static constexpr int THREADS = 32 * (UNIT_WARP + 1);
