@@ -403,6 +403,36 @@ int swiglu_moe_route(const void *logits, int32_t logits_fp32, int32_t renormaliz
                      uint64_t workspace_bytes, void *stream);
 
 /*
+ * The router by scores: as swiglu_moe_route, with the choice by
+ *     s[t,e] = softmax over e of logits[t,:] (score = 0), or
+ *              1 / (1 + exp(-logits[t,e]))   (score = 1)
+ *     c[t,e] = s[t,e] + bias[e]              (bias NULL: zero)
+ * among the experts of the best groups.  The E experts form `groups` groups of
+ * neighbours; a group's value is its largest c (group_best = 1), or its two
+ * largest added (2; its largest where it has one expert left), and the
+ * kept_groups groups of the largest value are kept (ties: the lowest number).
+ *     ids[t,j]     : expert of the j-th largest c in them (ties: the lowest)
+ *     weights[t,j] : scale * s (without the bias), the chosen s divided by
+ *                    their sum where renormalize = 1 (zeros where that is 0)
+ * The choice is that of the exact values: without a bias the order of c is the
+ * logits'; sums of a score and a bias, or of two scores, are told apart in FP64
+ * where FP32 cannot.  An expert whose logit or bias is -inf is never chosen, a
+ * group without others not kept; where fewer than k are left, the choices end
+ * as in swiglu_moe_route.  A NaN score ranks above every number and makes
+ * weights NaN (a NaN or +inf among softmax's logits does it for its token).
+ *   bias : device, FP32 [E], or NULL  (read); others as in swiglu_moe_route,
+ *       the workspace with swiglu_moe_route_workspace_size() bytes
+ * groups a power of two up to 32 that divides E; 1 <= kept_groups <= groups;
+ * 1 <= k <= min(kept_groups * E / groups, 32); others as in swiglu_moe_route.
+ */
+int swiglu_moe_route_scored(const void *logits, int32_t logits_fp32, int32_t score,
+                            const float *bias, int32_t groups, int32_t kept_groups,
+                            int32_t group_best, int32_t renormalize, float scale, int32_t *ids,
+                            float *weights, int32_t *offsets, int32_t *rows, int32_t *slots,
+                            int64_t T, int64_t E, int64_t k, void *workspace,
+                            uint64_t workspace_bytes, void *stream);
+
+/*
  * Products grouped by expert: the places [offsets[e], offsets[e+1]) belong to
  * expert e, and
  *     swiglu_fused_grouped :  Y[p] = SiLU(a W1[e]) (.) (a W2[e])
@@ -431,6 +461,58 @@ int swiglu_fused_grouped(const void *A, const void *W1, const void *W2, const in
 int swiglu_linear_grouped(const void *X, const void *W, const int32_t *offsets,
                           const int32_t *rows, void *Z, int64_t T, int64_t P, int64_t E, int64_t N,
                           int64_t K, void *stream);
+
+/*
+ * Symmetric 8-bit quantisation by rows: activations by token, or weights
+ * [N,K] (K-major, the transpose of this library's BF16 weights) by output
+ * channel.
+ *     m[r] = max over k of |X[r,k]|,   scale[r] = m[r] / 127
+ *     Q[r,k] = the integer nearest to the exact 127 X[r,k] / m[r] (halves to
+ *              even), in [-127, 127]
+ * A row of zeros has scale 0 and codes 0; a row with a NaN or an infinity has
+ * scale NaN and codes 0, so that its products are NaN.
+ *   X     : device, [R,K], BF16 (x_fp32 = 0) or FP32 (1)  (read)
+ *   Q     : device, int8 [R,K]  (written);  scale : device, FP32 [R]  (written)
+ * K a multiple of 8, X 16-byte, Q 8-byte and scale 4-byte aligned; no output
+ * overlaps another buffer.  R = 0 enqueues nothing, K = 0 zeroes scale.
+ */
+int swiglu_quant_int8(const void *X, int32_t x_fp32, void *Q, float *scale, int64_t R, int64_t K,
+                      void *stream);
+
+/*
+ * Products in 8-bit integers with a scale for each row and each output
+ * channel:
+ *     swiglu_linear_int8: Z[m,n] = x_scale[m] w_scale[n] sum_k X[m,k] W[n,k]
+ *     swiglu_fused_int8 : Y[m,n] = SiLU(g) u,  g and u so with W1, s1 and W2, s2
+ * and the same grouped by expert, with offsets and rows as in
+ * swiglu_fused_grouped: places p in [offsets[e], offsets[e+1]) take expert e's
+ * matrices and scales and the row rows[p] (or p) with its scale.
+ *   A, X          : device, int8 [M,K] (grouped: [T,K])  (read)
+ *   a_scale, x_scale : device, FP32 [M] ([T])  (read)
+ *   W1, W2, W     : device, int8 [N,K] ([E,N,K]), K-major  (read)
+ *   s1, s2, w_scale : device, FP32 [N] ([E,N])  (read)
+ *   Y, Z          : device, BF16 [M,N] ([P,N])  (written)
+ * All 256 codes are allowed.  Sums of products are exact below 2^24 and carry
+ * FP32's rounding beyond (K up to 1024 never reaches it); scales are applied
+ * in FP32, one rounding to BF16.  Equal calls give equal bits.
+ * K a multiple of 16 below 2^22, N a multiple of 8, N * K < 2^40; A, W and Y
+ * 16-byte aligned, scales 4-byte; Y overlaps no input; the rest as in
+ * swiglu_fused_grouped (M or P = 0 enqueues nothing, K = 0 or T = 0 fills Y
+ * with zeros, a row number outside [0, T) gives a row of zeros).
+ */
+int swiglu_linear_int8(const void *X, const float *x_scale, const void *W, const float *w_scale,
+                       void *Z, int64_t M, int64_t N, int64_t K, void *stream);
+int swiglu_fused_int8(const void *A, const float *a_scale, const void *W1, const float *s1,
+                      const void *W2, const float *s2, void *Y, int64_t M, int64_t N, int64_t K,
+                      void *stream);
+int swiglu_linear_grouped_int8(const void *X, const float *x_scale, const void *W,
+                               const float *w_scale, const int32_t *offsets, const int32_t *rows,
+                               void *Z, int64_t T, int64_t P, int64_t E, int64_t N, int64_t K,
+                               void *stream);
+int swiglu_fused_grouped_int8(const void *A, const float *a_scale, const void *W1, const float *s1,
+                              const void *W2, const float *s2, const int32_t *offsets,
+                              const int32_t *rows, void *Y, int64_t T, int64_t P, int64_t E,
+                              int64_t N, int64_t K, void *stream);
 
 /*
  * The end of a block: the join of the experts' rows, the norm after the

@@ -58,8 +58,14 @@ EXPORTS = {
     "swiglu_mlp_noalloc": ("ppppp p lll p", ctypes.c_int),
     "swiglu_moe_route_workspace_size": ("lll", ctypes.c_uint64),
     "swiglu_moe_route": ("p ii f ppppp lll pQ p", ctypes.c_int),
+    "swiglu_moe_route_scored": ("p i i p iii i f ppppp lll pQ p", ctypes.c_int),
     "swiglu_fused_grouped": ("ppp pp p lllll p", ctypes.c_int),
     "swiglu_linear_grouped": ("pp pp p lllll p", ctypes.c_int),
+    "swiglu_quant_int8": ("p i pp ll p", ctypes.c_int),
+    "swiglu_linear_int8": ("pp pp p lll p", ctypes.c_int),
+    "swiglu_fused_int8": ("pp pp pp p lll p", ctypes.c_int),
+    "swiglu_linear_grouped_int8": ("pp pp pp p lllll p", ctypes.c_int),
+    "swiglu_fused_grouped_int8": ("pp pp pp pp p lllll p", ctypes.c_int),
     "swiglu_residual_norm": ("ppp p ii pp l f p f pp llll p", ctypes.c_int),
     "swiglu_select_variant": ("lll i", ctypes.c_int),
     "swiglu_select_weight_kernel": ("ll", ctypes.c_int),
@@ -628,6 +634,25 @@ def swiglu_moe_route(logits, k: int, *, renormalize: bool = False, scale: float 
                                          workspace, stream))
 
 
+def swiglu_moe_route_scored(logits, k: int, *, score: str = "sigmoid", bias=None, groups: int = 1,
+                            kept_groups: int | None = None, group_best: int = 2, renormalize: bool = True,
+                            scale: float = 1.0, ids=None, weights=None, offsets=None, rows=None, slots=None,
+                            workspace=None, stream=None):
+    """swiglu_moe_route with the choice by scores: s = sigmoid(logits) or
+    softmax(logits) (`score`), c = s + bias (fp32 [E] or None), the k largest c
+    among the experts of the `kept_groups` best of `groups` groups of neighbours
+    (all without it).  A group's value is its largest c (group_best=1) or its
+    two largest added (2).  The weights are scale * s, the chosen s divided by
+    their sum with `renormalize`.  An expert whose logit or bias is -inf is never
+    chosen.  Returns MoeRoute."""
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return MoeRoute(*_native().moe_route_scored(logits, k, score == "sigmoid", bias, groups,
+                                                groups if kept_groups is None else kept_groups, group_best,
+                                                renormalize, scale, ids, weights, offsets, rows, slots, workspace,
+                                                stream))
+
+
 def swiglu_fused_grouped(A, W1, W2, offsets, rows=None, Y=None, *, stream=None):
     """Y[p] = SiLU(a @ W1[e]) * (a @ W2[e]), a = A[rows[p]] (A[p] without rows),
     for the places p in [offsets[e], offsets[e+1]) of expert e; W1/W2 [E,K,N].
@@ -644,6 +669,47 @@ def swiglu_linear_grouped(X, W, offsets, rows=None, Z=None, *, stream=None):
     [offsets[e], offsets[e+1]) of expert e; W [E,K,N].  Places that belong to no
     expert are left as they are; with K = 0 or no rows in X all of Z is zeros."""
     return _native().grouped(X, W, None, offsets, rows, Z, stream)
+
+
+def swiglu_quant_int8(X, Q=None, scale=None, *, stream=None):
+    """8-bit codes of the rows of X [...,K] (bf16 or fp32, 2-D or 3-D); returns
+    (Q int8 like X, scale fp32 [...]): scale = max|row| / 127, Q = the nearest
+    integer to 127 x / max|row|.  Rows are a token's activations, or an output
+    channel's weights ([N,K] or [E,N,K])."""
+    return _native().quant_int8(X, Q, scale, stream)
+
+
+def swiglu_linear_int8(X, x_scale, W, w_scale, Z=None, *, stream=None):
+    """Z = (X @ W.T) * x_scale[:,None] * w_scale; X int8 [M,K], W int8 [N,K]
+    (K-major), scales fp32 [M] and [N], Z bf16 [M,N]."""
+    return _native().int8_product(X, x_scale, W, w_scale, None, None, None, None, Z, stream)
+
+
+def swiglu_fused_int8(A, a_scale, W1, s1, W2, s2, Y=None, *, stream=None):
+    """Y = SiLU(g) * u with g = (A @ W1.T) * a_scale[:,None] * s1, u so with W2
+    and s2; A int8 [M,K], W1/W2 int8 [N,K] (K-major), scales fp32, Y bf16 [M,N]."""
+    if W2 is None:
+        raise TypeError("W2 must be a torch.Tensor")
+    return _native().int8_product(A, a_scale, W1, s1, W2, s2, None, None, Y, stream)
+
+
+def swiglu_linear_grouped_int8(X, x_scale, W, w_scale, offsets, rows=None, Z=None, *, stream=None):
+    """swiglu_linear_int8 for places grouped by expert: Z[p] of the row rows[p]
+    (p without rows) and its scale, with expert e's W [E,N,K] and w_scale [E,N]
+    for p in [offsets[e], offsets[e+1]).  Places of no expert are left as they are."""
+    if offsets is None:
+        raise TypeError("offsets must be a torch.Tensor")
+    return _native().int8_product(X, x_scale, W, w_scale, None, None, offsets, rows, Z, stream)
+
+
+def swiglu_fused_grouped_int8(A, a_scale, W1, s1, W2, s2, offsets, rows=None, Y=None, *, stream=None):
+    """swiglu_fused_int8 for places grouped by expert, with offsets and rows as in
+    swiglu_linear_grouped_int8; W1/W2 int8 [E,N,K], s1/s2 fp32 [E,N]."""
+    if W2 is None:
+        raise TypeError("W2 must be a torch.Tensor")
+    if offsets is None:
+        raise TypeError("offsets must be a torch.Tensor")
+    return _native().int8_product(A, a_scale, W1, s1, W2, s2, offsets, rows, Y, stream)
 
 
 def swiglu_residual_norm(Z, R, *, slots=None, weights=None, post_norm: bool = True, gamma_post=None,

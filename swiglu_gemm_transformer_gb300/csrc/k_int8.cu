@@ -1,0 +1,132 @@
+// k_int8.cu -- launcher and C entry points of the products in 8-bit integers,
+// dense and grouped by expert.
+#include <algorithm>
+
+#include "launch.h"
+#include "swiglu.h"
+#include "swiglu_int8_rows_kernel.cuh"
+
+namespace swiglu {
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+// Places and columns: the last tile's bounds, up to 256 past them, are 32-bit too.
+constexpr int64_t kMaxTiled = kMaxDim - 256;
+constexpr int64_t kMaxK = (int64_t(1) << 22) - 16;  // a lane's sum of 128 * 128 * K / 32
+
+struct Int8Call {
+  const void *A, *W1, *W2;  // W2 == nullptr: the linear form
+  const float *sa, *s1, *s2;
+  bool fused, grouped;
+  const int32_t *offsets, *rows;
+  void *Y;
+  int64_t T, P, E, N, K;
+  void *stream;
+};
+
+template <bool FUSED, int R, int NC>
+cudaError_t launch_rows(Int8RowsParams &p, cudaStream_t s) {
+  constexpr int WARPS = 8;
+  p.col_blocks = int32_t(ceil_div(p.N, WARPS * NC));
+  const int64_t tiles = p.offsets ? std::min(p.E, p.P) + p.P / R : ceil_div(p.P, R);
+  if (tiles * p.col_blocks > kMaxDim) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.col_blocks));
+  cfg.blockDim = dim3(32 * WARPS);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, swiglu_int8_rows_kernel<FUSED, R, NC, WARPS>, p);
+}
+
+int run_int8(const Int8Call &c) {
+  const int64_t T = c.T, P = c.P, E = c.E, N = c.N, K = c.K;
+  if (T < 0 || P < 0 || E < 1 || N < 0 || K < 0) return SWIGLU_ERR_INVALID_ARG;
+  if (!c.rows && T != P) return SWIGLU_ERR_INVALID_ARG;
+  if (T > kMaxDim || P > kMaxTiled || N > kMaxTiled || K > kMaxK || E > kRowsMaxExperts)
+    return SWIGLU_ERR_UNSUPPORTED;
+  if (P == 0 || N == 0) return SWIGLU_OK;
+  // one expert's matrix: the tensor map's largest stride is 2^40 bytes
+  if (uint64_t(N) * uint64_t(K) >= uint64_t(1) << 40) return SWIGLU_ERR_UNSUPPORTED;
+  if (!c.Y || (c.grouped && !c.offsets)) return SWIGLU_ERR_INVALID_ARG;
+  if (K > 0 && (!c.W1 || !c.s1 || (c.fused && (!c.W2 || !c.s2)) || (T > 0 && (!c.A || !c.sa))))
+    return SWIGLU_ERR_INVALID_ARG;
+  if (!ptr_aligned(c.Y, 16) || !ptr_aligned(c.offsets, 4) || !ptr_aligned(c.rows, 4))
+    return SWIGLU_ERR_MISALIGNED;
+  if (K > 0 && (!ptr_aligned(c.A, 16) || !ptr_aligned(c.W1, 16) || !ptr_aligned(c.W2, 16) ||
+                !ptr_aligned(c.sa, 4) || !ptr_aligned(c.s1, 4) || !ptr_aligned(c.s2, 4)))
+    return SWIGLU_ERR_MISALIGNED;
+  if (N % 8 != 0 || K % 16 != 0) return SWIGLU_ERR_MISALIGNED;
+  const uint64_t y_bytes = uint64_t(P) * N * 2, w_bytes = uint64_t(E) * N * K, s_bytes = uint64_t(E) * N * 4;
+  if (ranges_overlap(c.Y, y_bytes, c.A, uint64_t(T) * K) || ranges_overlap(c.Y, y_bytes, c.W1, w_bytes) ||
+      ranges_overlap(c.Y, y_bytes, c.W2, w_bytes) || ranges_overlap(c.Y, y_bytes, c.sa, uint64_t(T) * 4) ||
+      ranges_overlap(c.Y, y_bytes, c.s1, s_bytes) || ranges_overlap(c.Y, y_bytes, c.s2, s_bytes) ||
+      ranges_overlap(c.Y, y_bytes, c.offsets, uint64_t(E + 1) * 4) ||
+      ranges_overlap(c.Y, y_bytes, c.rows, uint64_t(P) * 4))
+    return SWIGLU_ERR_INVALID_ARG;
+  uint32_t *err = nullptr;
+  int sms = 0;
+  uint64_t timeout_ns = 0, gen = 0;
+  const int rc = device_info(&err, &sms, &timeout_ns, &gen);
+  if (rc != SWIGLU_OK) return rc;
+  const cudaStream_t s = static_cast<cudaStream_t>(c.stream);
+  // every product is zero: no rows to name, or no K
+  if (K == 0 || T == 0)
+    return cudaMemsetAsync(c.Y, 0, y_bytes, s) == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
+  Int8RowsParams p = {};
+  p.A = static_cast<const int8_t *>(c.A);
+  p.W1 = static_cast<const int8_t *>(c.W1);
+  p.W2 = static_cast<const int8_t *>(c.W2);
+  p.sa = c.sa;
+  p.s1 = c.s1;
+  p.s2 = c.s2;
+  p.offsets = c.offsets;
+  p.rows = c.rows;
+  p.Y = static_cast<__nv_bfloat16 *>(c.Y);
+  p.T = int32_t(T);
+  p.P = int32_t(P);
+  p.E = int32_t(E);
+  p.N = int32_t(N);
+  p.K = K;
+  cudaError_t e;
+  if (P <= E)
+    e = c.fused ? launch_rows<true, 1, 2>(p, s) : launch_rows<false, 1, 4>(p, s);
+  else
+    e = c.fused ? launch_rows<true, 8, 2>(p, s) : launch_rows<false, 8, 4>(p, s);
+  return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace swiglu
+
+extern "C" int swiglu_fused_int8(const void *A, const float *a_scale, const void *W1, const float *s1,
+                                 const void *W2, const float *s2, void *Y, int64_t M, int64_t N,
+                                 int64_t K, void *stream) {
+  return swiglu::run_int8({A, W1, W2, a_scale, s1, s2, true, false, nullptr, nullptr, Y, M, M, 1, N, K, stream});
+}
+
+extern "C" int swiglu_linear_int8(const void *X, const float *x_scale, const void *W, const float *w_scale,
+                                  void *Z, int64_t M, int64_t N, int64_t K, void *stream) {
+  return swiglu::run_int8(
+      {X, W, nullptr, x_scale, w_scale, nullptr, false, false, nullptr, nullptr, Z, M, M, 1, N, K, stream});
+}
+
+extern "C" int swiglu_fused_grouped_int8(const void *A, const float *a_scale, const void *W1,
+                                         const float *s1, const void *W2, const float *s2,
+                                         const int32_t *offsets, const int32_t *rows, void *Y, int64_t T,
+                                         int64_t P, int64_t E, int64_t N, int64_t K, void *stream) {
+  return swiglu::run_int8({A, W1, W2, a_scale, s1, s2, true, true, offsets, rows, Y, T, P, E, N, K, stream});
+}
+
+extern "C" int swiglu_linear_grouped_int8(const void *X, const float *x_scale, const void *W,
+                                          const float *w_scale, const int32_t *offsets,
+                                          const int32_t *rows, void *Z, int64_t T, int64_t P, int64_t E,
+                                          int64_t N, int64_t K, void *stream) {
+  return swiglu::run_int8(
+      {X, W, nullptr, x_scale, w_scale, nullptr, false, true, offsets, rows, Z, T, P, E, N, K, stream});
+}

@@ -33,8 +33,18 @@
 // tokens about a fifth more).  Every block of the second launch reads the counts
 // of all blocks, which is little at such sizes but grows with the square of the
 // tokens: 131072 tokens take 100 us with 64 experts and 292 us with 256.
+//
+// swiglu_moe_route_scored chooses by a score instead of the logit (choose_scored):
+//     s = sigmoid(l) or softmax(l),  c = s + bias,
+// in the `kept` groups of experts whose largest c (or two largest added) are
+// largest.  A warp per token; a group's experts lie in neighbouring lanes.  The
+// choice is that of the exact values: FP32 decides where the values compared
+// lie further apart than their rounding errors together, and a token where two
+// do not is chosen once more in FP64 (without a bias the logits' own order
+// decides, and only sums of two scores are compared).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math_constants.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -66,6 +76,9 @@ struct RouteParams {
   int32_t T, E, k, blocks, block_tokens;
   int32_t renormalize;
   float scale;
+  // scored form only
+  const float *bias;  // [E] or null
+  int32_t sigmoid, fp32, groups, kept, best;
 };
 
 // Unsigned number with the order of the floats; -inf -> 0 (masked), NaN above
@@ -158,6 +171,225 @@ __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t 
   }
 }
 
+__device__ __forceinline__ float logit(const RouteParams &p, bool fp32, int64_t at) {
+  return fp32 ? __ldg(static_cast<const float *>(p.logits) + at)
+              : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[at]);
+}
+
+// order_key in 64 bits.
+__device__ __forceinline__ unsigned long long order_key(double x) {
+  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
+  const unsigned long long k = b ^ ((b >> 63) ? ~0ull : 1ull << 63);
+  return x != x ? ~0ull : x == -CUDART_INF ? 0ull : k;
+}
+
+__device__ __forceinline__ double key_value(unsigned long long key) {
+  const unsigned long long b = key ^ ((key >> 63) ? 1ull << 63 : ~0ull);
+  return key == 0ull ? -CUDART_INF : __longlong_as_double(static_cast<long long>(b));
+}
+
+// The largest (key, lowest expert) of the warp's lanes.
+__device__ __forceinline__ void warp_best(uint32_t &key, int &e) {
+  const uint32_t top = __reduce_max_sync(kAll, key);
+  e = static_cast<int>(__reduce_min_sync(kAll, key == top ? static_cast<unsigned>(e) : 0x7fffffffu));
+  key = top;
+}
+
+__device__ __forceinline__ void warp_best(unsigned long long &key, int &e) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long k = __shfl_xor_sync(kAll, key, o);
+    const int f = __shfl_xor_sync(kAll, e, o);
+    const bool up = k > key || (k == key && f < e);
+    key = up ? k : key;
+    e = up ? f : e;
+  }
+}
+
+__device__ __forceinline__ float score_of(bool sigmoid, float x, float m, float sum) {
+  return sigmoid ? __frcp_rn(1.0f + expf(-x)) : __fdiv_rn(expf(x - m), sum);
+}
+__device__ __forceinline__ double score_of(bool sigmoid, double x, double m, double sum) {
+  return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / sum;
+}
+
+// Largest error of an FP32 score, as a part of the token's largest one.
+// Sigmoid: exp 2 ulp, sum and reciprocal half an ulp each.  Softmax: up to 32
+// additions in a lane and five across, on top of two exp.
+__device__ __forceinline__ float score_error(bool sigmoid) { return sigmoid ? 0x1p-21f : 0x1p-18f; }
+
+// One token by one warp, in V = float or double: the chosen experts, lane j
+// keeping choice j.  Returns whether V decided every comparison (FP64: always).
+//   lane: group lane / L of L = 32 / groups lanes, experts g E / groups + lane % L + L i
+// The values are read again where they are needed rather than kept: x and b
+// come from L1.
+template <class V, int EPL>
+__device__ __forceinline__ bool choose_exactly(const RouteParams &p, int64_t t, int lane,
+                                               int &my_id, float &my_weight) {
+  const bool sigmoid = p.sigmoid != 0, fp32 = p.fp32 != 0;
+  using Key = decltype(order_key(V()));
+  constexpr bool ROUNDED = sizeof(V) == 4;
+  const int L = 32 / p.groups, size = p.E / p.groups;
+  const int g = lane / L, li = lane % L;
+  const int64_t row = t * p.E;
+  auto expert = [&](int i) { return li + L * i < size ? g * size + li + L * i : -1; };
+  float x[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) x[i] = expert(i) >= 0 ? logit(p, fp32, row + expert(i)) : -INFINITY;
+  V m = 0, sum = 1;
+  float largest = 1.0f;  // bound of the scores
+  if (!sigmoid) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) top = max(top, order_key(x[i]));
+    m = key_value(__reduce_max_sync(kAll, top));
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sum += x[i] == -INFINITY ? V(0) : static_cast<V>(exp(V(x[i]) - m));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    largest = 1.0f / static_cast<float>(sum);
+  }
+  const float err = score_error(sigmoid) * largest;  // of one score
+  auto worth = [&](float xi, int e) -> V {           // s + b, or the logit where no bias is given
+    if (xi == -INFINITY) return V(-INFINITY);
+    return p.bias ? score_of(sigmoid, V(xi), m, sum) + V(__ldg(p.bias + e)) : V(xi);
+  };
+  Key key[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) key[i] = expert(i) >= 0 ? order_key(worth(x[i], expert(i))) : Key(0);
+  bool sure = true;
+  if (p.kept < p.groups) {
+    // the group's two largest
+    Key k1 = 0, k2 = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      k2 = max(k2, min(k1, key[i]));
+      k1 = max(k1, key[i]);
+    }
+    for (int o = 1; o < L; o <<= 1) {
+      const Key j1 = __shfl_xor_sync(kAll, k1, o), j2 = __shfl_xor_sync(kAll, k2, o);
+      k2 = max(min(k1, j1), max(k2, j2));
+      k1 = max(k1, j1);
+    }
+    V v1 = key_value(k1), v2 = key_value(k2);
+    const bool summed = p.best == 2;
+    if (summed && !p.bias) {  // the logits' order, but the scores are added
+      v1 = k1 == 0 ? V(0) : score_of(sigmoid, v1, m, sum);
+      v2 = k2 == 0 ? V(0) : score_of(sigmoid, v2, m, sum);
+    }
+    const V value = summed && k2 != 0 ? v1 + v2 : v1;
+    const Key mine = k1 == 0 ? Key(0) : order_key(value);
+    const float size12 = fmaxf(fabsf(float(v1)), k2 != 0 ? fabsf(float(v2)) : 0.0f);
+    int rank = 0;
+    for (int h = 0; h < p.groups; ++h) {
+      const Key other = __shfl_sync(kAll, mine, h * L);
+      rank += other > mine || (other == mine && h < g);
+    }
+    const bool keep = mine != 0 && rank < p.kept;
+    if (ROUNDED && (p.bias || summed)) {
+      const unsigned kept = __ballot_sync(kAll, keep);
+      for (int h = 0; h < p.groups; ++h) {
+        const V other = __shfl_sync(kAll, value, h * L);
+        const float s12 = fmaxf(size12, __shfl_sync(kAll, size12, h * L));
+        const bool there = __shfl_sync(kAll, mine, h * L) != 0;
+        if (mine != 0 && there && keep != ((kept >> (h * L)) & 1u) &&
+            fabsf(float(value - other)) <= 4.0f * err + 0x1p-21f * s12)
+          sure = false;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = keep ? key[i] : Key(0);
+  }
+  Key my_key = 0, next_key = 0;
+  int next_id = -1;
+  my_id = -1;
+  const int rounds = ROUNDED && p.bias ? p.k + 1 : p.k;
+  for (int j = 0; j < rounds; ++j) {
+    Key b = 0;
+    int e = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const bool up = key[i] > b;
+      b = up ? key[i] : b;
+      e = up ? g * size + li + L * i : e;
+    }
+    warp_best(b, e);
+    if (b == 0) e = -1;
+    my_key = lane == j ? b : my_key;
+    my_id = lane == j ? e : my_id;
+    next_key = b;
+    next_id = e;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = g * size + li + L * i == e ? Key(0) : key[i];
+  }
+  if (lane >= p.k) my_id = -1;
+  const float mx = my_id >= 0 ? logit(p, fp32, row + my_id) : -INFINITY;
+  if (ROUNDED && p.bias) {
+    // each choice against the next one; equal logits with equal biases are a
+    // true tie, which the expert's number has settled
+    const float mb = my_id >= 0 ? __ldg(p.bias + my_id) : 0.0f;
+    const float nx = next_id >= 0 ? logit(p, fp32, row + next_id) : -INFINITY;
+    const float nb = next_id >= 0 ? __ldg(p.bias + next_id) : 0.0f;
+    Key ok = __shfl_down_sync(kAll, my_key, 1);
+    float ox = __shfl_down_sync(kAll, mx, 1), ob = __shfl_down_sync(kAll, mb, 1);
+    if (lane == p.k - 1) ok = next_key, ox = nx, ob = nb;
+    if (lane < p.k && my_key != 0 && ok != 0 && !(ox == mx && ob == mb)) {
+      const float a = float(key_value(my_key)), b = float(key_value(ok));
+      if (a - b <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(a), fabsf(b))) sure = false;
+    }
+  }
+  V w = my_id >= 0 ? score_of(sigmoid, V(mx), m, sum) : V(0);
+  if (p.renormalize) {
+    V total = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+    if (ROUNDED && my_id >= 0 && total < V(1e-30)) sure = false;  // near underflow
+    w = total > V(0) || total != total ? w / total : V(0);
+  }
+  my_weight = my_id >= 0 ? static_cast<float>(V(p.scale) * w) : 0.0f;
+  return __all_sync(kAll, sure);
+}
+
+template <int EPL>
+__device__ __noinline__ void choose_in_64(const RouteParams &p, int64_t t, int lane, int &id, float &weight) {
+  choose_exactly<double, EPL>(p, t, lane, id, weight);
+}
+
+// choose() by scores: the token t by a whole warp.
+template <int EPL>
+__device__ __forceinline__ void choose_scored(const RouteParams &p, int64_t t, int64_t end, int lane,
+                                              uint16_t *ids16) {
+  if (t >= end) return;
+  int id;
+  float weight;
+  if (!choose_exactly<float, EPL>(p, t, lane, id, weight)) choose_in_64<EPL>(p, t, lane, id, weight);
+  if (lane < p.k) {
+    p.ids[t * p.k + lane] = id;
+    p.weights[t * p.k + lane] = weight;
+    ids16[lane] = static_cast<uint16_t>(id);
+  }
+}
+
+// How a block chooses: by the logits, LPT lanes per token,
+template <int LPT, int EPL, bool FP32>
+struct ByLogit {
+  static constexpr int LANES = LPT;
+  __device__ static __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane,
+                                                uint16_t *ids16) {
+    swiglu::choose<LPT, EPL, FP32>(p, t, end, lane, ids16);
+  }
+};
+// or by scores.
+template <int EPL>
+struct ByScore {
+  static constexpr int LANES = 32;
+  __device__ static __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane,
+                                                uint16_t *ids16) {
+    choose_scored<EPL>(p, t, end, lane, ids16);
+  }
+};
+
 // Walks this warp's entries [i0, i1) of the block, 32 at a time, adding them to
 // cnt[expert]; number(i, e, before) gets each entry's expert and the entries
 // counted before it (e = 0xffff: none).
@@ -222,8 +454,8 @@ __device__ __forceinline__ int scan_experts(RouteSmem &sm, int E, int32_t *offse
 
 // One block of tokens; ONE: a block of the only cluster, which does the whole
 // call, otherwise the first pass of it.
-template <int LPT, int EPL, bool FP32, bool ONE>
-__global__ void __launch_bounds__(1024, 1) route_choose_kernel(const RouteParams p) {
+template <class How, bool ONE>
+__global__ void __launch_bounds__(1024, 1) route_choose_kernel(const __grid_constant__ RouteParams p) {
   __shared__ RouteSmem sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int rank = blockIdx.x, ranks = ONE ? gridDim.x : 1;
@@ -235,11 +467,11 @@ __global__ void __launch_bounds__(1024, 1) route_choose_kernel(const RouteParams
   const int64_t b0 = int64_t(blockIdx.x) * tokens;
   const int nt = static_cast<int>(max(int64_t(0), min(int64_t(tokens), p.T - b0)));
   // each warp takes a run of tokens, 32 / LPT at a time
-  constexpr int SIDE = 32 / LPT;
+  constexpr int SIDE = 32 / How::LANES;
   const int per = (nt + warps * SIDE - 1) / (warps * SIDE) * SIDE;
   const int t0 = min(warp * per, nt), t1 = min(t0 + per, nt);
   for (int t = t0; t < t1; t += SIDE)
-    choose<LPT, EPL, FP32>(p, b0 + t + lane / LPT, b0 + t1, lane, sm.ids + (t + lane / LPT) * p.k);
+    How::choose(p, b0 + t + lane / How::LANES, b0 + t1, lane, sm.ids + (t + lane / How::LANES) * p.k);
   __syncwarp();
   walk(sm.ids, t0 * p.k, t1 * p.k, cnt, lane, [](int, unsigned, int) {});
   __syncthreads();
@@ -375,21 +607,64 @@ bool supported(int64_t T, int64_t E, int64_t k) {
   return E <= kMaxE && k <= kMaxK && T <= ((int64_t(1) << 31) - 1) / k;
 }
 
-template <int LPT, int EPL>
-cudaError_t launch_route(bool fp32, const RouteParams &p, cudaStream_t s) {
+template <class How>
+cudaError_t launch_route(const RouteParams &p, cudaStream_t s) {
   // warps: as many as there are groups of tokens and counters for
-  auto warps = [&](int tokens) { return std::min({32, kCounters / p.E, (tokens + 32 / LPT - 1) / (32 / LPT)}); };
+  constexpr int SIDE = 32 / How::LANES;
+  auto warps = [&](int tokens) { return std::min({32, kCounters / p.E, (tokens + SIDE - 1) / SIDE}); };
   if (p.T <= kOneTokens) {
     int blocks = 1;  // a power of two
     while (blocks * kOneBlockTokens < p.T) blocks *= 2;
-    return launch_pdl(fp32 ? route_choose_kernel<LPT, EPL, true, true>
-                           : route_choose_kernel<LPT, EPL, false, true>,
-                      blocks, blocks, 32 * warps(std::min(p.T, kOneBlockTokens)), p, s);
+    return launch_pdl(route_choose_kernel<How, true>, blocks, blocks, 32 * warps(std::min(p.T, kOneBlockTokens)),
+                      p, s);
   }
-  const cudaError_t e = launch_pdl(fp32 ? route_choose_kernel<LPT, EPL, true, false>
-                                        : route_choose_kernel<LPT, EPL, false, false>,
-                                   p.blocks, 1, 32 * warps(p.block_tokens), p, s);
+  const cudaError_t e =
+      launch_pdl(route_choose_kernel<How, false>, p.blocks, 1, 32 * warps(p.block_tokens), p, s);
   return e != cudaSuccess ? e : launch_pdl(route_place_kernel, p.blocks, 1, 1024, p, s);
+}
+
+template <int LPT, int EPL>
+cudaError_t launch_by_logit(bool fp32, const RouteParams &p, cudaStream_t s) {
+  return fp32 ? launch_route<ByLogit<LPT, EPL, true>>(p, s) : launch_route<ByLogit<LPT, EPL, false>>(p, s);
+}
+
+// What the two calls share: the checks but those of the choice, and the launch.
+template <class Launch>
+int run_route(RouteParams p, bool fp32, int64_t T, int64_t E, int64_t k, void *workspace,
+              uint64_t workspace_bytes, void *stream, Launch launch) {
+  if (!supported(T, E, k)) return SWIGLU_ERR_UNSUPPORTED;
+  if (!p.offsets || (T > 0 && (!p.logits || !p.ids || !p.weights || !p.rows || !p.slots)))
+    return SWIGLU_ERR_INVALID_ARG;
+  if (!ptr_aligned(p.logits, fp32 ? 4 : 2) || !ptr_aligned(p.ids, 4) || !ptr_aligned(p.weights, 4) ||
+      !ptr_aligned(p.offsets, 4) || !ptr_aligned(p.rows, 4) || !ptr_aligned(p.slots, 4) ||
+      !ptr_aligned(p.bias, 4) || !ptr_aligned(workspace, 4))
+    return SWIGLU_ERR_MISALIGNED;
+  const uint64_t need = swiglu_moe_route_workspace_size(T, E, k);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SWIGLU_ERR_INVALID_ARG;
+  // no output may overlap the inputs, the workspace or another output
+  const uint64_t n4 = uint64_t(T) * k * 4;
+  const void *ptr[8] = {p.logits, p.bias, p.ids, p.weights, p.rows, p.slots, p.offsets, need ? workspace : nullptr};
+  const uint64_t len[8] = {uint64_t(T) * E * (fp32 ? 4 : 2), uint64_t(E) * 4, n4, n4, n4, n4,
+                           uint64_t(E + 1) * 4, need};
+  for (int i = 2; i < 8; ++i)
+    for (int j = 0; j < i; ++j)
+      if (ranges_overlap(ptr[i], len[i], ptr[j], len[j])) return SWIGLU_ERR_INVALID_ARG;
+  uint32_t *err = nullptr;
+  int sms = 0;
+  uint64_t timeout_ns = 0, gen = 0;
+  int rc = device_info(&err, &sms, &timeout_ns, &gen);
+  if (rc != SWIGLU_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0)
+    return cudaMemsetAsync(p.offsets, 0, uint64_t(E + 1) * 4, s) == cudaSuccess ? SWIGLU_OK
+                                                                                : SWIGLU_ERR_CUDA;
+  p.counts = static_cast<int32_t *>(workspace);
+  p.T = int32_t(T);
+  p.E = int32_t(E);
+  p.k = int32_t(k);
+  p.block_tokens = block_tokens(T);
+  p.blocks = int32_t((T + p.block_tokens - 1) / p.block_tokens);
+  return launch(p, s) == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
 }
 
 }  // namespace
@@ -410,54 +685,61 @@ extern "C" int swiglu_moe_route(const void *logits, int32_t logits_fp32, int32_t
   if (T < 0 || E < 1 || k < 1 || k > E || (logits_fp32 != 0 && logits_fp32 != 1) ||
       (renormalize != 0 && renormalize != 1) || !std::isfinite(scale))
     return SWIGLU_ERR_INVALID_ARG;
-  if (!supported(T, E, k)) return SWIGLU_ERR_UNSUPPORTED;
-  if (!offsets || (T > 0 && (!logits || !ids || !weights || !rows || !slots)))
-    return SWIGLU_ERR_INVALID_ARG;
-  if (!ptr_aligned(logits, logits_fp32 ? 4 : 2) || !ptr_aligned(ids, 4) || !ptr_aligned(weights, 4) ||
-      !ptr_aligned(offsets, 4) || !ptr_aligned(rows, 4) || !ptr_aligned(slots, 4) ||
-      !ptr_aligned(workspace, 4))
-    return SWIGLU_ERR_MISALIGNED;
-  const uint64_t need = swiglu_moe_route_workspace_size(T, E, k);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return SWIGLU_ERR_INVALID_ARG;
-  // no output may overlap the logits, the workspace or another output
-  const uint64_t n4 = uint64_t(T) * k * 4;
-  const void *ptr[7] = {logits, ids, weights, rows, slots, offsets, need ? workspace : nullptr};
-  const uint64_t len[7] = {uint64_t(T) * E * (logits_fp32 ? 4 : 2), n4, n4, n4, n4,
-                           uint64_t(E + 1) * 4, need};
-  for (int i = 0; i < 7; ++i)
-    for (int j = 0; j < i; ++j)
-      if (ranges_overlap(ptr[i], len[i], ptr[j], len[j])) return SWIGLU_ERR_INVALID_ARG;
-  uint32_t *err = nullptr;
-  int sms = 0;
-  uint64_t timeout_ns = 0, gen = 0;
-  int rc = device_info(&err, &sms, &timeout_ns, &gen);
-  if (rc != SWIGLU_OK) return rc;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T == 0)
-    return cudaMemsetAsync(offsets, 0, uint64_t(E + 1) * 4, s) == cudaSuccess ? SWIGLU_OK
-                                                                              : SWIGLU_ERR_CUDA;
-  RouteParams p;
+  RouteParams p = {};
   p.logits = logits;
   p.ids = ids;
   p.weights = weights;
   p.offsets = offsets;
   p.rows = rows;
   p.slots = slots;
-  p.counts = static_cast<int32_t *>(workspace);
-  p.T = int32_t(T);
-  p.E = int32_t(E);
-  p.k = int32_t(k);
-  p.block_tokens = block_tokens(T);
-  p.blocks = int32_t((T + p.block_tokens - 1) / p.block_tokens);
   p.renormalize = renormalize;
   p.scale = scale;
   const bool f = logits_fp32 != 0;
   const int64_t lanes = std::max((E + 7) / 8, k);  // per token
-  const cudaError_t e = lanes <= 4    ? launch_route<4, 8>(f, p, s)
-                        : lanes <= 8  ? launch_route<8, 8>(f, p, s)
-                        : lanes <= 16 ? launch_route<16, 8>(f, p, s)
-                        : E <= 256    ? launch_route<32, 8>(f, p, s)
-                        : E <= 512    ? launch_route<32, 16>(f, p, s)
-                                      : launch_route<32, 32>(f, p, s);
-  return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
+  return run_route(p, f, T, E, k, workspace, workspace_bytes, stream, [=](const RouteParams &q, cudaStream_t s) {
+    return lanes <= 4    ? launch_by_logit<4, 8>(f, q, s)
+           : lanes <= 8  ? launch_by_logit<8, 8>(f, q, s)
+           : lanes <= 16 ? launch_by_logit<16, 8>(f, q, s)
+           : E <= 256    ? launch_by_logit<32, 8>(f, q, s)
+           : E <= 512    ? launch_by_logit<32, 16>(f, q, s)
+                         : launch_by_logit<32, 32>(f, q, s);
+  });
+}
+
+extern "C" int swiglu_moe_route_scored(const void *logits, int32_t logits_fp32, int32_t score,
+                                       const float *bias, int32_t groups, int32_t kept_groups,
+                                       int32_t group_best, int32_t renormalize, float scale,
+                                       int32_t *ids, float *weights, int32_t *offsets, int32_t *rows,
+                                       int32_t *slots, int64_t T, int64_t E, int64_t k, void *workspace,
+                                       uint64_t workspace_bytes, void *stream) {
+  using namespace swiglu;
+  if (T < 0 || E < 1 || k < 1 || (logits_fp32 != 0 && logits_fp32 != 1) || (score != 0 && score != 1) ||
+      (renormalize != 0 && renormalize != 1) || !std::isfinite(scale) || groups < 1 || E % groups != 0 ||
+      kept_groups < 1 || kept_groups > groups || (group_best != 1 && group_best != 2) ||
+      k > E / groups * kept_groups)
+    return SWIGLU_ERR_INVALID_ARG;
+  if (groups > 32 || (groups & (groups - 1)) != 0) return SWIGLU_ERR_UNSUPPORTED;
+  RouteParams p = {};
+  p.logits = logits;
+  p.ids = ids;
+  p.weights = weights;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.slots = slots;
+  p.renormalize = renormalize;
+  p.scale = scale;
+  p.bias = bias;
+  p.groups = groups;
+  p.kept = kept_groups;
+  p.best = group_best;
+  p.sigmoid = score;
+  p.fp32 = logits_fp32;
+  // experts of a lane: a group's lie in 32 / groups lanes
+  const int64_t lanes = 32 / groups, per_lane = (E / groups + lanes - 1) / lanes;
+  return run_route(p, logits_fp32 != 0, T, E, k, workspace, workspace_bytes, stream, [=](const RouteParams &q, cudaStream_t s) {
+    return per_lane <= 2    ? launch_route<ByScore<2>>(q, s)
+           : per_lane <= 8  ? launch_route<ByScore<8>>(q, s)
+           : per_lane <= 16 ? launch_route<ByScore<16>>(q, s)
+                            : launch_route<ByScore<32>>(q, s);
+  });
 }

@@ -31,6 +31,7 @@ const char *type_name(ScalarType t) {
     case ScalarType::BFloat16: return "torch.bfloat16";
     case ScalarType::Float: return "torch.float32";
     case ScalarType::Int: return "torch.int32";
+    case ScalarType::Char: return "torch.int8";
     default: return c10::toString(t);
   }
 }
@@ -82,6 +83,9 @@ struct Call {
     const Tensor &t = tensor(o, what, type, static_cast<int>(shape.size()));
     if (t.sizes() != shape) {
       if (shape.size() == 1) refuse(PyExc_ValueError, "%s must be [%lld]", what, (long long)shape[0]);
+      if (shape.size() == 3)
+        refuse(PyExc_ValueError, "%s must be [%lld, %lld, %lld]", what, (long long)shape[0], (long long)shape[1],
+               (long long)shape[2]);
       refuse(PyExc_ValueError, "%s must be [%lld, %lld]", what, (long long)shape[0], (long long)shape[1]);
     }
     return t;
@@ -162,6 +166,33 @@ PyObject *guarded(F f) {
   END_HANDLE_TH_ERRORS
 }
 
+// The outputs of the two routers, their workspace, and the call: f(outputs, workspace, bytes, stream).
+template <class F>
+PyObject *route(Call &c, int64_t T, int64_t E, int64_t k, PyObject *const *out_args, PyObject *workspace,
+                PyObject *stream, F f) {
+  const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
+  c10::cuda::OptionalCUDAStreamGuard pool;
+  void *s = c.enter(stream, pool);
+  Tensor out[5] = {c.output(out_args[0], "ids", ScalarType::Int, {T, k}),
+                   c.output(out_args[1], "weights", ScalarType::Float, {T, k}),
+                   c.output(out_args[2], "offsets", ScalarType::Int, {E + 1}),
+                   c.output(out_args[3], "rows", ScalarType::Int, {T * k}),
+                   c.output(out_args[4], "slots", ScalarType::Int, {T, k})};
+  uint64_t bytes = swiglu_moe_route_workspace_size(T, E, k);
+  Tensor ws;
+  if (workspace != Py_None) {
+    ws = c.tensor(workspace, "workspace", 1);
+    bytes = ws.nbytes();
+  } else if (bytes > 0) {
+    ws = c.output(Py_None, "workspace", ScalarType::Byte, {static_cast<int64_t>(bytes)});
+  }
+  c.check(unlocked([&] { return f(out, ws.defined() ? ws.data_ptr() : nullptr, bytes, s); }));
+  PyObject *r = PyTuple_New(5);
+  if (!r) throw Refused();
+  for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(std::move(out[i])));
+  return r;
+}
+
 // (logits, k, renormalize, scale, ids, weights, offsets, rows, slots, workspace, stream)
 PyObject *moe_route(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
@@ -171,33 +202,125 @@ PyObject *moe_route(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t T = logits.size(0), E = logits.size(1), k = integer(a[1]);
     if (k < 1 || k > E)
       refuse(PyExc_ValueError, "k must be in [1, %lld], got %lld", (long long)E, (long long)k);
-    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
-    c10::cuda::OptionalCUDAStreamGuard pool;
-    void *s = c.enter(a[10], pool);
-    Tensor out[5] = {c.output(a[4], "ids", ScalarType::Int, {T, k}),
-                     c.output(a[5], "weights", ScalarType::Float, {T, k}),
-                     c.output(a[6], "offsets", ScalarType::Int, {E + 1}),
-                     c.output(a[7], "rows", ScalarType::Int, {T * k}),
-                     c.output(a[8], "slots", ScalarType::Int, {T, k})};
-    uint64_t bytes = swiglu_moe_route_workspace_size(T, E, k);
-    Tensor ws;
-    if (a[9] != Py_None) {
-      ws = c.tensor(a[9], "workspace", 1);
-      bytes = ws.nbytes();
-    } else if (bytes > 0) {
-      ws = c.output(Py_None, "workspace", ScalarType::Byte, {static_cast<int64_t>(bytes)});
-    }
     const bool fp32 = logits.scalar_type() == ScalarType::Float, renorm = truth(a[2]);
     const float scale = static_cast<float>(number(a[3]));
+    return route(c, T, E, k, a + 4, a[9], a[10], [&](const Tensor *out, void *ws, uint64_t bytes, void *s) {
+      return swiglu_moe_route(logits.data_ptr(), fp32, renorm, scale, ptr<int32_t>(out[0]), ptr<float>(out[1]),
+                              ptr<int32_t>(out[2]), ptr<int32_t>(out[3]), ptr<int32_t>(out[4]), T, E, k, ws, bytes,
+                              s);
+    });
+  });
+}
+
+// (logits, k, sigmoid, bias or None, groups, kept_groups, group_best, renormalize, scale, ids, weights, offsets,
+//  rows, slots, workspace, stream)
+PyObject *moe_route_scored(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    if (n != 16) refuse(PyExc_TypeError, "moe_route_scored takes 16 arguments");
+    Call c{"swiglu_moe_route_scored"};
+    const Tensor &logits = c.either(a[0], "logits", 2);
+    const int64_t T = logits.size(0), E = logits.size(1), k = integer(a[1]);
+    const bool sigmoid = truth(a[2]);
+    const float *bias = nullptr;
+    if (a[3] != Py_None) {
+      const Tensor &b = c.tensor(a[3], "bias", ScalarType::Float, 1);
+      if (b.numel() != E) refuse(PyExc_ValueError, "bias must have %lld elements", (long long)E);
+      bias = ptr<float>(b);
+    }
+    const int64_t groups = integer(a[4]), kept = integer(a[5]), best = integer(a[6]);
+    if (groups < 1 || groups > 32 || (groups & (groups - 1)) != 0 || E % groups != 0)
+      refuse(PyExc_ValueError, "groups must be a power of two up to 32 that divides %lld experts, got %lld",
+             (long long)E, (long long)groups);
+    if (kept < 1 || kept > groups)
+      refuse(PyExc_ValueError, "kept_groups must be in [1, %lld], got %lld", (long long)groups, (long long)kept);
+    if (best != 1 && best != 2) refuse(PyExc_ValueError, "group_best must be 1 or 2, got %lld", (long long)best);
+    if (k < 1 || k > E / groups * kept)
+      refuse(PyExc_ValueError, "k must be in [1, %lld], got %lld", (long long)(E / groups * kept), (long long)k);
+    const bool fp32 = logits.scalar_type() == ScalarType::Float, renorm = truth(a[7]);
+    const float scale = static_cast<float>(number(a[8]));
+    return route(c, T, E, k, a + 9, a[14], a[15], [&](const Tensor *out, void *ws, uint64_t bytes, void *s) {
+      return swiglu_moe_route_scored(logits.data_ptr(), fp32, sigmoid, bias, static_cast<int32_t>(groups),
+                                     static_cast<int32_t>(kept), static_cast<int32_t>(best), renorm, scale,
+                                     ptr<int32_t>(out[0]), ptr<float>(out[1]), ptr<int32_t>(out[2]),
+                                     ptr<int32_t>(out[3]), ptr<int32_t>(out[4]), T, E, k, ws, bytes, s);
+    });
+  });
+}
+
+// (X, Q or None, scale or None, stream)
+PyObject *quant_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    if (n != 4) refuse(PyExc_TypeError, "quant_int8 takes 4 arguments");
+    Call c{"swiglu_quant_int8"};
+    const int dims = THPVariable_Check(a[0]) && THPVariable_Unpack(a[0]).dim() == 3 ? 3 : 2;
+    const Tensor &X = c.either(a[0], "X", dims);
+    const int64_t K = X.size(dims - 1);
+    int64_t R = 1;
+    for (int i = 0; i < dims - 1; ++i) R *= X.size(i);
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
+    c10::cuda::OptionalCUDAStreamGuard pool;
+    void *s = c.enter(a[3], pool);
+    Tensor out[2] = {c.output(a[1], "Q", ScalarType::Char, X.sizes()),
+                     c.output(a[2], "scale", ScalarType::Float, X.sizes().slice(0, dims - 1))};
     c.check(unlocked([&] {
-      return swiglu_moe_route(logits.data_ptr(), fp32, renorm, scale, ptr<int32_t>(out[0]),
-                              ptr<float>(out[1]), ptr<int32_t>(out[2]), ptr<int32_t>(out[3]),
-                              ptr<int32_t>(out[4]), T, E, k, ws.defined() ? ws.data_ptr() : nullptr, bytes, s);
+      return swiglu_quant_int8(X.data_ptr(), X.scalar_type() == ScalarType::Float, out[0].data_ptr(),
+                               ptr<float>(out[1]), R, K, s);
     }));
-    PyObject *r = PyTuple_New(5);
+    PyObject *r = PyTuple_New(2);
     if (!r) throw Refused();
-    for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(std::move(out[i])));
+    for (int i = 0; i < 2; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(std::move(out[i])));
     return r;
+  });
+}
+
+// (A, a_scale, W1, s1, W2 or None, s2 or None, offsets or None, rows or None, Y or None, stream)
+PyObject *int8_product(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject * {
+    if (n != 10) refuse(PyExc_TypeError, "int8_product takes 10 arguments");
+    const bool fused = a[4] != Py_None, grouped = a[6] != Py_None;
+    Call c{grouped ? (fused ? "swiglu_fused_grouped_int8" : "swiglu_linear_grouped_int8")
+                   : (fused ? "swiglu_fused_int8" : "swiglu_linear_int8")};
+    const auto i8 = ScalarType::Char, f32 = ScalarType::Float;
+    const int dims = grouped ? 3 : 2;
+    const Tensor &A = c.tensor(a[0], fused ? "A" : "X", i8, 2);
+    const Tensor &sa = c.tensor(a[1], fused ? "a_scale" : "x_scale", f32, 1);
+    const Tensor &W1 = c.tensor(a[2], fused ? "W1" : "W", i8, dims);
+    const Tensor &s1 = c.tensor(a[3], fused ? "s1" : "w_scale", f32, dims - 1);
+    const Tensor &W2 = fused ? c.tensor(a[4], "W2", i8, dims) : W1;
+    const Tensor &s2 = fused ? c.tensor(a[5], "s2", f32, dims - 1) : s1;
+    if (W2.sizes() != W1.sizes()) refuse(PyExc_ValueError, "W1 and W2 must match in shape");
+    const int64_t T = A.size(0), K = A.size(1), E = grouped ? W1.size(0) : 1, N = W1.size(dims - 2);
+    if (W1.size(dims - 1) != K)
+      refuse(PyExc_ValueError, "shape mismatch: rows of %lld, weights of %lld", (long long)K,
+             (long long)W1.size(dims - 1));
+    if (sa.numel() != T) refuse(PyExc_ValueError, "the rows' scales must have %lld elements", (long long)T);
+    if (s1.sizes() != W1.sizes().slice(0, dims - 1) || s2.sizes() != s1.sizes())
+      refuse(PyExc_ValueError, "the weights' scales must have the weights' shape without K");
+    const Tensor *offsets = nullptr, *rows = nullptr;
+    if (grouped) {
+      offsets = &c.tensor(a[6], "offsets", ScalarType::Int, 1);
+      if (offsets->numel() != E + 1)
+        refuse(PyExc_ValueError, "offsets must have %lld elements", (long long)E + 1);
+      if (a[7] != Py_None) rows = &c.tensor(a[7], "rows", ScalarType::Int, 1);
+    }
+    const int64_t P = rows ? rows->numel() : T;
+    const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
+    c10::cuda::OptionalCUDAStreamGuard pool;
+    void *s = c.enter(a[9], pool);
+    Tensor Y = c.output(a[8], "the output", ScalarType::BFloat16, {P, N});
+    // (an empty tensor has no address: any other stands for "rows are given")
+    const int32_t *o = grouped ? ptr<int32_t>(*offsets) : nullptr;
+    const int32_t *r = !rows ? nullptr : P > 0 ? ptr<int32_t>(*rows) : o;
+    const void *w1 = W1.data_ptr(), *w2 = W2.data_ptr();
+    const float *fa = ptr<float>(sa), *f1 = ptr<float>(s1), *f2 = ptr<float>(s2);
+    c.check(unlocked([&] {
+      if (!grouped)
+        return fused ? swiglu_fused_int8(A.data_ptr(), fa, w1, f1, w2, f2, Y.data_ptr(), T, N, K, s)
+                     : swiglu_linear_int8(A.data_ptr(), fa, w1, f1, Y.data_ptr(), T, N, K, s);
+      return fused ? swiglu_fused_grouped_int8(A.data_ptr(), fa, w1, f1, w2, f2, o, r, Y.data_ptr(), T, P, E, N, K, s)
+                   : swiglu_linear_grouped_int8(A.data_ptr(), fa, w1, f1, o, r, Y.data_ptr(), T, P, E, N, K, s);
+    }));
+    return THPVariable_Wrap(std::move(Y));
   });
 }
 
@@ -314,6 +437,9 @@ PyCFunction fast() {
 
 PyMethodDef methods[] = {
     {"moe_route", fast<moe_route>(), METH_FASTCALL, nullptr},
+    {"moe_route_scored", fast<moe_route_scored>(), METH_FASTCALL, nullptr},
+    {"quant_int8", fast<quant_int8>(), METH_FASTCALL, nullptr},
+    {"int8_product", fast<int8_product>(), METH_FASTCALL, nullptr},
     {"grouped", fast<grouped>(), METH_FASTCALL, nullptr},
     {"residual_norm", fast<residual_norm>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -1,0 +1,121 @@
+"""Argument checks of the 8-bit calls and the router by scores (no GPU: the
+checks are pure host arithmetic on addresses that are never dereferenced)."""
+import pytest
+import torch
+
+import swiglu_gemm_transformer_gb300 as sg
+from swiglu_gemm_transformer_gb300 import _build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return sg.lib()
+
+
+A, B, C, D, E, F, G, H, I, J = (0x10000000 * i for i in range(1, 11))
+INV, MIS, UNS, OK = sg.ERR_INVALID_ARG, sg.ERR_MISALIGNED, sg.ERR_UNSUPPORTED, sg.OK
+
+
+def _route(lib, logits=A, fp32=0, score=1, bias=G, groups=8, kept=4, best=2, renorm=0, scale=1.0, ids=B, weights=C, offsets=D,
+           rows=E, slots=F, T=16, E_=64, k=8, ws=None, nbytes=0):
+    return lib.swiglu_moe_route_scored(logits, fp32, score, bias, groups, kept, best, renorm, scale, ids, weights, offsets, rows,
+                                       slots, T, E_, k, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), INV), (dict(E_=0), INV), (dict(k=0), INV), (dict(k=33), INV), (dict(fp32=2), INV), (dict(score=2), INV),
+    (dict(renorm=2), INV), (dict(scale=float("nan")), INV), (dict(groups=0), INV), (dict(groups=7), INV), (dict(kept=0), INV),
+    (dict(kept=9), INV), (dict(best=0), INV), (dict(best=3), INV), (dict(E_=66), INV),
+    (dict(groups=64, kept=16), UNS), (dict(E_=60, groups=6, kept=3), UNS), (dict(E_=2048), UNS), (dict(k=33, kept=8), UNS),
+    (dict(T=1 << 30), UNS), (dict(logits=None), INV), (dict(ids=None), INV), (dict(offsets=None), INV),
+    (dict(logits=A + 1), MIS), (dict(bias=G + 2), MIS), (dict(slots=F + 2), MIS),
+    (dict(ids=A), INV), (dict(weights=G + 4), INV), (dict(offsets=G + 252), INV),   # overlaps
+    (dict(T=4096), INV), (dict(T=4096, ws=H, nbytes=16), INV), (dict(T=4096, ws=G - 64, nbytes=1 << 20), INV),
+])
+def test_route_refusals(lib, kw, want):
+    assert _route(lib, **kw) == want
+
+
+def _quant(lib, X=A, fp32=0, Q=B, scale=C, R=16, K=64):
+    return lib.swiglu_quant_int8(X, fp32, Q, scale, R, K, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(R=-1), INV), (dict(K=-8), INV), (dict(fp32=2), INV), (dict(X=None), INV), (dict(Q=None), INV), (dict(scale=None), INV),
+    (dict(R=1 << 31), UNS), (dict(K=1 << 31), UNS), (dict(K=60), MIS), (dict(X=A + 8), MIS), (dict(Q=B + 4), MIS),
+    (dict(scale=C + 2), MIS), (dict(Q=A + 16), INV), (dict(scale=A + 64), INV), (dict(scale=B + 1020), INV),
+    (dict(X=B - 2048, fp32=1), INV),
+    (dict(R=0), OK),
+])
+def test_quant_refusals(lib, kw, want):
+    assert _quant(lib, **kw) == want
+
+
+def _product(lib, fused, grouped, A_=A, sa=B, W1=C, s1=D, W2=E, s2=F, off=G, rows=H, Y=I, T=64, P=128, E_=8, N=64, K=64):
+    if grouped:
+        if fused:
+            return lib.swiglu_fused_grouped_int8(A_, sa, W1, s1, W2, s2, off, rows, Y, T, P, E_, N, K, None)
+        return lib.swiglu_linear_grouped_int8(A_, sa, W1, s1, off, rows, Y, T, P, E_, N, K, None)
+    if fused:
+        return lib.swiglu_fused_int8(A_, sa, W1, s1, W2, s2, Y, T, N, K, None)
+    return lib.swiglu_linear_int8(A_, sa, W1, s1, Y, T, N, K, None)
+
+
+FUSED = pytest.mark.parametrize("fused", [True, False], ids=["fused", "linear"])
+GROUPED = pytest.mark.parametrize("grouped", [True, False], ids=["grouped", "dense"])
+
+
+@FUSED
+@GROUPED
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), INV), (dict(N=-8), INV), (dict(K=-16), INV), (dict(A_=None), INV), (dict(sa=None), INV), (dict(W1=None), INV),
+    (dict(s1=None), INV), (dict(Y=None), INV), (dict(T=1 << 31), UNS), (dict(N=1 << 31), UNS), (dict(K=1 << 22), UNS),
+    (dict(N=1 << 20, K=1 << 21), UNS), (dict(N=60), MIS), (dict(K=56), MIS), (dict(A_=A + 8), MIS), (dict(W1=C + 8), MIS),
+    (dict(sa=B + 2), MIS), (dict(s1=D + 1), MIS), (dict(Y=I + 8), MIS),
+    (dict(Y=A), INV), (dict(Y=B - 64), INV), (dict(Y=C + 64), INV), (dict(Y=D), INV),   # overlaps
+    (dict(N=0), OK),
+])
+def test_product_refusals(lib, fused, grouped, kw, want):
+    assert _product(lib, fused, grouped, **kw) == want
+
+
+@FUSED
+@pytest.mark.parametrize("kw,want", [
+    (dict(P=-1), INV), (dict(E_=0), INV), (dict(off=None), INV), (dict(rows=None), INV), (dict(E_=1025), UNS), (dict(P=1 << 31), UNS),
+    (dict(P=(1 << 31) - 256), UNS), (dict(N=(1 << 31) - 256, K=16), UNS), (dict(off=G + 2), MIS), (dict(rows=H + 1), MIS),
+    (dict(Y=G - 64), INV), (dict(Y=H), INV), (dict(P=0), OK),
+])
+def test_grouped_refusals(lib, fused, kw, want):
+    assert _product(lib, fused, True, **kw) == want
+
+
+@GROUPED
+@pytest.mark.parametrize("kw,want", [(dict(W2=None), INV), (dict(s2=None), INV), (dict(W2=E + 8), MIS), (dict(s2=F + 2), MIS),
+                                     (dict(Y=E), INV), (dict(Y=F - 16), INV)])
+def test_fused_needs_both_weights(lib, grouped, kw, want):
+    assert _product(lib, True, grouped, **kw) == want
+
+
+def test_dense_without_rows(lib):
+    assert _product(lib, True, False, T=0) == OK
+
+
+def test_python_binding_refuses_cpu_tensors_and_types(lib):
+    x, q = torch.zeros(8, 16), torch.zeros(8, 16, dtype=torch.int8)
+    s, off = torch.zeros(8), torch.zeros(3, dtype=torch.int32)
+    w, ws = torch.zeros(2, 8, 16, dtype=torch.int8), torch.zeros(2, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        sg.swiglu_moe_route_scored(x, 2)
+    with pytest.raises(TypeError, match="bfloat16 or float32"):
+        sg.swiglu_quant_int8(x.half())
+    for call in (lambda: sg.swiglu_quant_int8(x), lambda: sg.swiglu_linear_int8(q, s, q, s), lambda: sg.swiglu_fused_int8(q, s, q, s, q, s),
+                 lambda: sg.swiglu_linear_grouped_int8(q, s, w, ws, off), lambda: sg.swiglu_fused_grouped_int8(q, s, w, ws, w, ws, off)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(TypeError):
+        sg.swiglu_linear_grouped_int8(q, s, w, ws, None)
+    with pytest.raises(TypeError):
+        sg.swiglu_fused_int8(q, s, q, s, None, s)
+    with pytest.raises(TypeError):
+        sg.swiglu_fused_grouped_int8(q, s, w, ws, w, ws, None)

@@ -1,0 +1,383 @@
+"""GPU tests of the 8-bit quantisation and products against plain 64-bit
+implementations (written here; no code shared with the library).
+
+Tolerances, derived from the arithmetic:
+  * quantisation: codes are exact; a scale is one FP32 quotient.
+  * products: sums of products are whole numbers, exact below 2^24; a sum whose
+    terms' magnitudes S pass that is off by at most K 2^-23 S (truncating FP32
+    additions included).  Conversion and scales: three FP32 roundings; the
+    result's rounding to BF16 is half a step, 2^-8 relative.  For SiLU(g) u the
+    errors of g and u enter with |d SiLU| <= 1.1, fast exp and divide with 2^-19.
+"""
+import math
+import zlib
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF, I8, F32 = torch.bfloat16, torch.int8, torch.float32
+
+
+@pytest.fixture(scope="module")
+def sg():
+    import __graft_entry__
+    __graft_entry__.build()
+    import swiglu_gemm_transformer_gb300 as m
+    m.lib()
+    return m
+
+
+def _status(sg):
+    rc, detail = sg.swiglu_device_status()
+    assert rc == sg.OK, f"device status {sg.status_string(rc)} detail {detail}"
+
+
+def _gen(*seed):
+    return torch.Generator().manual_seed(zlib.crc32(repr(seed).encode()))
+
+
+# ---- quantisation ---------------------------------------------------------------
+
+
+def quant_ref(X):
+    x = X.double()
+    top = x.abs().amax(-1, keepdim=True) if x.shape[-1] else x.new_zeros(*x.shape[:-1], 1)
+    q = torch.round(127 * x / top)  # halves to even
+    q = torch.where((top > 0) & torch.isfinite(top), q, 0.0)
+    scale = torch.where(torch.isfinite(top), (top.float() / 127), math.nan)
+    return q.to(I8), scale.squeeze(-1).float()
+
+
+def check_quant(sg, X, **kw):
+    q, s = sg.swiglu_quant_int8(X.to(DEV), **kw)
+    assert q.dtype == I8 and s.dtype == F32 and q.shape == X.shape and s.shape == X.shape[:-1]
+    want, scale = quant_ref(X)
+    assert torch.equal(q.cpu(), want)
+    assert torch.equal(torch.nan_to_num(s.cpu(), nan=-1.0), torch.nan_to_num(scale, nan=-1.0))
+    return q, s
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", [(1, 8), (9, 16), (61, 1024), (33, 1032), (5, 4096), (17, 4104), (3, 8192), (2, 8200), (3, 32768),
+                                   (2, 32776), (1, 100000), (3, 7, 264), (2, 300, 896), (2000, 128)], ids=lambda s: "x".join(map(str, s)))
+def test_quant(sg, shape, dtype):
+    check_quant(sg, (torch.randn(*shape, generator=_gen("quant", shape)) * 3).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_quant_halves_go_to_even(sg, dtype):
+    x = torch.arange(-127, 128).float().repeat(4)[:1016].unsqueeze(0)  # max 127 * 2^p: halves below
+    rows = [x * 2.0, torch.cat([x * 0.5 + 0.25, torch.full((1, 8), 127.0)], 1)[:, :1016]]
+    top = torch.arange(1, 256).float()
+    many = torch.cat([top[:, None], torch.arange(0, 255).float().expand(255, 255) * top[:, None] / 254], 1)  # odd 254ths of each max
+    check_quant(sg, torch.cat(rows).to(dtype))
+    check_quant(sg, many[:, :256].contiguous().to(dtype))
+    # one FP32 step to either side of a half
+    if dtype == F32:
+        h = (torch.arange(0, 127).float() + 0.5) / 127
+        up, down = torch.nextafter(h, h + 1), torch.nextafter(h, h - 1)
+        check_quant(sg, torch.cat([h, up, down, -h, -up, -down, torch.ones(6)])[None, :768].contiguous())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("K", [64, 40000])
+def test_quant_rows_out_of_the_ordinary(sg, dtype, K):
+    x = torch.randn(12, K, generator=_gen("odd", K))
+    x[0] = 0.0
+    x[1, 5] = math.nan
+    x[2, K - 1] = -math.inf
+    x[3] *= 1e-40      # subnormal
+    x[4] *= 1e37
+    x[5] = -0.0
+    x[6] = 0.0
+    x[6, 3] = torch.finfo(dtype).smallest_normal
+    x[7] = torch.finfo(dtype).max
+    x[8, 1:] = 0.0
+    x[9, 7] = 1e30     # one value above all others
+    check_quant(sg, x.to(dtype))
+
+
+def test_quant_empty(sg):
+    q, s = sg.swiglu_quant_int8(torch.empty(0, 16, device=DEV))
+    assert q.shape == (0, 16) and s.shape == (0,)
+    q, s = sg.swiglu_quant_int8(torch.empty(5, 0, device=DEV, dtype=BF))
+    assert s.tolist() == [0.0] * 5
+
+
+def test_quant_into_given_outputs_and_refusals(sg):
+    x = torch.randn(6, 32, generator=_gen("given")).to(DEV)
+    Q, S = torch.empty(6, 32, dtype=I8, device=DEV), torch.empty(6, device=DEV)
+    q, s = sg.swiglu_quant_int8(x, Q, S)
+    assert q.data_ptr() == Q.data_ptr() and s.data_ptr() == S.data_ptr()
+    assert torch.equal(Q.cpu(), quant_ref(x.cpu())[0])
+    for bad in (x[0], x.t(), x[:, ::2], x[None, None]):
+        with pytest.raises(ValueError):
+            sg.swiglu_quant_int8(bad)
+    with pytest.raises(ValueError):
+        sg.swiglu_quant_int8(x, Q[:5])
+    with pytest.raises(TypeError):
+        sg.swiglu_quant_int8(x, Q.float())
+    with pytest.raises(sg.SwigluError):
+        sg.swiglu_quant_int8(x[:, :28].contiguous())
+
+
+# ---- products ---------------------------------------------------------------------
+
+
+def product_ref(A, sa, Ws, offsets, rows):
+    """(value, allowed error) in 64 bits; NaN where no expert owns the place."""
+    A, sa = A.to(DEV).double(), sa.to(DEV).double()
+    P = len(rows) if rows is not None else A.shape[0]
+    N, K = Ws[0][0].shape[1:]
+    ref = torch.full((P, N), math.nan, dtype=torch.double, device=DEV)
+    tol = torch.zeros_like(ref)
+    for e in range(len(offsets) - 1):
+        a, b = offsets[e], offsets[e + 1]
+        if a >= b:
+            continue
+        if rows is None:
+            x, s, ok = A[a:b], sa[a:b], torch.ones(b - a, dtype=torch.bool, device=DEV)
+        else:
+            r = torch.tensor(rows[a:b], device=DEV)
+            ok = (r >= 0) & (r < A.shape[0])
+            r = r.clamp(0, A.shape[0] - 1)
+            x, s = A[r], sa[r]
+        out = []
+        for W, w in Ws:
+            wd, scale = W[e].to(DEV).double(), s[:, None] * w[e].to(DEV).double()
+            size = x.abs() @ wd.abs().t()
+            z = (x @ wd.t()) * scale
+            out.append((z, torch.where(size >= 2.0**24, K * 2.0**-23 * size, 0.0) * scale.abs() + 3 * 2.0**-24 * z.abs()))
+        (g, dg), (u, du) = out[0], out[-1]
+        if len(Ws) == 1:
+            y, t = g, dg
+        else:
+            h = g * torch.sigmoid(g)
+            y, t = h * u, 1.1 * dg * (u.abs() + du) + h.abs() * du + 2.0**-19 * (h * u).abs()
+        ref[a:b], tol[a:b] = torch.where(ok[:, None], y, 0.0), torch.where(ok[:, None], t, 0.0)
+    return ref, tol + 2.0**-8 * ref.abs() + 1e-37
+
+
+SENTINEL = -77.0
+
+
+def check_product(sg, fused, sizes, N, K, T=None, first=0, spare=0, seed=0, edit=None, dense=False, full=False):
+    """sizes: rows of each expert; T: rows of A that `rows` draws from (None: no rows); full: codes of one sign, the largest."""
+    E = len(sizes)
+    gen = _gen("int8", fused, tuple(sizes), N, K, seed)
+    offsets = [first]
+    for s in sizes:
+        offsets.append(offsets[-1] + s)
+    P = offsets[-1] + spare
+    codes = (lambda *s: torch.randint(-128, -126, s, generator=gen).to(I8)) if full else (lambda *s: torch.randint(-128, 128, s, generator=gen).to(I8))
+    M = P if T is None else T
+    A, sa = codes(M, K), torch.rand(M, generator=gen) * 0.02 + 1e-3
+    Ws = [(codes(E, N, K), (torch.rand(E, N, generator=gen) + 0.1) * 0.02 / math.sqrt(max(K, 1)) * (0.1 if full else 1)) for _ in range(2 if fused else 1)]
+    rows = None if T is None else torch.randint(0, T, (P,), generator=gen).tolist()
+    if edit:
+        edit(A, sa, Ws, rows)
+    Y = torch.full((P, N), SENTINEL, dtype=BF, device=DEV)
+    args = [A.to(DEV), sa.to(DEV)]
+    for W, w in Ws:
+        args += [W.to(DEV)[0], w.to(DEV)[0]] if dense else [W.to(DEV), w.to(DEV)]
+    if dense:
+        (sg.swiglu_fused_int8 if fused else sg.swiglu_linear_int8)(*args, Y)
+    else:
+        off = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+        rd = None if rows is None else torch.tensor(rows, dtype=torch.int32, device=DEV)
+        (sg.swiglu_fused_grouped_int8 if fused else sg.swiglu_linear_grouped_int8)(*args, off, rd, Y)
+    _status(sg)
+    ref, tol = product_ref(A, sa, Ws, offsets, rows)
+    got = Y.double()
+    assert (got[:first] == SENTINEL).all() and (got[offsets[-1]:] == SENTINEL).all()
+    body = slice(first, offsets[-1])
+    want_nan = torch.isnan(ref[body])
+    assert torch.equal(torch.isnan(got[body]), want_nan)
+    err = torch.where(want_nan, 0.0, (got - ref).abs()[body])
+    bad = err > torch.where(want_nan, 1.0, tol[body])
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, first {bad.nonzero()[0].tolist()}, worst {(err / tol[body]).max()}"
+    return Y
+
+
+FORMS = pytest.mark.parametrize("fused", [True, False], ids=["fused", "linear"])
+
+
+@FORMS
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17, 31, 33, 64, 100, 128, 129, 191, 192, 193, 257, 700])
+@pytest.mark.parametrize("NK", [(8, 16), (72, 144), (264, 208), (520, 1104), (128, 4880)], ids=lambda s: "x".join(map(str, s)))
+def test_dense(sg, fused, M, NK):
+    check_product(sg, fused, [M], *NK, dense=True)
+
+
+@FORMS
+@pytest.mark.parametrize("gather", [True, False], ids=["rows", "dense"])
+@pytest.mark.parametrize("sizes", [[1], [5, 0, 3], [0, 0, 1, 0], [31, 32, 33], [64, 65, 1, 0, 63], [191, 192, 193, 0, 2],
+                                   [700, 0, 0, 1, 513], [95, 96, 97, 385]], ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("NK", [(8, 16), (72, 144), (264, 208), (512, 64)], ids=lambda s: "x".join(map(str, s)))
+def test_grouped(sg, fused, gather, sizes, NK):
+    check_product(sg, fused, sizes, *NK, T=53 if gather else None)
+
+
+@FORMS
+@pytest.mark.parametrize("E", [1, 2, 31, 32, 33, 64, 257, 1024])
+def test_grouped_expert_counts(sg, fused, E):
+    sizes = torch.randint(0, 4, (E,), generator=_gen("experts", E)).tolist()
+    sizes[-1] = 1
+    check_product(sg, fused, sizes, 40, 48, T=17)
+
+
+@FORMS
+def test_one_token(sg, fused):
+    check_product(sg, fused, [0, 1, 0, 0, 1, 1, 0, 1], 1024, 2048, T=1)
+    check_product(sg, fused, [1], 2568, 3584, dense=True)
+
+
+@FORMS
+def test_more_units_than_pairs(sg, fused):
+    check_product(sg, fused, [300, 17, 0, 520, 64, 1, 129, 33], 2568, 144, T=200)
+    check_product(sg, fused, [1500], 4872, 272, dense=True)
+
+
+@FORMS
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("sizes", [[3, 0, 40], [1, 0, 1]])
+def test_grouped_leaves_other_places_alone(sg, fused, gather, sizes):
+    check_product(sg, fused, sizes, 136, 80, T=9 if gather else None, first=5, spare=11)
+
+
+@FORMS
+@pytest.mark.parametrize("M", [3, 300])
+def test_sums_past_24_bits(sg, fused, M):
+    # every product near 2^14: sums of 2^27
+    check_product(sg, fused, [M], 136, 9216, dense=True, full=True)
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_sums_are_exact_up_to_24_bits(sg, M):
+    """K = 1024 products of 127 or 128 squared, told apart by one: scales of one make Z the rounded integer."""
+    K, N = 1024, 64
+    A = torch.full((M, K), -128, dtype=I8)
+    W = torch.full((N, K), -128, dtype=I8)
+    W[:, 0] = torch.arange(N) - 128
+    A[:, 1:3] = torch.randint(-128, 127, (M, 2), generator=_gen("exact")).to(I8)
+    W[:, 3:] *= torch.tensor([1, 0], dtype=I8).repeat(511)[:1021]  # stay inside 2^24
+    one = torch.ones(max(M, N), device=DEV)
+    Z = sg.swiglu_linear_int8(A.to(DEV), one[:M].contiguous(), W.to(DEV), one[:N].contiguous())
+    want = (A.long() @ W.long().t()).float().to(BF)
+    assert torch.equal(Z.cpu(), want)
+    # the low bits decide as well: subtract a multiple of 256 by products of the other sign
+    W2 = torch.cat([W, W.neg().clamp(-127)], 1)
+    A2 = torch.cat([A, A], 1)
+    Z = sg.swiglu_linear_int8(A2.to(DEV), one[:M].contiguous(), W2.to(DEV), one[:N].contiguous())
+    assert torch.equal(Z.cpu(), (A2.long() @ W2.long().t()).float().to(BF))
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_long_k(sg, M):
+    # past 2^17 an FP32 or a 32-bit sum of the largest products would pass its range
+    check_product(sg, False, [M], 16, (1 << 17) + 48, dense=True, full=True)
+
+
+@FORMS
+@pytest.mark.parametrize("T", [6, 200])
+def test_row_numbers_outside_a_give_zeros(sg, fused, T):
+    def edit(A, sa, Ws, rows):
+        for i, r in enumerate((-1, T, -(1 << 31), (1 << 31) - 1)):
+            rows[3 * i + 1] = r
+        sa[0] = math.nan  # (the clamped row's scale does not reach them)
+        for i in range(len(rows)):
+            rows[i] = 1 if rows[i] == 0 else rows[i]
+    Y = check_product(sg, fused, [13, 2] if T == 6 else [130, 70], 72, 144, T=T, edit=edit)
+    assert (Y[1] == 0).all() and (Y[4] == 0).all() and (Y[7] == 0).all()
+
+
+@FORMS
+@pytest.mark.parametrize("M", [4, 150])
+def test_scales_that_are_nan_or_zero_stay_in_their_row_and_column(sg, fused, M):
+    def edit(A, sa, Ws, rows):
+        sa[1], sa[2] = math.nan, 0.0
+        Ws[0][1][0, 5] = math.nan
+        Ws[-1][1][0, 6] = 0.0
+    check_product(sg, fused, [M], 72, 144, dense=True, edit=edit)
+
+
+@FORMS
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("offsets", [[0, 30, 10, 50], [-5, 10, 20, 90], [40, 30, 20, 10], [60, 60, 60, 60]])
+def test_malformed_offsets_stay_in_bounds(sg, fused, few, offsets):
+    """Clamped to [0, P] and made not decreasing."""
+    P = 3 if few else 60
+    offsets = [min(o, 3) for o in offsets] if few else offsets
+    gen = _gen("malformed")
+    q = lambda *s: torch.randint(-127, 128, s, generator=gen).to(I8).to(DEV)  # noqa: E731
+    f = lambda *s: (torch.rand(*s, generator=gen) * 0.01).to(DEV)  # noqa: E731
+    A, sa = q(P, 64), f(P)
+    Ws = [q(3, 40, 64), f(3, 40)] * (2 if fused else 1)
+    fn = sg.swiglu_fused_grouped_int8 if fused else sg.swiglu_linear_grouped_int8
+    Y = [torch.full((P, 40), SENTINEL, dtype=BF, device=DEV) for _ in range(2)]
+    fn(A, sa, *Ws, torch.tensor(offsets, dtype=torch.int32, device=DEV), None, Y[0])
+    clean, top = [], 0
+    for o in offsets:
+        top = max(top, min(max(o, 0), P))
+        clean.append(top)
+    fn(A, sa, *Ws, torch.tensor(clean, dtype=torch.int32, device=DEV), None, Y[1])
+    _status(sg)
+    assert torch.equal(Y[0], Y[1])
+
+
+@FORMS
+def test_zero_k_and_no_rows(sg, fused):
+    z = lambda *s, d=I8: torch.zeros(*s, dtype=d, device=DEV)  # noqa: E731
+    off = torch.tensor([0, 2, 5], dtype=torch.int32, device=DEV)
+    fn = sg.swiglu_fused_grouped_int8 if fused else sg.swiglu_linear_grouped_int8
+    n = 2 if fused else 1
+    Y = torch.full((5, 16), SENTINEL, dtype=BF, device=DEV)
+    fn(z(5, 0), z(5, d=F32), *[z(2, 16, 0), z(2, 16, d=F32)] * n, off, None, Y)
+    assert (Y == 0).all()
+    Y.fill_(SENTINEL)
+    fn(z(0, 32), z(0, d=F32), *[z(2, 16, 32), z(2, 16, d=F32)] * n, off, z(5, d=torch.int32), Y)
+    assert (Y == 0).all()
+    assert fn(z(4, 32), z(4, d=F32), *[z(2, 16, 32), z(2, 16, d=F32)] * n, off, z(0, d=torch.int32)).shape == (0, 16)
+    dense = sg.swiglu_fused_int8 if fused else sg.swiglu_linear_int8
+    assert dense(z(0, 32), z(0, d=F32), *[z(16, 32), z(16, d=F32)] * n).shape == (0, 16)
+    assert dense(z(4, 32), z(4, d=F32), *[z(0, 32), z(0, d=F32)] * n).shape == (4, 0)
+    assert (dense(z(4, 0), z(4, d=F32), *[z(16, 0), z(16, d=F32)] * n) == 0).all()
+
+
+@FORMS
+@pytest.mark.parametrize("sizes", [[1, 0, 2], [40, 0, 5], [300, 200, 7]])
+def test_repeats_bit_for_bit_on_another_stream(sg, fused, sizes):
+    a = check_product(sg, fused, sizes, 264, 1104, T=50)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b = check_product(sg, fused, sizes, 264, 1104, T=50)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
+def test_binding_refusals(sg):
+    q, s = torch.zeros(4, 32, dtype=I8, device=DEV), torch.zeros(4, device=DEV)
+    W, w = torch.zeros(16, 32, dtype=I8, device=DEV), torch.zeros(16, device=DEV)
+    We, we = W[None].repeat(3, 1, 1), w[None].repeat(3, 1)
+    off = torch.zeros(4, dtype=torch.int32, device=DEV)
+    for call, err in ((lambda: sg.swiglu_linear_int8(q.to(torch.uint8), s, W, w), TypeError),
+                      (lambda: sg.swiglu_linear_int8(q, s.to(BF), W, w), TypeError),
+                      (lambda: sg.swiglu_linear_int8(q, s[:3], W, w), ValueError),
+                      (lambda: sg.swiglu_linear_int8(q, s, W, w[:8]), ValueError),
+                      (lambda: sg.swiglu_linear_int8(q, s, W[:, :16].contiguous(), w), ValueError),
+                      (lambda: sg.swiglu_linear_int8(q, s, W.t(), w), ValueError),
+                      (lambda: sg.swiglu_fused_int8(q, s, W, w, W[:8], w[:8]), ValueError),
+                      (lambda: sg.swiglu_fused_int8(q, s, W, w, W, None), TypeError),
+                      (lambda: sg.swiglu_linear_int8(q, s, W, w, torch.zeros(4, 8, dtype=BF, device=DEV)), ValueError),
+                      (lambda: sg.swiglu_linear_grouped_int8(q, s, We, we, off[:3]), ValueError),
+                      (lambda: sg.swiglu_linear_grouped_int8(q, s, We, w, off), ValueError),
+                      (lambda: sg.swiglu_linear_grouped_int8(q, s, We, we, off.long()), TypeError),
+                      (lambda: sg.swiglu_linear_grouped_int8(q, s, W, w, off), ValueError),
+                      (lambda: sg.swiglu_linear_int8(q[:, :24].contiguous(), s, W[:, :24].contiguous(), w), sg.SwigluError)):
+        with pytest.raises(err):
+            call()
+    _status(sg)
