@@ -1,9 +1,11 @@
 // k_int8.cu -- launcher and C entry points of the products in 8-bit integers,
 // dense and grouped by expert.
 #include <algorithm>
+#include <cstring>
 
 #include "launch.h"
 #include "swiglu.h"
+#include "swiglu_int8_kernel.cuh"
 #include "swiglu_int8_rows_kernel.cuh"
 
 namespace swiglu {
@@ -42,6 +44,89 @@ cudaError_t launch_rows(Int8RowsParams &p, cudaStream_t s) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, swiglu_int8_rows_kernel<FUSED, R, NC, WARPS>, p);
+}
+
+struct TensorLaunch {
+  CUtensorMap a, a2, w1, w2;
+  Int8Params p;
+  int64_t units;  // most units the call can have
+  int device;
+  uint64_t ctx_gen;
+  cudaStream_t stream;
+};
+
+template <class C>
+cudaError_t launch_tensor(TensorLaunch &t) {
+  static PerDeviceOnce once;
+  static int max_clusters[64] = {0};
+  auto kern = swiglu_int8_kernel<C>;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = t.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;  // the occupancy query takes the cluster shape only
+  if (once.needed(t.device, t.ctx_gen)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(2 * 64, 1, 1);
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    max_clusters[t.device & 63] = n;
+    once.done(t.device, t.ctx_gen);
+  }
+  // a persistent grid of pairs
+  cfg.gridDim = dim3(2 * unsigned(std::min<int64_t>(t.units, max_clusters[t.device & 63])), 1, 1);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, t.a, t.a2, t.w1, t.w2, t.p);
+}
+
+// The tensor-core form.
+int run_tensor(const Int8Call &c, uint32_t *err, uint64_t timeout_ns, uint64_t ctx_gen) {
+  using Fused = Int8Cfg<true>;
+  constexpr int NT = Fused::NT, BK = Fused::BK;
+  TensorLaunch t;
+  std::memset(&t, 0, sizeof t);
+  t.stream = static_cast<cudaStream_t>(c.stream);
+  t.ctx_gen = ctx_gen;
+  if (cudaGetDevice(&t.device) != cudaSuccess) return SWIGLU_ERR_CUDA;
+  const uint64_t T = c.T, E = c.E, N = c.N, K = c.K;
+  const uint64_t adim[2] = {K, T}, astr[1] = {K};
+  const uint32_t abox[2] = {BK, c.rows ? 1u : 32u}, abox2[2] = {BK, NT / 2};
+  const uint64_t wdim[3] = {K, N, E}, wstr[2] = {K, N * K};
+  const uint32_t wbox[3] = {BK, 64, 1};
+  int rc = encode_u8_map(&t.a, c.A, 2, adim, astr, abox);
+  if (!c.rows && rc == SWIGLU_OK) rc = encode_u8_map(&t.a2, c.A, 2, adim, astr, abox2);
+  if (rc == SWIGLU_OK) rc = encode_u8_map(&t.w1, c.W1, 3, wdim, wstr, wbox);
+  if (rc == SWIGLU_OK) rc = encode_u8_map(&t.w2, c.fused ? c.W2 : c.W1, 3, wdim, wstr, wbox);
+  if (rc != SWIGLU_OK) return rc;
+  Int8Params &p = t.p;
+  p.sa = c.sa;
+  p.s1 = c.s1;
+  p.s2 = c.s2;
+  p.offsets = c.offsets;
+  p.rows = c.rows;
+  p.Y = static_cast<__nv_bfloat16 *>(c.Y);
+  p.T = int32_t(c.T);
+  p.P = int32_t(c.P);
+  p.E = int32_t(c.E);
+  p.N = int32_t(c.N);
+  p.num_k_blk = int32_t(ceil_div(c.K, BK));
+  p.num_n_blk = int32_t(ceil_div(c.N, c.fused ? 128 : 256));
+  p.timeout_ns = timeout_ns;
+  p.err = err;
+  t.units = (c.offsets ? std::min(c.E, c.P) + c.P / NT : ceil_div(c.P, NT)) * p.num_n_blk;
+  const cudaError_t e = c.fused ? launch_tensor<Fused>(t) : launch_tensor<Int8Cfg<false>>(t);
+  return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
 }
 
 int run_int8(const Int8Call &c) {
@@ -93,6 +178,7 @@ int run_int8(const Int8Call &c) {
   p.E = int32_t(E);
   p.N = int32_t(N);
   p.K = K;
+  if (P > 16) return run_tensor(c, err, timeout_ns, gen);
   cudaError_t e;
   if (P <= E)
     e = c.fused ? launch_rows<true, 1, 2>(p, s) : launch_rows<false, 1, 4>(p, s);

@@ -72,6 +72,9 @@ int device_info(uint32_t **err, int *sm_count, uint64_t *timeout_ns, uint64_t *c
 // bytes of dimensions 1.. ) with the 128-byte swizzle; call after device_info().
 int encode_bf16_map(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims,
                     const uint64_t *strides, const uint32_t *box);
+// The same for a tensor of bytes.
+int encode_u8_map(CUtensorMap *m, const void *ptr, int rank, const uint64_t *dims,
+                  const uint64_t *strides, const uint32_t *box);
 
 // Argument checks shared by the entry points of several files.
 inline bool ptr_aligned(const void *p, uintptr_t a) {

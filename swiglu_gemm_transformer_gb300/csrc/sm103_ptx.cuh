@@ -198,6 +198,26 @@ __device__ __forceinline__ void mma_f16_tmem_a_k64(uint32_t d, uint32_t a, uint6
       : "memory");
 }
 
+// One K step of 64 of a CTA pair with A from both CTAs' tensor memory (kind::f16,
+// M = 256: row i of CTA r's half in its lane i): D (+)= A x B over four K
+// slices of 16, steps as above; issued by the even CTA.
+__device__ __forceinline__ void mma_f16_pair_tmem_a_k64(uint32_t d, uint32_t a, uint64_t bdesc,
+                                                        uint32_t idesc, uint32_t first) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "setp.eq.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 b1, %2, 2;\n\t"
+      "add.s64 b2, %2, 4;\n\t"
+      "add.s64 b3, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1+8], b1, %3, t;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1+16], b2, %3, t;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1+24], b3, %3, t;\n\t}"
+      ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(first)
+      : "memory");
+}
+
 // Warp: store 32 consecutive 32-bit columns into this warp's 32 TMEM lanes
 // (thread i writes lane base+i).  Complete after tmem_wait_st().
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -523,6 +543,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major,
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
          ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The same with A=B=F16 (format code 0), both K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // Instruction descriptor, kind::f8f6f4 with E4M3 A and B (format code 0) and F32 D.

@@ -56,13 +56,11 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
-#include "grouped_units.h"
+#include "grouped_ring.cuh"
 #include "sm103_ptx.cuh"
 #include "tc_common.cuh"
 
 namespace swiglu {
-
-constexpr int kMaxExperts = 1024;
 
 struct GroupedParams {
   const int32_t *offsets;  // [E + 1]
@@ -137,40 +135,6 @@ __device__ __forceinline__ static bool bar_all(int id, int threads, bool ok) {
       : "memory");
   return r != 0;
 }
-
-// The units of one role, in order.  Every lane of the role's warp calls
-// next() (or one lane alone, for a role of one lane: ALONE).
-template <bool ALONE>
-class GroupedUnits {
- public:
-  __device__ GroupedUnits(const GroupedUnit *ring, uint32_t full, uint32_t empty,
-                          const GroupedParams &p, volatile int *abort_flag)
-      : ring_(ring), full_(full), empty_(empty), p_(p), abort_(abort_flag) {}
-  // False at the end, or when a wait gave up (ok then false).
-  __device__ bool next(GroupedUnit &u, bool &ok) {
-    const uint32_t block = i_ >> 5;
-    if ((i_ & 31u) == 0u) {
-      ok = wait_bar(full_ + 8u * (block & 1u), (block >> 1) & 1u, p_.timeout_ns, abort_, p_.err,
-                    WAIT_SCHED_FULL);
-      if (!ALONE) ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return false;
-    }
-    const int4 v = *reinterpret_cast<const int4 *>(ring_ + (i_ & 63u));
-    u.row0 = v.x, u.end = v.y, u.e = v.z, u.nb = v.w;
-    if ((i_ & 31u) == 31u) {  // the block has been read
-      if (!ALONE) __syncwarp();
-      if (ALONE || (threadIdx.x & 31u) == 0u) ptx::mbar_arrive(empty_ + 8u * (block & 1u));
-    }
-    ++i_;
-    return u.row0 >= 0;
-  }
-
- private:
-  const GroupedUnit *ring_;
-  uint32_t full_, empty_, i_ = 0;
-  const GroupedParams &p_;
-  volatile int *abort_;
-};
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
@@ -338,62 +302,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (warp == C::UNIT_WARP) {
     // ------------------------------------------------------------ unit finder
-    // Group bounds and row-tile counts.  The bounds are clamped to [0, P] and
-    // made monotone, so that no value of `offsets` reaches past Y.
-    int top = 0, sum = 0;
-    constexpr int AHEAD = 4;  // loads in flight: each is a trip to memory
-    int raw[AHEAD];
-    for (int e0 = 0; e0 <= p.E; e0 += 32) {
-      const int e = e0 + lane, slot = (e0 / 32) % AHEAD;
-      if (slot == 0) {
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-          raw[i] = e + 32 * i <= p.E ? __ldg(p.offsets + e + 32 * i) : 0;
-      }
-      int v = raw[0];
-#pragma unroll
-      for (int i = 1; i < AHEAD; ++i) v = slot == i ? raw[i] : v;
-      v = e <= p.E ? min(max(v, 0), p.P) : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int w = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v = max(v, w);
-      }
-      v = max(v, top);
-      const int prev = __shfl_up_sync(0xffffffffu, v, 1);
-      // row tiles of expert e - 1
-      int t = e >= 1 && e <= p.E ? row_tiles<C::NT>(v - (lane == 0 ? top : prev)) : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int w = __shfl_up_sync(0xffffffffu, t, o);
-        if (lane >= o) t += w;
-      }
-      t += sum;
-      if (e <= p.E) {
-        off[e] = v;
-        tiles[e] = t;
-      }
-      top = __shfl_sync(0xffffffffu, v, 31);
-      sum = __shfl_sync(0xffffffffu, t, 31);
-    }
-    __syncwarp();
-    for (uint32_t block = 0;; ++block) {
-      const bool ok = wait_bar(unite_bar + 8u * (block & 1u), ((block >> 1) & 1u) ^ 1u,
-                               block_limit(p.timeout_ns), abort_flag, p.err, WAIT_SCHED_EMPTY);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const GroupedUnit r = grouped_unit<C::GROUP>(cid + (int64_t(block) * 32 + lane) * ncl, off,
-                                                   tiles, p.E, p.num_n_blk);
-      *reinterpret_cast<int4 *>(ring + 32 * (block & 1u) + lane) = make_int4(r.row0, r.end, r.e, r.nb);
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(unitf_bar + 8u * (block & 1u));
-      if (__any_sync(0xffffffffu, r.row0 < 0)) break;
-    }
+    find_units<C::NT, C::GROUP>(ring, off, tiles, unitf_bar, unite_bar, p.offsets, p.P, p.E, p.num_n_blk, cid, ncl,
+                                p.timeout_ns, p.err, abort_flag);
   } else if (warp == C::PRODUCER_WARP) {
     // ------------------------------------------------------------ weights (both CTAs)
     if (ptx::elect_one()) {
       uint32_t stage = 0, phase = 0, issued = 0;
       bool ok = true;
-      GroupedUnits<true> units(ring, unitf_bar, unite_bar, p, abort_flag);
+      GroupedUnits<true> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
       GroupedUnit un;
       while (ok && units.next(un, ok)) {
         const int col0 = un.nb * 2 * C::COLS + static_cast<int>(rank) * C::COLS;
@@ -444,7 +360,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       constexpr int PER = C::NT / 8 / C::ROW_WARPS;  // gathers of a warp per stage
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      GroupedUnits<true> units(ring, unitf_bar, unite_bar, p, abort_flag);
+      GroupedUnits<true> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
       GroupedUnit un;
       while (ok && units.next(un, ok)) {
         const int row0 = un.row0 + static_cast<int>(rank) * (un.n() >> 1);
@@ -497,7 +413,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (rank == 0 && ptx::elect_one()) {
       uint32_t stage = 0, phase = 0, abuf = 0, aphase = 0;
       bool ok = true;
-      GroupedUnits<true> units(ring, unitf_bar, unite_bar, p, abort_flag);
+      GroupedUnits<true> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
       GroupedUnit un;
       while (ok && units.next(un, ok)) {
         const uint32_t idesc = ptx::idesc_bf16(C::MMA_M, un.n(), true, false);
@@ -544,7 +460,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     uint32_t abuf = 0, aphase = 0;
-    GroupedUnits<false> units(ring, unitf_bar, unite_bar, p, abort_flag);
+    GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
     // the next unit, its sums complete; false at the end, or when a wait gave up
     auto take = [&] {
       bool ok = true;
