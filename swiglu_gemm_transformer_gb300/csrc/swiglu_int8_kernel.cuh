@@ -114,11 +114,13 @@ __device__ __forceinline__ static void sts128(uint32_t addr, uint32_t a, uint32_
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// wait_bar with acquire at cluster scope, for what the other CTA has written.
-__device__ __forceinline__ static bool wait_bar_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                                        volatile int *abort_flag, uint32_t *err, uint32_t where) {
-  if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-  return wait_slow(bar, parity, limit_ns, abort_flag, err, where) && ptx::mbar_try_wait_cluster(bar, parity);
+// wait_bar for an arrival of the other CTA and what it wrote to its shared memory.
+__device__ __forceinline__ static bool wait_bar_peer(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                                     volatile int *abort_flag, uint32_t *err, uint32_t where) {
+  const bool ok = ptx::mbar_try_wait_relaxed_cluster(bar, parity) ||
+                  wait_slow(bar, parity, limit_ns, abort_flag, err, where);
+  ptx::fence_acquire_shared_cluster();
+  return ok;
 }
 
 template <class C>
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           for (int kb = 0; kb < 2 * nk; ++kb, ++step) {
             const uint32_t buf = step % C::BUFS, parity = (step / C::BUFS) & 1u;
             ok = wait(opf_bar(buf), parity, WAIT_MMA_FULL) &&
-                 wait_bar_cluster(peer_bar(buf), parity, p.timeout_ns, abort_flag, p.err, WAIT_MMA_FULL);
+                 wait_bar_peer(peer_bar(buf), parity, p.timeout_ns, abort_flag, p.err, WAIT_MMA_FULL);
             if (!ok) break;
             ptx::tc_fence_after();
             const uint64_t rdesc =
@@ -473,7 +475,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (!(ok = wait(opf_bar(buf), parity, WAIT_MMA_FULL))) break;
             ptx::tc_fence_after();
             ptx::tc_fence_before();
-            ptx::mbar_arrive_cluster(ptx::mapa_shared(peer_bar(buf), 0));
+            ptx::fence_release_shared_cluster();
+            ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(peer_bar(buf), 0));
           }
         }
       }
