@@ -62,10 +62,11 @@ EXPORTS = {
     "swiglu_fused_grouped": ("ppp pp p lllll p", ctypes.c_int),
     "swiglu_linear_grouped": ("pp pp p lllll p", ctypes.c_int),
     "swiglu_quant_int8": ("p i pp ll p", ctypes.c_int),
-    "swiglu_linear_int8": ("pp pp p lll p", ctypes.c_int),
-    "swiglu_fused_int8": ("pp pp pp p lll p", ctypes.c_int),
-    "swiglu_linear_grouped_int8": ("pp pp pp p lllll p", ctypes.c_int),
-    "swiglu_fused_grouped_int8": ("pp pp pp pp p lllll p", ctypes.c_int),
+    "swiglu_int8_workspace_size": ("lll", ctypes.c_uint64),
+    "swiglu_linear_int8": ("pp pp p lll pQ p", ctypes.c_int),
+    "swiglu_fused_int8": ("pp pp pp p lll pQ p", ctypes.c_int),
+    "swiglu_linear_grouped_int8": ("pp pp pp p lllll pQ p", ctypes.c_int),
+    "swiglu_fused_grouped_int8": ("pp pp pp pp p lllll pQ p", ctypes.c_int),
     "swiglu_residual_norm": ("ppp p ii pp l f p f pp llll p", ctypes.c_int),
     "swiglu_select_variant": ("lll i", ctypes.c_int),
     "swiglu_select_weight_kernel": ("ll", ctypes.c_int),
@@ -679,37 +680,40 @@ def swiglu_quant_int8(X, Q=None, scale=None, *, stream=None):
     return _native().quant_int8(X, Q, scale, stream)
 
 
-def swiglu_linear_int8(X, x_scale, W, w_scale, Z=None, *, stream=None):
+def swiglu_linear_int8(X, x_scale, W, w_scale, Z=None, *, workspace=None, stream=None):
     """Z = (X @ W.T) * x_scale[:,None] * w_scale; X int8 [M,K], W int8 [N,K]
-    (K-major), scales fp32 [M] and [N], Z bf16 [M,N]."""
-    return _native().int8_product(X, x_scale, W, w_scale, None, None, None, None, Z, stream)
+    (K-major), scales fp32 [M] and [N], Z bf16 [M,N].
+
+    ``workspace``, here and in the calls below: a CUDA tensor of at least
+    swiglu_int8_workspace_size() bytes; when None, one is allocated."""
+    return _native().int8_product(X, x_scale, W, w_scale, None, None, None, None, Z, workspace, stream)
 
 
-def swiglu_fused_int8(A, a_scale, W1, s1, W2, s2, Y=None, *, stream=None):
+def swiglu_fused_int8(A, a_scale, W1, s1, W2, s2, Y=None, *, workspace=None, stream=None):
     """Y = SiLU(g) * u with g = (A @ W1.T) * a_scale[:,None] * s1, u so with W2
     and s2; A int8 [M,K], W1/W2 int8 [N,K] (K-major), scales fp32, Y bf16 [M,N]."""
     if W2 is None:
         raise TypeError("W2 must be a torch.Tensor")
-    return _native().int8_product(A, a_scale, W1, s1, W2, s2, None, None, Y, stream)
+    return _native().int8_product(A, a_scale, W1, s1, W2, s2, None, None, Y, workspace, stream)
 
 
-def swiglu_linear_grouped_int8(X, x_scale, W, w_scale, offsets, rows=None, Z=None, *, stream=None):
+def swiglu_linear_grouped_int8(X, x_scale, W, w_scale, offsets, rows=None, Z=None, *, workspace=None, stream=None):
     """swiglu_linear_int8 for places grouped by expert: Z[p] of the row rows[p]
     (p without rows) and its scale, with expert e's W [E,N,K] and w_scale [E,N]
     for p in [offsets[e], offsets[e+1]).  Places of no expert are left as they are."""
     if offsets is None:
         raise TypeError("offsets must be a torch.Tensor")
-    return _native().int8_product(X, x_scale, W, w_scale, None, None, offsets, rows, Z, stream)
+    return _native().int8_product(X, x_scale, W, w_scale, None, None, offsets, rows, Z, workspace, stream)
 
 
-def swiglu_fused_grouped_int8(A, a_scale, W1, s1, W2, s2, offsets, rows=None, Y=None, *, stream=None):
+def swiglu_fused_grouped_int8(A, a_scale, W1, s1, W2, s2, offsets, rows=None, Y=None, *, workspace=None, stream=None):
     """swiglu_fused_int8 for places grouped by expert, with offsets and rows as in
     swiglu_linear_grouped_int8; W1/W2 int8 [E,N,K], s1/s2 fp32 [E,N]."""
     if W2 is None:
         raise TypeError("W2 must be a torch.Tensor")
     if offsets is None:
         raise TypeError("offsets must be a torch.Tensor")
-    return _native().int8_product(A, a_scale, W1, s1, W2, s2, offsets, rows, Y, stream)
+    return _native().int8_product(A, a_scale, W1, s1, W2, s2, offsets, rows, Y, workspace, stream)
 
 
 def swiglu_residual_norm(Z, R, *, slots=None, weights=None, post_norm: bool = True, gamma_post=None,

@@ -1,5 +1,6 @@
 // k_int8.cu -- launcher and C entry points of the products in 8-bit integers,
-// dense and grouped by expert.
+// dense and grouped by expert, and the kernel that widens the rows' codes to
+// FP16 before the tensor-core form.
 #include <algorithm>
 #include <cstring>
 
@@ -25,8 +26,56 @@ struct Int8Call {
   const int32_t *offsets, *rows;
   void *Y;
   int64_t T, P, E, N, K;
+  void *workspace;
+  uint64_t workspace_bytes;
   void *stream;
 };
+
+// Places up to which the rows kernel runs (RULE).
+constexpr int64_t kFewRows = 16;
+
+// The tensor-core form reads FP16 rows: A's, or, where there are fewer places
+// than rows, the places'.
+uint64_t widened_bytes(int64_t T, int64_t P, int64_t K) { return uint64_t(std::min(T, P)) * K * 2; }
+
+// 16 codes per thread and turn, to the workspace; row r is A's row rows[r] (any
+// row where that names none), or r.  Bound by the copy rate.
+__global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t *A, const int32_t *rows, __half *out,
+                                                         int64_t count, int32_t per_row, int32_t T) {
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < count; i += int64_t(gridDim.x) * blockDim.x) {
+    int64_t from = i;
+    if (rows) {
+      const int64_t r = i / per_row;
+      from = int64_t(min(max(__ldg(rows + r), 0), T - 1)) * per_row + (i - r * per_row);
+    }
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(A) + from);
+    uint32_t o[8];
+    widen4(v.x, o[0], o[1]);
+    widen4(v.y, o[2], o[3]);
+    widen4(v.z, o[4], o[5]);
+    widen4(v.w, o[6], o[7]);
+    uint4 *to = reinterpret_cast<uint4 *>(out) + 2 * i;
+    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+cudaError_t launch_widen(const Int8Call &c, const int32_t *rows, int64_t n, int sms) {
+  const int64_t per_row = c.K / 16, count = n * per_row;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(count, 256), int64_t(sms) * 8)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = static_cast<cudaStream_t>(c.stream);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, widen_rows_kernel, static_cast<const int8_t *>(c.A), rows,
+                            static_cast<__half *>(c.workspace), count, int32_t(per_row), int32_t(c.T));
+}
 
 template <bool FUSED, int R, int NC>
 cudaError_t launch_rows(Int8RowsParams &p, cudaStream_t s) {
@@ -91,24 +140,28 @@ cudaError_t launch_tensor(TensorLaunch &t) {
 }
 
 // The tensor-core form.
-int run_tensor(const Int8Call &c, uint32_t *err, uint64_t timeout_ns, uint64_t ctx_gen) {
+int run_tensor(const Int8Call &c, uint32_t *err, int sms, uint64_t timeout_ns, uint64_t ctx_gen) {
   using Fused = Int8Cfg<true>;
-  constexpr int NT = Fused::NT, BK = Fused::BK;
+  constexpr int NT = Fused::NT;
   TensorLaunch t;
   std::memset(&t, 0, sizeof t);
   t.stream = static_cast<cudaStream_t>(c.stream);
   t.ctx_gen = ctx_gen;
   if (cudaGetDevice(&t.device) != cudaSuccess) return SWIGLU_ERR_CUDA;
-  const uint64_t T = c.T, E = c.E, N = c.N, K = c.K;
-  const uint64_t adim[2] = {K, T}, astr[1] = {K};
-  const uint32_t abox[2] = {BK, c.rows ? 1u : 32u}, abox2[2] = {BK, NT / 2};
+  // Rows in the places' order where they are no more than A's; else A's rows, which
+  // the kernel gathers.
+  const bool gather = c.rows && c.P > c.T;
+  const uint64_t R = uint64_t(std::min(c.T, c.P)), E = c.E, N = c.N, K = c.K;
+  const uint64_t adim[2] = {K, R}, astr[1] = {K * 2};
+  const uint32_t abox[2] = {Fused::BK, gather ? 1u : 32u}, abox2[2] = {Fused::BK, NT / 2};
   const uint64_t wdim[3] = {K, N, E}, wstr[2] = {K, N * K};
-  const uint32_t wbox[3] = {BK, 64, 1};
-  int rc = encode_u8_map(&t.a, c.A, 2, adim, astr, abox);
-  if (!c.rows && rc == SWIGLU_OK) rc = encode_u8_map(&t.a2, c.A, 2, adim, astr, abox2);
+  const uint32_t wbox[3] = {Fused::W_BK, 64, 1};
+  int rc = encode_bf16_map(&t.a, c.workspace, 2, adim, astr, abox);  // (16-bit elements)
+  if (!gather && rc == SWIGLU_OK) rc = encode_bf16_map(&t.a2, c.workspace, 2, adim, astr, abox2);
   if (rc == SWIGLU_OK) rc = encode_u8_map(&t.w1, c.W1, 3, wdim, wstr, wbox);
   if (rc == SWIGLU_OK) rc = encode_u8_map(&t.w2, c.fused ? c.W2 : c.W1, 3, wdim, wstr, wbox);
   if (rc != SWIGLU_OK) return rc;
+  if (launch_widen(c, gather ? nullptr : c.rows, int64_t(R), sms) != cudaSuccess) return SWIGLU_ERR_CUDA;
   Int8Params &p = t.p;
   p.sa = c.sa;
   p.s1 = c.s1;
@@ -120,7 +173,8 @@ int run_tensor(const Int8Call &c, uint32_t *err, uint64_t timeout_ns, uint64_t c
   p.P = int32_t(c.P);
   p.E = int32_t(c.E);
   p.N = int32_t(c.N);
-  p.num_k_blk = int32_t(ceil_div(c.K, BK));
+  p.gather = gather;
+  p.num_k_blk = int32_t(ceil_div(c.K, Fused::W_BK));
   p.num_n_blk = int32_t(ceil_div(c.N, c.fused ? 128 : 256));
   p.timeout_ns = timeout_ns;
   p.err = err;
@@ -154,6 +208,17 @@ int run_int8(const Int8Call &c) {
       ranges_overlap(c.Y, y_bytes, c.offsets, uint64_t(E + 1) * 4) ||
       ranges_overlap(c.Y, y_bytes, c.rows, uint64_t(P) * 4))
     return SWIGLU_ERR_INVALID_ARG;
+  const uint64_t need = swiglu_int8_workspace_size(T, P, K);
+  if (need > 0) {
+    if (!c.workspace || c.workspace_bytes < need) return SWIGLU_ERR_INVALID_ARG;
+    if (!ptr_aligned(c.workspace, 16)) return SWIGLU_ERR_MISALIGNED;
+    // (A, W1, W2, scales, offsets, rows and Y; all are read or written after it)
+    const void *ptr[9] = {c.A, c.W1, c.W2, c.sa, c.s1, c.s2, c.offsets, c.rows, c.Y};
+    const uint64_t len[9] = {uint64_t(T) * K, w_bytes, w_bytes, uint64_t(T) * 4, s_bytes, s_bytes,
+                             uint64_t(E + 1) * 4, uint64_t(P) * 4, y_bytes};
+    for (int i = 0; i < 9; ++i)
+      if (ranges_overlap(c.workspace, need, ptr[i], len[i])) return SWIGLU_ERR_INVALID_ARG;
+  }
   uint32_t *err = nullptr;
   int sms = 0;
   uint64_t timeout_ns = 0, gen = 0;
@@ -178,7 +243,7 @@ int run_int8(const Int8Call &c) {
   p.E = int32_t(E);
   p.N = int32_t(N);
   p.K = K;
-  if (P > 16) return run_tensor(c, err, timeout_ns, gen);
+  if (P > kFewRows) return run_tensor(c, err, sms, timeout_ns, gen);
   cudaError_t e;
   if (P <= E)
     e = c.fused ? launch_rows<true, 1, 2>(p, s) : launch_rows<false, 1, 4>(p, s);
@@ -190,29 +255,40 @@ int run_int8(const Int8Call &c) {
 }  // namespace
 }  // namespace swiglu
 
+extern "C" uint64_t swiglu_int8_workspace_size(int64_t T, int64_t P, int64_t K) {
+  using namespace swiglu;
+  if (T < 1 || T > kMaxDim || P <= kFewRows || P > kMaxTiled || K < 1 || K > kMaxK) return 0;
+  return widened_bytes(T, P, K);
+}
+
 extern "C" int swiglu_fused_int8(const void *A, const float *a_scale, const void *W1, const float *s1,
                                  const void *W2, const float *s2, void *Y, int64_t M, int64_t N,
-                                 int64_t K, void *stream) {
-  return swiglu::run_int8({A, W1, W2, a_scale, s1, s2, true, false, nullptr, nullptr, Y, M, M, 1, N, K, stream});
+                                 int64_t K, void *workspace, uint64_t workspace_bytes, void *stream) {
+  return swiglu::run_int8({A, W1, W2, a_scale, s1, s2, true, false, nullptr, nullptr, Y, M, M, 1, N, K,
+                           workspace, workspace_bytes, stream});
 }
 
 extern "C" int swiglu_linear_int8(const void *X, const float *x_scale, const void *W, const float *w_scale,
-                                  void *Z, int64_t M, int64_t N, int64_t K, void *stream) {
-  return swiglu::run_int8(
-      {X, W, nullptr, x_scale, w_scale, nullptr, false, false, nullptr, nullptr, Z, M, M, 1, N, K, stream});
+                                  void *Z, int64_t M, int64_t N, int64_t K, void *workspace,
+                                  uint64_t workspace_bytes, void *stream) {
+  return swiglu::run_int8({X, W, nullptr, x_scale, w_scale, nullptr, false, false, nullptr, nullptr, Z, M, M, 1, N, K,
+                           workspace, workspace_bytes, stream});
 }
 
 extern "C" int swiglu_fused_grouped_int8(const void *A, const float *a_scale, const void *W1,
                                          const float *s1, const void *W2, const float *s2,
                                          const int32_t *offsets, const int32_t *rows, void *Y, int64_t T,
-                                         int64_t P, int64_t E, int64_t N, int64_t K, void *stream) {
-  return swiglu::run_int8({A, W1, W2, a_scale, s1, s2, true, true, offsets, rows, Y, T, P, E, N, K, stream});
+                                         int64_t P, int64_t E, int64_t N, int64_t K, void *workspace,
+                                         uint64_t workspace_bytes, void *stream) {
+  return swiglu::run_int8({A, W1, W2, a_scale, s1, s2, true, true, offsets, rows, Y, T, P, E, N, K,
+                           workspace, workspace_bytes, stream});
 }
 
 extern "C" int swiglu_linear_grouped_int8(const void *X, const float *x_scale, const void *W,
                                           const float *w_scale, const int32_t *offsets,
                                           const int32_t *rows, void *Z, int64_t T, int64_t P, int64_t E,
-                                          int64_t N, int64_t K, void *stream) {
-  return swiglu::run_int8(
-      {X, W, nullptr, x_scale, w_scale, nullptr, false, true, offsets, rows, Z, T, P, E, N, K, stream});
+                                          int64_t N, int64_t K, void *workspace, uint64_t workspace_bytes,
+                                          void *stream) {
+  return swiglu::run_int8({X, W, nullptr, x_scale, w_scale, nullptr, false, true, offsets, rows, Z, T, P, E, N, K,
+                           workspace, workspace_bytes, stream});
 }

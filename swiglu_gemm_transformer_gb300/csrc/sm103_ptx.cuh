@@ -358,29 +358,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster_relaxed(uint32_t c
                : "memory");
 }
 
-// Release and acquire at cluster scope of shared memory alone (this CTA's writes;
-// any CTA's of the cluster): unlike release.cluster and acquire.cluster they
-// do not wait for global memory.
-__device__ __forceinline__ void fence_release_shared_cluster() {
-  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
-}
-__device__ __forceinline__ void fence_acquire_shared_cluster() {
-  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
-}
-
-// mbar_try_wait without ordering, at cluster scope.
-__device__ __forceinline__ bool mbar_try_wait_relaxed_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 __device__ __forceinline__ void st_shared_cluster_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }

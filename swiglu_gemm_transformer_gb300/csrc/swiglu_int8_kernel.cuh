@@ -9,22 +9,20 @@
 // MMA, whose FP32 sums of their products are exact below 2^24.  As in the
 // BF16 grouped kernel the weights are the MMA's M side (256 per pair) and the
 // rows its N side, in steps of 32; the units and their finder are the same.
-//   * weights and rows are copied as codes, 128 of K a stage (TMA; gathered rows
-//     four at a time), half the bytes of 16-bit operands;
-//   * the weights are widened straight into tensor memory, as the MMA's A
+//   * the weights are copied as codes, 128 of K a stage (TMA), half the bytes of
+//     16-bit operands, and widened straight into tensor memory, as the MMA's A
 //     operand: K-major codes give a thread its lane's K in 16-byte loads, and
-//     shared memory, which feeds copies, loads and the MMA's B operand alike,
-//     is spared their 16-bit form.  Each of two groups of four warps takes
-//     every other K step of 64;
-//   * the rows are widened into shared memory (K-major, 128-byte swizzle), by two
-//     more groups of four warps;
+//     shared memory, which feeds copies, loads and the MMA's B operand alike, is
+//     spared their 16-bit form.  Groups of four warps take K steps of 64 in turn;
+//   * the rows come as FP16, widened once per call by a small kernel before this
+//     one (k_int8.cu): widened here they cost as many instructions as the
+//     weights, once for each column tile (7B projection, 2047 rows: MEASURE);
 //   * accumulators of 192 columns, double-buffered, leave 128 columns for
-//     four K steps of weights;
+//     four K steps of weights.  A buffer of them is freed, filled, announced and
+//     read in turn, so the codes are widened before the wait for it;
 //   * FUSED: gate and up of a column lie in lanes 2j and 2j ^ 9 of one warp (odd
 //     lanes take the up columns, in an order that keeps the loads of eight
-//     lanes on different banks), so shuffles bring them together;
-//   * the odd CTA's operands are announced to the MMA's thread by a thread of
-//     its own, so that no other pays for the release at cluster scope.
+//     lanes on different banks), so shuffles bring them together.
 // Every wait is bounded as in the other kernels.
 #pragma once
 
@@ -45,7 +43,8 @@ struct Int8Params {
   const int32_t *rows;        // [P] or null
   __nv_bfloat16 *Y;           // [P, N]
   int32_t T, P, E, N;         // rows of A, rows of Y, experts, output columns
-  int32_t num_k_blk, num_n_blk;
+  int32_t gather;             // 1: the FP16 rows are A's; 0: they are in the places' order
+  int32_t num_k_blk, num_n_blk;  // stages of codes, column tiles
   uint64_t timeout_ns;
   uint32_t *err;
 };
@@ -54,40 +53,41 @@ template <bool FUSED_>
 struct Int8Cfg {
   static constexpr bool FUSED = FUSED_;
   static constexpr int NT = 192;                 // most rows of a tile
-  static constexpr int BK = 128;                 // K of a stage of codes
+  static constexpr int BK = 64;                  // K of a step
   static constexpr int COLS = FUSED ? 64 : 128;  // output columns per CTA
-  static constexpr int BOX_BYTES = 64 * BK;      // 64 columns' codes
+  static constexpr int W_BK = 128;               // K of a stage of codes
+  static constexpr int BOX_BYTES = 64 * W_BK;    // 64 columns' codes
   static constexpr int W_BYTES = 2 * BOX_BYTES;  // W1 | W2, or two boxes of W
-  static constexpr int A_BYTES = NT / 2 * BK;
-  static constexpr int STAGE_BYTES = W_BYTES + A_BYTES;
-  static constexpr int STAGES = 5;
-  static constexpr int BUFS = 4;                 // widened operands, 64 of K each
-  static constexpr int BUF_BYTES = NT / 2 * 64 * 2;
+  static constexpr int W_STAGES = 6;
+  static constexpr int A_BYTES = NT / 2 * BK * 2;  // a step's rows (FP16)
+  static constexpr int A_STAGES = 8;
+  static constexpr int BUFS = 4;                 // widened weights, a step each
   static constexpr int EPI_WARPS = 8;
   // one epilogue warp's block: 16 rows x 32 columns BF16 (rows 80 bytes apart:
   // 16-byte reads of eight rows touch every bank once), FUSED 16 x 16 (48 apart)
   static constexpr int STG_PITCH = FUSED ? 48 : 80;
   static constexpr int STG_BYTES = 1280;
-  static constexpr int BUF_OFF = STAGES * STAGE_BYTES;
-  static constexpr int STG_OFF = BUF_OFF + BUFS * BUF_BYTES;
+  static constexpr int A_OFF = W_STAGES * W_BYTES;
+  static constexpr int STG_OFF = A_OFF + A_STAGES * A_BYTES;
   static constexpr int TAB_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
   static constexpr int TAB_BYTES = 2 * (kMaxExperts + 1) * 4;
   static constexpr int UNIT_OFF = (TAB_OFF + TAB_BYTES + 15) / 16 * 16;  // two blocks of 32 units
   static constexpr int BAR_OFF = UNIT_OFF + 2 * 32 * 16;
-  static constexpr int NUM_BARS = 2 * STAGES + 3 * BUFS + 9;
+  static constexpr int NUM_BARS = 2 * W_STAGES + 2 * A_STAGES + BUFS + 9;
   static constexpr int SMEM_BYTES = BAR_OFF + NUM_BARS * 8 + 16 + 1024;
-  static constexpr int W_WARP = EPI_WARPS;       // first of eight that widen weights,
-  static constexpr int R_WARP = W_WARP + 8;      // of eight that widen rows
-  static constexpr int PRODUCER_WARP = R_WARP + 8;
+  static constexpr int W_WARP = EPI_WARPS;       // first of those that widen weights
+  static constexpr int W_GROUPS = 3;             // of four warps
+  static constexpr int PRODUCER_WARP = W_WARP + 4 * W_GROUPS;
   static constexpr int MMA_WARP = PRODUCER_WARP + 1;
   static constexpr int UNIT_WARP = MMA_WARP + 1;
   static constexpr int LOAD_WARP = UNIT_WARP + 1;  // first of those that copy rows
-  static constexpr int LOAD_WARPS = 4;
+  static constexpr int LOAD_WARPS = 8;
   static constexpr int THREADS = 32 * (LOAD_WARP + LOAD_WARPS);
   static constexpr int ACC_COLS = NT;            // TMEM columns of one accumulator buffer
-  static constexpr int OP_COL = 2 * ACC_COLS;    // then the widened weights, 32 columns a K step
+  static constexpr int OP_COL = 2 * ACC_COLS;    // then the widened weights, 32 columns a step
   static constexpr int GROUP = 8;
   static_assert(OP_COL + BUFS * 32 == 512, "tensor memory");
+  static_assert(A_STAGES % BUFS == 0, "one arrival frees rows and weights");
   static_assert(NT / 8 % LOAD_WARPS == 0, "gathers split evenly");
   static_assert(THREADS <= 1024, "threads");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -110,19 +110,6 @@ __device__ __forceinline__ static uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ static void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// wait_bar for an arrival of the other CTA and what it wrote to its shared memory.
-__device__ __forceinline__ static bool wait_bar_peer(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                                     volatile int *abort_flag, uint32_t *err, uint32_t where) {
-  const bool ok = ptx::mbar_try_wait_relaxed_cluster(bar, parity) ||
-                  wait_slow(bar, parity, limit_ns, abort_flag, err, where);
-  ptx::fence_acquire_shared_cluster();
-  return ok;
-}
-
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     swiglu_int8_kernel(const __grid_constant__ CUtensorMap tmA,   // dense: boxes of 32 rows; gathered: one row
@@ -136,13 +123,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint8_t *smem = smem_raw + (base - raw);
 
   const uint32_t bars = base + C::BAR_OFF;
-  auto full_bar = [&](int s) { return bars + 8u * s; };                       // codes of a stage are there
-  auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };        // and have been widened
-  auto opf_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + b); };      // this CTA's operands are there
-  auto ope_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + C::BUFS + b); };       // the MMA has read them
-  auto peer_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + 2 * C::BUFS + b); };  // leader: the other CTA's
-  const uint32_t accf = bars + 8u * (2 * C::STAGES + 3 * C::BUFS), acce = accf + 16u;    // two each
-  const uint32_t unitf_bar = accf + 32u, unite_bar = accf + 48u;                         // two each
+  auto full_bar = [&](int s) { return bars + 8u * s; };                    // a stage's codes are there
+  auto empty_bar = [&](int s) { return bars + 8u * (C::W_STAGES + s); };   // and have been read
+  const uint32_t abars = bars + 8u * 2 * C::W_STAGES;
+  auto rows_bar = [&](int s) { return abars + 8u * s; };                   // leader: both CTAs' rows of a step are there
+  auto done_bar = [&](int s) { return abars + 8u * (C::A_STAGES + s); };   // the MMA has read the step's operands
+  auto op_bar = [&](int b) { return abars + 8u * (2 * C::A_STAGES + b); };  // leader: both CTAs' widened weights
+  const uint32_t accf = abars + 8u * (2 * C::A_STAGES + C::BUFS), acce = accf + 16u;  // two each
+  const uint32_t unitf_bar = accf + 32u, unite_bar = accf + 48u;                      // two each
   const uint32_t drain_bar = accf + 64u;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + C::NUM_BARS * 8);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -154,26 +142,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();  // 0 = the pair's leader
   const int nk = p.num_k_blk;
-  const bool gather = p.rows != nullptr;
+  const bool gather = p.gather != 0;
   const int loaders = gather ? C::LOAD_WARPS : 1;
 
   if (warp == C::PRODUCER_WARP && lane == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(full_bar(s), 1 + loaders);
-      ptx::mbar_init(empty_bar(s), 16);  // the warps that widen
+    for (int s = 0; s < C::W_STAGES; ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 8);  // four warps for each step
     }
-    for (int b = 0; b < C::BUFS; ++b) {
-      ptx::mbar_init(opf_bar(b), 8);  // one group of each kind
-      ptx::mbar_init(ope_bar(b), 1);
-      ptx::mbar_init(peer_bar(b), 1);
+    for (int s = 0; s < C::A_STAGES; ++s) {
+      ptx::mbar_init(rows_bar(s), 1 + 2 * loaders);
+      ptx::mbar_init(done_bar(s), 1);
     }
+    for (int b = 0; b < C::BUFS; ++b) ptx::mbar_init(op_bar(b), 8);  // four warps of each CTA
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(accf + 8u * b, 1);
       ptx::mbar_init(acce + 8u * b, 2 * C::EPI_WARPS);
       ptx::mbar_init(unitf_bar + 8u * b, 1);
       // readers of the units: epilogue, widening warps, weights' thread, rows'
-      // threads, the MMA's thread or (odd CTA) the one that announces operands
-      ptx::mbar_init(unite_bar + 8u * b, C::EPI_WARPS + 16 + 1 + loaders + 1);
+      // threads and, in the leader, the MMA's
+      ptx::mbar_init(unite_bar + 8u * b, C::EPI_WARPS + 4 * C::W_GROUPS + 1 + loaders + (rank == 0 ? 1 : 0));
     }
     ptx::mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -228,7 +216,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (int j = 0; j < 3; ++j) {
         const int row = un.row0 + 16 * (h + 2 * (2 * j + (lane >> 4))) + (lane & 15);
         int src = -1;
-        if (row < un.end) src = gather ? __ldg(p.rows + row) : row;
+        if (row < un.end) src = p.rows ? __ldg(p.rows + row) : row;
         const bool valid = src >= 0 && src < p.T;
         sa[j] = valid ? __ldg(p.sa + src) : 0.0f;
         named[j] = __ballot_sync(0xffffffffu, valid);
@@ -299,109 +287,46 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         aphase ^= 1u;
       }
     }
-  } else if (warp < C::R_WARP) {
-    // ------------------------------------------------------------ weights' codes into tensor memory
-    const int g = (warp - C::W_WARP) >> 2, q = warp & 3;
+  } else if (warp < C::PRODUCER_WARP) {
+    // ------------------------------------------------------------ weights' codes into tensor memory (both CTAs)
+    const int q = warp & 3;
     // the lane's row of codes: a column of W1 or W2 (FUSED), of either half of W
     const int col = C::FUSED ? 16 * q + ((lane >> 1) ^ (lane & 1 ? 4 : 0)) : (32 * q + lane) & 63;
     const int box = C::FUSED ? lane & 1 : q >> 1;
-    const uint32_t src = base + box * C::BOX_BYTES + col * C::BK;
+    const uint32_t src = base + box * C::BOX_BYTES + col * C::W_BK;
     const uint32_t dst = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + C::OP_COL;
-    uint32_t stage = 0, phase = 0, step = 0;  // step: of this group, buffer (2 step + g) % 4
+    uint32_t step = (warp - C::W_WARP) >> 2, end = 0;  // this group's steps: every W_GROUPS-th
     bool ok = true;
     GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
     GroupedUnit un;
     while (ok && units.next(un, ok)) {
-      for (int kb = 0; kb < nk; ++kb, ++step) {
-        const uint32_t buf = (2 * step + g) % C::BUFS, round = (2 * step + g) / C::BUFS;
-        ok = wait(full_bar(stage), phase, WAIT_MMA_FULL);
-        ok = __all_sync(0xffffffffu, ok);
+      for (end += 2 * nk; step < end; step += C::W_GROUPS) {
+        const uint32_t buf = step % C::BUFS, stage = step / 2 % C::W_STAGES;
+        ok = __all_sync(0xffffffffu, wait(full_bar(stage), step / 2 / C::W_STAGES & 1u, WAIT_MMA_FULL));
         if (!ok) break;
-        uint4 v[4];
+        uint32_t o[32];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          v[t] = lds128(src + stage * C::STAGE_BYTES + (((4 * g + t) ^ (col & 7)) << 4));
-        ok = wait(ope_bar(buf), (round & 1u) ^ 1u, WAIT_MMA_ACC_EMPTY);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int t = 0; t < 4; t += 2) {
-          uint32_t o[16];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            widen4(v[t + j].x, o[8 * j], o[8 * j + 1]);
-            widen4(v[t + j].y, o[8 * j + 2], o[8 * j + 3]);
-            widen4(v[t + j].z, o[8 * j + 4], o[8 * j + 5]);
-            widen4(v[t + j].w, o[8 * j + 6], o[8 * j + 7]);
-          }
-          ptx::tmem_st16(dst + buf * 32 + t * 8, o);
+        for (int t = 0; t < 4; ++t) {
+          const uint4 v = lds128(src + stage * C::W_BYTES + (((4 * (step & 1u) + t) ^ (col & 7)) << 4));
+          widen4(v.x, o[8 * t], o[8 * t + 1]);
+          widen4(v.y, o[8 * t + 2], o[8 * t + 3]);
+          widen4(v.z, o[8 * t + 4], o[8 * t + 5]);
+          widen4(v.w, o[8 * t + 6], o[8 * t + 7]);
         }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty_bar(stage));
+        if (step >= C::BUFS) {  // the buffer's last step has been read
+          const uint32_t last = step - C::BUFS;
+          ok = __all_sync(0xffffffffu, wait(done_bar(last % C::A_STAGES), last / C::A_STAGES & 1u, WAIT_MMA_ACC_EMPTY));
+          if (!ok) break;
+          ptx::tc_fence_after();
+        }
+        ptx::tmem_st32(dst + buf * 32, o);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(opf_bar(buf));
-          ptx::mbar_arrive(empty_bar(stage));
-        }
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    // Consume the MMA's arrivals still due on this CTA's "operands read" barriers,
-    // so that none targets this CTA after it exits.
-    if (ok && q == 0 && lane == 0)
-      for (uint32_t i = step < 2 ? 0 : step - 2; i < step; ++i)
-        wait_quiet(ope_bar((2 * i + g) % C::BUFS), ((2 * i + g) / C::BUFS) & 1u, p.timeout_ns);
-    __syncwarp();
-  } else if (warp < C::PRODUCER_WARP) {
-    // ------------------------------------------------------------ rows' codes into the B operand
-    const int g = (warp - C::R_WARP) >> 2, q = warp & 3;
-    // a warp takes 8 rows x 4 pieces of 16 codes a turn; eight lanes read rows r
-    // and r + 4, whose pieces lie on different banks, and store them in two
-    // orders, for the same reason
-    const int second = (lane >> 2) & 1, piece = lane & 3;
-    const int r8 = 4 * second + (lane >> 3);
-    const int first = 8 * q + r8;  // row in the CTA's half; row % 8 = r8
-    const uint32_t src = base + C::W_BYTES + first * C::BK + (((4 * g + piece) ^ r8) << 4);
-    const uint32_t dst = base + C::BUF_OFF + first * 128;
-    const uint32_t at0 = ((2 * piece + second) ^ r8) << 4, at1 = ((2 * piece + 1 - second) ^ r8) << 4;
-    uint32_t stage = 0, phase = 0, step = 0;
-    bool ok = true;
-    GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
-    GroupedUnit un;
-    while (ok && units.next(un, ok)) {
-      const int rows = un.rows_of(static_cast<int>(rank));
-      for (int kb = 0; kb < nk; ++kb, ++step) {
-        const uint32_t buf = (2 * step + g) % C::BUFS, round = (2 * step + g) / C::BUFS;
-        ok = wait(full_bar(stage), phase, WAIT_MMA_FULL) && wait(ope_bar(buf), (round & 1u) ^ 1u, WAIT_MMA_ACC_EMPTY);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < C::NT / 2 / 32; ++i) {
-          if (32 * i + 8 * q >= rows) break;
-          const uint4 v = lds128(src + stage * C::STAGE_BYTES + i * 32 * C::BK);
-          uint32_t o[8];
-          widen4(v.x, o[0], o[1]);
-          widen4(v.y, o[2], o[3]);
-          widen4(v.z, o[4], o[5]);
-          widen4(v.w, o[6], o[7]);
-          const uint32_t to = dst + buf * C::BUF_BYTES + i * 32 * 128;
-          sts128(to + at0, second ? o[4] : o[0], second ? o[5] : o[1], second ? o[6] : o[2], second ? o[7] : o[3]);
-          sts128(to + at1, second ? o[0] : o[4], second ? o[1] : o[5], second ? o[2] : o[6], second ? o[3] : o[7]);
-        }
-        ptx::fence_proxy_async_smem();  // generic-proxy writes, read by the MMA (async proxy)
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(opf_bar(buf));
-          ptx::mbar_arrive(empty_bar(stage));
-        }
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        // (relaxed: the stores into tensor memory are complete)
+        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(op_bar(buf), 0));
       }
     }
     __syncwarp();
@@ -414,18 +339,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       GroupedUnit un;
       while (ok && units.next(un, ok)) {
         const int col0 = (un.nb * 2 + static_cast<int>(rank)) * C::COLS;
-        const uint32_t bytes = C::W_BYTES + un.row_bytes(static_cast<int>(rank), gather);
         for (int kb = 0; kb < nk; ++kb) {
           if (!(ok = wait(empty_bar(stage), phase ^ 1u, WAIT_PRODUCER_EMPTY))) break;
-          const uint32_t sw = base + stage * C::STAGE_BYTES;
+          const uint32_t sw = base + stage * C::W_BYTES;
           const uint32_t fb = ptx::mapa_shared(full_bar(stage), rank);
-          ptx::mbar_arrive_expect_tx(full_bar(stage), bytes);
-          ptx::tma_load_3d_pair(sw, &tmW1, fb, kb * C::BK, col0, un.e);
+          ptx::mbar_arrive_expect_tx(full_bar(stage), C::W_BYTES);
+          ptx::tma_load_3d_pair(sw, &tmW1, fb, kb * C::W_BK, col0, un.e);
           if (C::FUSED)
-            ptx::tma_load_3d_pair(sw + C::BOX_BYTES, &tmW2, fb, kb * C::BK, col0, un.e);
+            ptx::tma_load_3d_pair(sw + C::BOX_BYTES, &tmW2, fb, kb * C::W_BK, col0, un.e);
           else
-            ptx::tma_load_3d_pair(sw + C::BOX_BYTES, &tmW1, fb, kb * C::BK, col0 + 64, un.e);
-          if (++stage == C::STAGES) {
+            ptx::tma_load_3d_pair(sw + C::BOX_BYTES, &tmW1, fb, kb * C::W_BK, col0 + 64, un.e);
+          if (++stage == C::W_STAGES) {
             stage = 0;
             phase ^= 1u;
           }
@@ -435,51 +359,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     __syncwarp();
   } else if (warp == C::MMA_WARP) {
-    if (ptx::elect_one()) {
-      uint32_t step = 0, abuf = 0, aphase = 0;  // step: of 64 of K
+    // ------------------------------------------------------------ MMA issuer (leader only)
+    if (rank == 0 && ptx::elect_one()) {
+      uint32_t step = 0, abuf = 0, aphase = 0;
       bool ok = true;
       GroupedUnits<true> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
       GroupedUnit un;
-      if (rank == 0) {
-        // ---------------------------------------------------------- MMA issuer
-        while (ok && units.next(un, ok)) {
-          const uint32_t idesc = ptx::idesc_f16(256, un.n());
-          if (!(ok = wait(acce + 8u * abuf, aphase ^ 1u, WAIT_MMA_ACC_EMPTY))) break;
-          ptx::tc_fence_after();
-          const uint32_t d = tmem_base + abuf * C::ACC_COLS;
-          for (int kb = 0; kb < 2 * nk; ++kb, ++step) {
-            const uint32_t buf = step % C::BUFS, parity = (step / C::BUFS) & 1u;
-            ok = wait(opf_bar(buf), parity, WAIT_MMA_FULL) &&
-                 wait_bar_peer(peer_bar(buf), parity, p.timeout_ns, abort_flag, p.err, WAIT_MMA_FULL);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            const uint64_t rdesc =
-                ptx::smem_desc(base + C::BUF_OFF + buf * C::BUF_BYTES, 16, 1024, ptx::SW_128B);
-            ptx::mma_f16_pair_tmem_a_k64(d, tmem_base + C::OP_COL + buf * 32, rdesc, idesc, kb == 0 ? 1u : 0u);
-            ptx::mma_commit_pair_mc(ope_bar(buf), 0x3);
-          }
+      while (ok && units.next(un, ok)) {
+        const uint32_t idesc = ptx::idesc_f16(256, un.n());
+        if (!(ok = wait(acce + 8u * abuf, aphase ^ 1u, WAIT_MMA_ACC_EMPTY))) break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem_base + abuf * C::ACC_COLS;
+        for (int kb = 0; kb < 2 * nk; ++kb, ++step) {
+          const uint32_t buf = step % C::BUFS, slot = step % C::A_STAGES;
+          ok = wait(rows_bar(slot), step / C::A_STAGES & 1u, WAIT_MMA_FULL) &&
+               wait(op_bar(buf), step / C::BUFS & 1u, WAIT_MMA_FULL);
           if (!ok) break;
-          ptx::mma_commit_pair_mc(accf + 8u * abuf, 0x3);
-          if (++abuf == 2) {
-            abuf = 0;
-            aphase ^= 1u;
-          }
+          ptx::tc_fence_after();
+          const uint64_t rdesc = ptx::smem_desc(base + C::A_OFF + slot * C::A_BYTES, 16, 1024, ptx::SW_128B);
+          ptx::mma_f16_pair_tmem_a_k64(d, tmem_base + C::OP_COL + buf * 32, rdesc, idesc, kb == 0 ? 1u : 0u);
+          ptx::mma_commit_pair_mc(done_bar(slot), 0x3);
         }
-        ptx::mma_commit_pair_mc(drain_bar, 0x1);
-        wait_quiet(drain_bar, 0, p.timeout_ns);
-      } else {
-        // ---------------------------------------------------------- announces this CTA's operands
-        while (ok && units.next(un, ok)) {
-          for (int kb = 0; kb < 2 * nk; ++kb, ++step) {
-            const uint32_t buf = step % C::BUFS, parity = (step / C::BUFS) & 1u;
-            if (!(ok = wait(opf_bar(buf), parity, WAIT_MMA_FULL))) break;
-            ptx::tc_fence_after();
-            ptx::tc_fence_before();
-            ptx::fence_release_shared_cluster();
-            ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(peer_bar(buf), 0));
-          }
+        if (!ok) break;
+        ptx::mma_commit_pair_mc(accf + 8u * abuf, 0x3);
+        if (++abuf == 2) {
+          abuf = 0;
+          aphase ^= 1u;
         }
       }
+      ptx::mma_commit_pair_mc(drain_bar, 0x1);
+      wait_quiet(drain_bar, 0, p.timeout_ns);
     }
     __syncwarp();
   } else if (warp == C::UNIT_WARP) {
@@ -490,17 +399,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else {
     // ------------------------------------------------------------ copies of rows (both CTAs)
     // As in the BF16 kernel: rows past the tile's end are not copied, and every
-    // thread arrives for every stage.
+    // thread arrives for every step.
     const int w = warp - C::LOAD_WARP;
     if (w < loaders && ptx::elect_one()) {
-      constexpr int PER = C::NT / 8 / C::LOAD_WARPS;  // gathers of a warp per stage
-      uint32_t stage = 0, phase = 0;
+      constexpr int PER = C::NT / 8 / C::LOAD_WARPS;  // gathers of a warp per step
+      uint32_t step = 0;
       bool ok = true;
       GroupedUnits<true> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
       GroupedUnit un;
       while (ok && units.next(un, ok)) {
         const int row0 = un.row0 + static_cast<int>(rank) * (un.n() >> 1);
         const int rows = un.rows_of(static_cast<int>(rank));
+        const uint32_t bytes = un.row_bytes(0, gather) + un.row_bytes(1, gather);  // of both CTAs
         // the last group of four repeats the tile's last row
         int idx[PER][4];
         if (gather) {
@@ -512,10 +422,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               idx[j][i] = min(max(__ldg(p.rows + at), 0), p.T - 1);
             }
         }
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!(ok = wait(empty_bar(stage), phase ^ 1u, WAIT_PRODUCER_EMPTY))) break;
-          const uint32_t sa = base + stage * C::STAGE_BYTES + C::W_BYTES;
-          const uint32_t fb = ptx::mapa_shared(full_bar(stage), rank);
+        for (int kb = 0; kb < 2 * nk; ++kb, ++step) {
+          const uint32_t slot = step % C::A_STAGES;
+          if (!(ok = wait(done_bar(slot), (step / C::A_STAGES & 1u) ^ 1u, WAIT_PRODUCER_EMPTY))) break;
+          const uint32_t sa = base + C::A_OFF + slot * C::A_BYTES;
+          const uint32_t fb = ptx::mapa_shared(rows_bar(slot), 0);
+          if (rank == 0 && w == 0) ptx::mbar_arrive_expect_tx(rows_bar(slot), bytes);
           ptx::mbar_arrive_cluster_relaxed(fb);
           if (gather) {
 #pragma unroll
@@ -529,15 +441,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             ptx::tma_load_2d_pair(sa, &tmA2, fb, kb * C::BK, row0);
           } else {
             for (int i = 0; i < rows; i += 32)
-              ptx::tma_load_2d_pair(sa + i * C::BK, &tmA, fb, kb * C::BK, row0 + i);
-          }
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+              ptx::tma_load_2d_pair(sa + i * C::BK * 2, &tmA, fb, kb * C::BK, row0 + i);
           }
         }
       }
-      if (!ok) spin_ns(100000);  // aborted: copies already in flight into this CTA land
+      if (!ok) {
+        spin_ns(100000);  // aborted: copies already in flight into this CTA land
+      } else if (w == 0) {
+        // Consume the MMA's arrivals still due on this CTA's barriers, so that none
+        // targets this CTA after it exits.
+        for (uint32_t i = step < C::A_STAGES ? 0 : step - C::A_STAGES; i < step; ++i)
+          wait_quiet(done_bar(i % C::A_STAGES), i / C::A_STAGES & 1u, p.timeout_ns);
+      }
     }
     __syncwarp();
   }

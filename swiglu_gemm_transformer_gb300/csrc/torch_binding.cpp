@@ -273,10 +273,10 @@ PyObject *quant_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// (A, a_scale, W1, s1, W2 or None, s2 or None, offsets or None, rows or None, Y or None, stream)
+// (A, a_scale, W1, s1, W2 or None, s2 or None, offsets or None, rows or None, Y or None, workspace or None, stream)
 PyObject *int8_product(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
-    if (n != 10) refuse(PyExc_TypeError, "int8_product takes 10 arguments");
+    if (n != 11) refuse(PyExc_TypeError, "int8_product takes 11 arguments");
     const bool fused = a[4] != Py_None, grouped = a[6] != Py_None;
     Call c{grouped ? (fused ? "swiglu_fused_grouped_int8" : "swiglu_linear_grouped_int8")
                    : (fused ? "swiglu_fused_int8" : "swiglu_linear_int8")};
@@ -306,19 +306,30 @@ PyObject *int8_product(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t P = rows ? rows->numel() : T;
     const c10::cuda::CUDAGuard on(static_cast<c10::DeviceIndex>(c.device));
     c10::cuda::OptionalCUDAStreamGuard pool;
-    void *s = c.enter(a[9], pool);
+    void *s = c.enter(a[10], pool);
     Tensor Y = c.output(a[8], "the output", ScalarType::BFloat16, {P, N});
+    uint64_t bytes = N > 0 ? swiglu_int8_workspace_size(T, P, K) : 0;
+    Tensor ws;
+    if (a[9] != Py_None) {
+      ws = c.tensor(a[9], "workspace", 1);
+      bytes = ws.nbytes();
+    } else if (bytes > 0) {
+      ws = c.output(Py_None, "workspace", ScalarType::Byte, {static_cast<int64_t>(bytes)});
+    }
+    void *wp = ws.defined() ? ws.data_ptr() : nullptr;
     // (an empty tensor has no address: any other stands for "rows are given")
     const int32_t *o = grouped ? ptr<int32_t>(*offsets) : nullptr;
     const int32_t *r = !rows ? nullptr : P > 0 ? ptr<int32_t>(*rows) : o;
     const void *w1 = W1.data_ptr(), *w2 = W2.data_ptr();
     const float *fa = ptr<float>(sa), *f1 = ptr<float>(s1), *f2 = ptr<float>(s2);
     c.check(unlocked([&] {
+      const void *x = A.data_ptr();
+      void *y = Y.data_ptr();
       if (!grouped)
-        return fused ? swiglu_fused_int8(A.data_ptr(), fa, w1, f1, w2, f2, Y.data_ptr(), T, N, K, s)
-                     : swiglu_linear_int8(A.data_ptr(), fa, w1, f1, Y.data_ptr(), T, N, K, s);
-      return fused ? swiglu_fused_grouped_int8(A.data_ptr(), fa, w1, f1, w2, f2, o, r, Y.data_ptr(), T, P, E, N, K, s)
-                   : swiglu_linear_grouped_int8(A.data_ptr(), fa, w1, f1, o, r, Y.data_ptr(), T, P, E, N, K, s);
+        return fused ? swiglu_fused_int8(x, fa, w1, f1, w2, f2, y, T, N, K, wp, bytes, s)
+                     : swiglu_linear_int8(x, fa, w1, f1, y, T, N, K, wp, bytes, s);
+      return fused ? swiglu_fused_grouped_int8(x, fa, w1, f1, w2, f2, o, r, y, T, P, E, N, K, wp, bytes, s)
+                   : swiglu_linear_grouped_int8(x, fa, w1, f1, o, r, y, T, P, E, N, K, wp, bytes, s);
     }));
     return THPVariable_Wrap(std::move(Y));
   });

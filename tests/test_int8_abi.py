@@ -52,14 +52,23 @@ def test_quant_refusals(lib, kw, want):
     assert _quant(lib, **kw) == want
 
 
-def _product(lib, fused, grouped, A_=A, sa=B, W1=C, s1=D, W2=E, s2=F, off=G, rows=H, Y=I, T=64, P=128, E_=8, N=64, K=64):
+def _product(lib, fused, grouped, A_=A, sa=B, W1=C, s1=D, W2=E, s2=F, off=G, rows=H, Y=I, T=64, P=128, E_=8, N=64, K=64, ws=J,
+             nbytes=1 << 20):
     if grouped:
         if fused:
-            return lib.swiglu_fused_grouped_int8(A_, sa, W1, s1, W2, s2, off, rows, Y, T, P, E_, N, K, None)
-        return lib.swiglu_linear_grouped_int8(A_, sa, W1, s1, off, rows, Y, T, P, E_, N, K, None)
+            return lib.swiglu_fused_grouped_int8(A_, sa, W1, s1, W2, s2, off, rows, Y, T, P, E_, N, K, ws, nbytes, None)
+        return lib.swiglu_linear_grouped_int8(A_, sa, W1, s1, off, rows, Y, T, P, E_, N, K, ws, nbytes, None)
     if fused:
-        return lib.swiglu_fused_int8(A_, sa, W1, s1, W2, s2, Y, T, N, K, None)
-    return lib.swiglu_linear_int8(A_, sa, W1, s1, Y, T, N, K, None)
+        return lib.swiglu_fused_int8(A_, sa, W1, s1, W2, s2, Y, T, N, K, ws, nbytes, None)
+    return lib.swiglu_linear_int8(A_, sa, W1, s1, Y, T, N, K, ws, nbytes, None)
+
+
+def test_workspace_size(lib):
+    assert lib.swiglu_int8_workspace_size(64, 128, 64) == 64 * 64 * 2   # A's rows
+    assert lib.swiglu_int8_workspace_size(128, 64, 64) == 64 * 64 * 2   # the places'
+    for T, P, K in ((1, 8, 64), (0, 64, 64), (64, 0, 64), (64, 64, 0), (-1, 64, 64), (64, -1, 64), (64, 64, -16), (1 << 31, 64, 64),
+                    (64, 1 << 31, 64), (64, 64, 1 << 22)):
+        assert lib.swiglu_int8_workspace_size(T, P, K) == 0
 
 
 FUSED = pytest.mark.parametrize("fused", [True, False], ids=["fused", "linear"])
@@ -74,6 +83,8 @@ GROUPED = pytest.mark.parametrize("grouped", [True, False], ids=["grouped", "den
     (dict(N=1 << 20, K=1 << 21), UNS), (dict(N=60), MIS), (dict(K=56), MIS), (dict(A_=A + 8), MIS), (dict(W1=C + 8), MIS),
     (dict(sa=B + 2), MIS), (dict(s1=D + 1), MIS), (dict(Y=I + 8), MIS),
     (dict(Y=A), INV), (dict(Y=B - 64), INV), (dict(Y=C + 64), INV), (dict(Y=D), INV),   # overlaps
+    (dict(ws=None), INV), (dict(nbytes=64 * 64 * 2 - 1), INV), (dict(ws=J + 8), MIS), (dict(ws=A), INV), (dict(ws=I - 64), INV),
+    (dict(ws=B - 4096), INV), (dict(ws=C + 64), INV), (dict(ws=D), INV),
     (dict(N=0), OK),
 ])
 def test_product_refusals(lib, fused, grouped, kw, want):
