@@ -153,9 +153,9 @@ int run_tensor(const Int8Call &c, uint32_t *err, int sms, uint64_t timeout_ns, u
   const bool gather = c.rows && c.P > c.T;
   const uint64_t R = uint64_t(std::min(c.T, c.P)), E = c.E, N = c.N, K = c.K;
   const uint64_t adim[2] = {K, R}, astr[1] = {K * 2};
-  const uint32_t abox[2] = {Fused::BK, gather ? 1u : 32u}, abox2[2] = {Fused::BK, NT / 2};
+  const uint32_t abox[2] = {64, gather ? 1u : 32u}, abox2[2] = {64, NT / 2};
   const uint64_t wdim[3] = {K, N, E}, wstr[2] = {K, N * K};
-  const uint32_t wbox[3] = {Fused::W_BK, 64, 1};
+  const uint32_t wbox[3] = {Fused::BK, 64, 1};
   int rc = encode_bf16_map(&t.a, c.workspace, 2, adim, astr, abox);  // (16-bit elements)
   if (!gather && rc == SWIGLU_OK) rc = encode_bf16_map(&t.a2, c.workspace, 2, adim, astr, abox2);
   if (rc == SWIGLU_OK) rc = encode_u8_map(&t.w1, c.W1, 3, wdim, wstr, wbox);
@@ -174,7 +174,7 @@ int run_tensor(const Int8Call &c, uint32_t *err, int sms, uint64_t timeout_ns, u
   p.E = int32_t(c.E);
   p.N = int32_t(c.N);
   p.gather = gather;
-  p.num_k_blk = int32_t(ceil_div(c.K, Fused::W_BK));
+  p.num_k_blk = int32_t(ceil_div(c.K, Fused::BK));
   p.num_n_blk = int32_t(ceil_div(c.N, c.fused ? 128 : 256));
   p.timeout_ns = timeout_ns;
   p.err = err;

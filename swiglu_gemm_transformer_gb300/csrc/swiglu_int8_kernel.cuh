@@ -13,13 +13,16 @@
 //     16-bit operands, and widened straight into tensor memory, as the MMA's A
 //     operand: K-major codes give a thread its lane's K in 16-byte loads, and
 //     shared memory, which feeds copies, loads and the MMA's B operand alike, is
-//     spared their 16-bit form.  Groups of four warps take K steps of 64 in turn;
+//     spared their 16-bit form.  Groups of four warps take halves of 64 of K in
+//     turn;
 //   * the rows come as FP16, widened once per call by a small kernel before this
 //     one (k_int8.cu): widened here they cost as many instructions as the
 //     weights, once for each column tile (7B projection, 2047 rows: MEASURE);
-//   * accumulators of 192 columns, double-buffered, leave 128 columns for
-//     four K steps of weights.  A buffer of them is freed, filled, announced and
-//     read in turn, so the codes are widened before the wait for it;
+//   * accumulators of 192 columns, double-buffered, leave 128 columns for two
+//     steps of weights, of 128 of K each.  A buffer of them is freed, filled,
+//     announced and read in turn, so the codes are widened before the wait for
+//     it.  Steps of 64 (four buffers) were bound by the MMA's thread, which a
+//     commit holds up for about 230 cycles: 480 a step however few rows it had;
 //   * FUSED: gate and up of a column lie in lanes 2j and 2j ^ 9 of one warp (odd
 //     lanes take the up columns, in an order that keeps the loads of eight
 //     lanes on different banks), so shuffles bring them together.
@@ -44,7 +47,7 @@ struct Int8Params {
   __nv_bfloat16 *Y;           // [P, N]
   int32_t T, P, E, N;         // rows of A, rows of Y, experts, output columns
   int32_t gather;             // 1: the FP16 rows are A's; 0: they are in the places' order
-  int32_t num_k_blk, num_n_blk;  // stages of codes, column tiles
+  int32_t num_k_blk, num_n_blk;  // K steps, column tiles
   uint64_t timeout_ns;
   uint32_t *err;
 };
@@ -53,15 +56,15 @@ template <bool FUSED_>
 struct Int8Cfg {
   static constexpr bool FUSED = FUSED_;
   static constexpr int NT = 192;                 // most rows of a tile
-  static constexpr int BK = 64;                  // K of a step
+  static constexpr int BK = 128;                 // K of a step
   static constexpr int COLS = FUSED ? 64 : 128;  // output columns per CTA
-  static constexpr int W_BK = 128;               // K of a stage of codes
-  static constexpr int BOX_BYTES = 64 * W_BK;    // 64 columns' codes
+  static constexpr int BOX_BYTES = 64 * BK;      // 64 columns' codes
   static constexpr int W_BYTES = 2 * BOX_BYTES;  // W1 | W2, or two boxes of W
   static constexpr int W_STAGES = 6;
-  static constexpr int A_BYTES = NT / 2 * BK * 2;  // a step's rows (FP16)
-  static constexpr int A_STAGES = 8;
-  static constexpr int BUFS = 4;                 // widened weights, a step each
+  static constexpr int HALF_BYTES = NT / 2 * 64 * 2;  // the rows' FP16 values, 64 of K
+  static constexpr int A_BYTES = 2 * HALF_BYTES;
+  static constexpr int A_STAGES = 4;
+  static constexpr int BUFS = 2;                 // widened weights, a step each
   static constexpr int EPI_WARPS = 8;
   // one epilogue warp's block: 16 rows x 32 columns BF16 (rows 80 bytes apart:
   // 16-byte reads of eight rows touch every bank once), FUSED 16 x 16 (48 apart)
@@ -84,9 +87,9 @@ struct Int8Cfg {
   static constexpr int LOAD_WARPS = 8;
   static constexpr int THREADS = 32 * (LOAD_WARP + LOAD_WARPS);
   static constexpr int ACC_COLS = NT;            // TMEM columns of one accumulator buffer
-  static constexpr int OP_COL = 2 * ACC_COLS;    // then the widened weights, 32 columns a step
+  static constexpr int OP_COL = 2 * ACC_COLS;    // then the widened weights, 64 columns a step
   static constexpr int GROUP = 8;
-  static_assert(OP_COL + BUFS * 32 == 512, "tensor memory");
+  static_assert(OP_COL + BUFS * 64 == 512, "tensor memory");
   static_assert(A_STAGES % BUFS == 0, "one arrival frees rows and weights");
   static_assert(NT / 8 % LOAD_WARPS == 0, "gathers split evenly");
   static_assert(THREADS <= 1024, "threads");
@@ -148,13 +151,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   if (warp == C::PRODUCER_WARP && lane == 0) {
     for (int s = 0; s < C::W_STAGES; ++s) {
       ptx::mbar_init(full_bar(s), 1);
-      ptx::mbar_init(empty_bar(s), 8);  // four warps for each step
+      ptx::mbar_init(empty_bar(s), 8);  // four warps for each half
     }
     for (int s = 0; s < C::A_STAGES; ++s) {
       ptx::mbar_init(rows_bar(s), 1 + 2 * loaders);
       ptx::mbar_init(done_bar(s), 1);
     }
-    for (int b = 0; b < C::BUFS; ++b) ptx::mbar_init(op_bar(b), 8);  // four warps of each CTA
+    for (int b = 0; b < C::BUFS; ++b) ptx::mbar_init(op_bar(b), 16);  // the same, of both CTAs
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(accf + 8u * b, 1);
       ptx::mbar_init(acce + 8u * b, 2 * C::EPI_WARPS);
@@ -293,21 +296,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // the lane's row of codes: a column of W1 or W2 (FUSED), of either half of W
     const int col = C::FUSED ? 16 * q + ((lane >> 1) ^ (lane & 1 ? 4 : 0)) : (32 * q + lane) & 63;
     const int box = C::FUSED ? lane & 1 : q >> 1;
-    const uint32_t src = base + box * C::BOX_BYTES + col * C::W_BK;
+    const uint32_t src = base + box * C::BOX_BYTES + col * C::BK;
     const uint32_t dst = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + C::OP_COL;
-    uint32_t step = (warp - C::W_WARP) >> 2, end = 0;  // this group's steps: every W_GROUPS-th
+    uint32_t half = (warp - C::W_WARP) >> 2, end = 0;  // this group's half steps: every W_GROUPS-th
     bool ok = true;
     GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
     GroupedUnit un;
     while (ok && units.next(un, ok)) {
-      for (end += 2 * nk; step < end; step += C::W_GROUPS) {
-        const uint32_t buf = step % C::BUFS, stage = step / 2 % C::W_STAGES;
-        ok = __all_sync(0xffffffffu, wait(full_bar(stage), step / 2 / C::W_STAGES & 1u, WAIT_MMA_FULL));
+      for (end += 2 * nk; half < end; half += C::W_GROUPS) {
+        const uint32_t step = half / 2, buf = step % C::BUFS, stage = step % C::W_STAGES;
+        ok = __all_sync(0xffffffffu, wait(full_bar(stage), step / C::W_STAGES & 1u, WAIT_MMA_FULL));
         if (!ok) break;
         uint32_t o[32];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const uint4 v = lds128(src + stage * C::W_BYTES + (((4 * (step & 1u) + t) ^ (col & 7)) << 4));
+          const uint4 v = lds128(src + stage * C::W_BYTES + (((4 * (half & 1u) + t) ^ (col & 7)) << 4));
           widen4(v.x, o[8 * t], o[8 * t + 1]);
           widen4(v.y, o[8 * t + 2], o[8 * t + 3]);
           widen4(v.z, o[8 * t + 4], o[8 * t + 5]);
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (!ok) break;
           ptx::tc_fence_after();
         }
-        ptx::tmem_st32(dst + buf * 32, o);
+        ptx::tmem_st32(dst + buf * 64 + (half & 1u) * 32, o);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
@@ -344,11 +347,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint32_t sw = base + stage * C::W_BYTES;
           const uint32_t fb = ptx::mapa_shared(full_bar(stage), rank);
           ptx::mbar_arrive_expect_tx(full_bar(stage), C::W_BYTES);
-          ptx::tma_load_3d_pair(sw, &tmW1, fb, kb * C::W_BK, col0, un.e);
+          ptx::tma_load_3d_pair(sw, &tmW1, fb, kb * C::BK, col0, un.e);
           if (C::FUSED)
-            ptx::tma_load_3d_pair(sw + C::BOX_BYTES, &tmW2, fb, kb * C::W_BK, col0, un.e);
+            ptx::tma_load_3d_pair(sw + C::BOX_BYTES, &tmW2, fb, kb * C::BK, col0, un.e);
           else
-            ptx::tma_load_3d_pair(sw + C::BOX_BYTES, &tmW1, fb, kb * C::W_BK, col0 + 64, un.e);
+            ptx::tma_load_3d_pair(sw + C::BOX_BYTES, &tmW1, fb, kb * C::BK, col0 + 64, un.e);
           if (++stage == C::W_STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -370,14 +373,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!(ok = wait(acce + 8u * abuf, aphase ^ 1u, WAIT_MMA_ACC_EMPTY))) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + abuf * C::ACC_COLS;
-        for (int kb = 0; kb < 2 * nk; ++kb, ++step) {
+        for (int kb = 0; kb < nk; ++kb, ++step) {
           const uint32_t buf = step % C::BUFS, slot = step % C::A_STAGES;
           ok = wait(rows_bar(slot), step / C::A_STAGES & 1u, WAIT_MMA_FULL) &&
                wait(op_bar(buf), step / C::BUFS & 1u, WAIT_MMA_FULL);
           if (!ok) break;
           ptx::tc_fence_after();
+          const uint32_t op = tmem_base + C::OP_COL + buf * 64;
           const uint64_t rdesc = ptx::smem_desc(base + C::A_OFF + slot * C::A_BYTES, 16, 1024, ptx::SW_128B);
-          ptx::mma_f16_pair_tmem_a_k64(d, tmem_base + C::OP_COL + buf * 32, rdesc, idesc, kb == 0 ? 1u : 0u);
+          ptx::mma_f16_pair_tmem_a_k64(d, op, rdesc, idesc, kb == 0 ? 1u : 0u);
+          ptx::mma_f16_pair_tmem_a_k64(d, op + 32, rdesc + C::HALF_BYTES / 16, idesc, 0u);
           ptx::mma_commit_pair_mc(done_bar(slot), 0x3);
         }
         if (!ok) break;
@@ -410,7 +415,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       while (ok && units.next(un, ok)) {
         const int row0 = un.row0 + static_cast<int>(rank) * (un.n() >> 1);
         const int rows = un.rows_of(static_cast<int>(rank));
-        const uint32_t bytes = un.row_bytes(0, gather) + un.row_bytes(1, gather);  // of both CTAs
+        const uint32_t bytes = 2 * (un.row_bytes(0, gather) + un.row_bytes(1, gather));  // of both CTAs
         // the last group of four repeats the tile's last row
         int idx[PER][4];
         if (gather) {
@@ -422,26 +427,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               idx[j][i] = min(max(__ldg(p.rows + at), 0), p.T - 1);
             }
         }
-        for (int kb = 0; kb < 2 * nk; ++kb, ++step) {
+        for (int kb = 0; kb < nk; ++kb, ++step) {
           const uint32_t slot = step % C::A_STAGES;
           if (!(ok = wait(done_bar(slot), (step / C::A_STAGES & 1u) ^ 1u, WAIT_PRODUCER_EMPTY))) break;
-          const uint32_t sa = base + C::A_OFF + slot * C::A_BYTES;
           const uint32_t fb = ptx::mapa_shared(rows_bar(slot), 0);
           if (rank == 0 && w == 0) ptx::mbar_arrive_expect_tx(rows_bar(slot), bytes);
           ptx::mbar_arrive_cluster_relaxed(fb);
-          if (gather) {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) {
-              const int g = w + j * C::LOAD_WARPS;
-              if (4 * g < rows)
-                ptx::tma_gather4_pair(sa + g * 512, &tmA, fb, kb * C::BK, idx[j][0], idx[j][1], idx[j][2],
-                                      idx[j][3]);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sa = base + C::A_OFF + slot * C::A_BYTES + h * C::HALF_BYTES;
+            const int k = kb * C::BK + 64 * h;
+            if (gather) {
+#pragma unroll
+              for (int j = 0; j < PER; ++j) {
+                const int g = w + j * C::LOAD_WARPS;
+                if (4 * g < rows)
+                  ptx::tma_gather4_pair(sa + g * 512, &tmA, fb, k, idx[j][0], idx[j][1], idx[j][2], idx[j][3]);
+              }
+            } else if (rows > C::NT / 2 - 32) {
+              ptx::tma_load_2d_pair(sa, &tmA2, fb, k, row0);
+            } else {
+              for (int i = 0; i < rows; i += 32) ptx::tma_load_2d_pair(sa + i * 128, &tmA, fb, k, row0 + i);
             }
-          } else if (rows > C::NT / 2 - 32) {
-            ptx::tma_load_2d_pair(sa, &tmA2, fb, kb * C::BK, row0);
-          } else {
-            for (int i = 0; i < rows; i += 32)
-              ptx::tma_load_2d_pair(sa + i * C::BK * 2, &tmA, fb, kb * C::BK, row0 + i);
           }
         }
       }
