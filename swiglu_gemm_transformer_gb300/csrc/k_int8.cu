@@ -122,19 +122,23 @@ cudaError_t launch_tensor(TensorLaunch &t) {
   cfg.stream = t.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;  // the occupancy query takes the cluster shape only
+  if (C::SPLIT) attr[0].val.clusterDim.x = 2 * t.p.pairs;
   if (once.needed(t.device, t.ctx_gen)) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(2 * 64, 1, 1);
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-    if (e != cudaSuccess) return e;
-    if (n < 1) return cudaErrorInvalidConfiguration;
-    max_clusters[t.device & 63] = n;
+    if (!C::SPLIT) {
+      cfg.gridDim = dim3(2 * 64, 1, 1);
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < 1) return cudaErrorInvalidConfiguration;
+      max_clusters[t.device & 63] = n;
+    }
     once.done(t.device, t.ctx_gen);
   }
-  // a persistent grid of pairs
-  cfg.gridDim = dim3(2 * unsigned(std::min<int64_t>(t.units, max_clusters[t.device & 63])), 1, 1);
+  // SPLIT: a cluster per unit; else a persistent grid of pairs
+  const int64_t clusters = C::SPLIT ? t.units : std::min<int64_t>(t.units, max_clusters[t.device & 63]);
+  cfg.gridDim = dim3(unsigned(clusters) * attr[0].val.clusterDim.x, 1, 1);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, t.a, t.a2, t.w1, t.w2, t.p);
 }
@@ -142,7 +146,7 @@ cudaError_t launch_tensor(TensorLaunch &t) {
 // The tensor-core form.
 int run_tensor(const Int8Call &c, uint32_t *err, int sms, uint64_t timeout_ns, uint64_t ctx_gen) {
   using Fused = Int8Cfg<true>;
-  constexpr int NT = Fused::NT;
+  using Split = Int8Cfg<true, true>;
   TensorLaunch t;
   std::memset(&t, 0, sizeof t);
   t.stream = static_cast<cudaStream_t>(c.stream);
@@ -152,8 +156,15 @@ int run_tensor(const Int8Call &c, uint32_t *err, int sms, uint64_t timeout_ns, u
   // the kernel gathers.
   const bool gather = c.rows && c.P > c.T;
   const uint64_t R = uint64_t(std::min(c.T, c.P)), E = c.E, N = c.N, K = c.K;
+  const int32_t k_blk = int32_t(ceil_div(c.K, Fused::BK)), n_blk = int32_t(ceil_div(c.N, c.fused ? 128 : 256));
+  auto units = [&](int nt) { return (c.offsets ? std::min(c.E, c.P) + c.P / nt : ceil_div(c.P, nt)) * n_blk; };
+  // Few units and enough K to share: several pairs to a unit.  A cluster of four
+  // or eight CTAs fits the GPU 36 or 15 times.  (MEASURE)
+  const int64_t few = units(Split::NT);
+  const int pairs = few > 36 || k_blk < 8 ? 1 : few > 15 ? 2 : Split::MAX_PAIRS;
+  const int nt = pairs > 1 ? Split::NT : Fused::NT;
   const uint64_t adim[2] = {K, R}, astr[1] = {K * 2};
-  const uint32_t abox[2] = {64, gather ? 1u : 32u}, abox2[2] = {64, NT / 2};
+  const uint32_t abox[2] = {64, gather ? 1u : 32u}, abox2[2] = {64, uint32_t(nt / 2)};
   const uint64_t wdim[3] = {K, N, E}, wstr[2] = {K, N * K};
   const uint32_t wbox[3] = {Fused::BK, 64, 1};
   int rc = encode_bf16_map(&t.a, c.workspace, 2, adim, astr, abox);  // (16-bit elements)
@@ -174,12 +185,15 @@ int run_tensor(const Int8Call &c, uint32_t *err, int sms, uint64_t timeout_ns, u
   p.E = int32_t(c.E);
   p.N = int32_t(c.N);
   p.gather = gather;
-  p.num_k_blk = int32_t(ceil_div(c.K, Fused::BK));
-  p.num_n_blk = int32_t(ceil_div(c.N, c.fused ? 128 : 256));
+  p.num_k_blk = k_blk;
+  p.num_n_blk = n_blk;
   p.timeout_ns = timeout_ns;
   p.err = err;
-  t.units = (c.offsets ? std::min(c.E, c.P) + c.P / NT : ceil_div(c.P, NT)) * p.num_n_blk;
-  const cudaError_t e = c.fused ? launch_tensor<Fused>(t) : launch_tensor<Int8Cfg<false>>(t);
+  p.pairs = pairs;
+  t.units = units(nt);
+  const cudaError_t e = pairs > 1 ? c.fused ? launch_tensor<Int8Cfg<true, true>>(t) : launch_tensor<Int8Cfg<false, true>>(t)
+                        : c.fused ? launch_tensor<Fused>(t)
+                                  : launch_tensor<Int8Cfg<false>>(t);
   return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
 }
 

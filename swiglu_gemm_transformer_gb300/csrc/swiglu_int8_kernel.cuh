@@ -26,6 +26,10 @@
 //   * FUSED: gate and up of a column lie in lanes 2j and 2j ^ 9 of one warp (odd
 //     lanes take the up columns, in an order that keeps the loads of eight
 //     lanes on different banks), so shuffles bring them together.
+// SPLIT: for calls of so few units that most SMs would stand idle: the pairs of a
+// cluster share one unit's K; then each finishes a part of its rows, to whose
+// sums it adds the others', in order, from its shared memory (the rings, idle by
+// then).  With one pair finishing all 125 rows a call took 15.4 us, 12.8 so.
 // Every wait is bounded as in the other kernels.
 #pragma once
 
@@ -48,14 +52,17 @@ struct Int8Params {
   int32_t T, P, E, N;         // rows of A, rows of Y, experts, output columns
   int32_t gather;             // 1: the FP16 rows are A's; 0: they are in the places' order
   int32_t num_k_blk, num_n_blk;  // K steps, column tiles
+  int32_t pairs;                 // SPLIT: pairs of a cluster, at most num_k_blk
   uint64_t timeout_ns;
   uint32_t *err;
 };
 
-template <bool FUSED_>
+template <bool FUSED_, bool SPLIT_ = false>
 struct Int8Cfg {
   static constexpr bool FUSED = FUSED_;
-  static constexpr int NT = 192;                 // most rows of a tile
+  static constexpr bool SPLIT = SPLIT_;
+  static constexpr int MAX_PAIRS = 4;            // SPLIT: pairs of a cluster
+  static constexpr int NT = SPLIT ? 128 : 192;   // most rows of a tile
   static constexpr int BK = 128;                 // K of a step
   static constexpr int COLS = FUSED ? 64 : 128;  // output columns per CTA
   static constexpr int BOX_BYTES = 64 * BK;      // 64 columns' codes
@@ -86,10 +93,12 @@ struct Int8Cfg {
   static constexpr int LOAD_WARP = UNIT_WARP + 1;  // first of those that copy rows
   static constexpr int LOAD_WARPS = 8;
   static constexpr int THREADS = 32 * (LOAD_WARP + LOAD_WARPS);
-  static constexpr int ACC_COLS = NT;            // TMEM columns of one accumulator buffer
+  static constexpr int ACC_COLS = 192;           // TMEM columns of one accumulator buffer
   static constexpr int OP_COL = 2 * ACC_COLS;    // then the widened weights, 64 columns a step
   static constexpr int GROUP = 8;
-  static_assert(OP_COL + BUFS * 64 == 512, "tensor memory");
+  static_assert(NT <= ACC_COLS && OP_COL + BUFS * 64 == 512, "tensor memory");
+  // (two pairs: one half of the rows from one other; four: a quarter from three)
+  static_assert(!SPLIT || NT * 128 * 4 <= STG_OFF, "sums fit the rings");
   static_assert(A_STAGES % BUFS == 0, "one arrival frees rows and weights");
   static_assert(NT / 8 % LOAD_WARPS == 0, "gathers split evenly");
   static_assert(THREADS <= 1024, "threads");
@@ -143,8 +152,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = ptx::cluster_ctarank();  // 0 = the pair's leader
-  const int nk = p.num_k_blk;
+  const uint32_t crank = ptx::cluster_ctarank();
+  const uint32_t lead = C::SPLIT ? crank & ~1u : 0u;  // cluster rank of this pair's leader
+  const uint32_t rank = crank - lead;                 // 0 = the pair's leader
+  const uint16_t both = static_cast<uint16_t>(0x3u << lead);  // the pair's CTAs, as a mask
+  const int kb0 = C::SPLIT ? p.num_k_blk * static_cast<int>(lead >> 1) / p.pairs : 0;
+  const int kb1 = C::SPLIT ? p.num_k_blk * static_cast<int>((lead >> 1) + 1) / p.pairs : p.num_k_blk;
   const bool gather = p.gather != 0;
   const int loaders = gather ? C::LOAD_WARPS : 1;
 
@@ -189,102 +202,129 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     return wait_bar(bar, parity, p.timeout_ns, abort_flag, p.err, where);
   };
 
-  if (warp < C::EPI_WARPS) {
-    // ------------------------------------------------------------ epilogue (both CTAs)
-    // Warp q (mod 4) reads TMEM lanes [32q, 32q + 32), the tile's rows in the
-    // columns; warps 0-3 take the even chunks of 16 rows, warps 4-7 the odd ones.
-    // Linear: lane i is output column 32q + i.  FUSED: see the head of the file.
-    const int q = warp & 3, h = warp >> 2;
-    const bool up = C::FUSED && (lane & 1);
-    const int lcol = C::FUSED ? (lane >> 1) ^ (up ? 4 : 0) : lane;  // the lane's column in the warp's
-    const int wcol = C::FUSED ? 16 * q : 32 * q;
-    const uint32_t stg = base + C::STG_OFF + warp * C::STG_BYTES;
-    uint32_t abuf = 0, aphase = 0;
-    GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
-    GroupedUnit un;
-    bool ok = true;
-    while (units.next(un, ok)) {
-      const int nchunk = un.n() / 16;
-      const int col0 = (un.nb * 2 + static_cast<int>(rank)) * C::COLS + wcol;
-      // scales of the lane's column, and of the rows of this warp's chunks: lane
-      // l, word j is row l % 16 of the warp's chunk 2 j + l / 16
-      float w1 = 0.0f, w2 = 0.0f, sa[3];
-      if (col0 + lcol < p.N) {
-        const int64_t at = int64_t(un.e) * p.N + col0 + lcol;
-        w1 = __ldg(p.s1 + at);
-        if (C::FUSED) w2 = __ldg(p.s2 + at);
-      }
-      unsigned named[3];  // which of those rows name a row of A
+  // ---- epilogue (warps 0-7, both CTAs) ----
+  // Warp q (mod 4) reads TMEM lanes [32q, 32q + 32), the tile's rows in the
+  // columns; warps 0-3 take the even chunks of 16 rows, warps 4-7 the odd ones.
+  // Linear: lane i is output column 32q + i.  FUSED: see the head of the file.
+  const int q = warp & 3, h = (warp >> 2) & 1;
+  const bool up = C::FUSED && (lane & 1);
+  const int lcol = C::FUSED ? (lane >> 1) ^ (up ? 4 : 0) : lane;  // the lane's column in the warp's
+  GroupedUnit mine = {-1, -1, 0, 0};  // the tile at hand
+  bool have = false;                  // SPLIT: its sums are complete
+  float w1 = 0.0f, w2 = 0.0f, sa[3];
+  unsigned named[3];
+  auto tile_col = [&] {  // the warp's first column
+    return (mine.nb * 2 + static_cast<int>(rank)) * C::COLS + (C::FUSED ? 16 * q : 32 * q);
+  };
+  // The scales of the lane's column, and of the rows of this warp's chunks: lane
+  // l, word j is row l % 16 of the warp's chunk 2 j + l / 16, and a bit that
+  // tells whether it names a row of A.
+  auto load_scales = [&] {
+    w1 = w2 = 0.0f;
+    if (tile_col() + lcol < p.N) {
+      const int64_t at = int64_t(mine.e) * p.N + tile_col() + lcol;
+      w1 = __ldg(p.s1 + at);
+      if (C::FUSED) w2 = __ldg(p.s2 + at);
+    }
 #pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const int row = un.row0 + 16 * (h + 2 * (2 * j + (lane >> 4))) + (lane & 15);
-        int src = -1;
-        if (row < un.end) src = p.rows ? __ldg(p.rows + row) : row;
-        const bool valid = src >= 0 && src < p.T;
-        sa[j] = valid ? __ldg(p.sa + src) : 0.0f;
-        named[j] = __ballot_sync(0xffffffffu, valid);
+    for (int j = 0; j < 3; ++j) {
+      const int row = mine.row0 + 16 * (h + 2 * (2 * j + (lane >> 4))) + (lane & 15);
+      int src = -1;
+      if (row < mine.end) src = p.rows ? __ldg(p.rows + row) : row;
+      const bool valid = src >= 0 && src < p.T;
+      sa[j] = valid ? __ldg(p.sa + src) : 0.0f;
+      named[j] = __ballot_sync(0xffffffffu, valid);
+    }
+  };
+  // SPLIT: the pair that finishes chunk c, and the chunk's number there.
+  auto owner = [&](int c) { return (c >> 1) % p.pairs; };
+  auto place = [&](int c) { return (c >> 1) / p.pairs * 2 + (c & 1); };
+  // Finishes and stores the tile, whose accumulator starts at `tacc`; arrives on
+  // `release` (cluster address) once the warp has read it.
+  auto finish = [&](uint32_t tacc, uint32_t release) {
+    const uint32_t stg = base + C::STG_OFF + warp * C::STG_BYTES;
+    const int nchunk = mine.n() / 16, col0 = tile_col();
+    if (!C::SPLIT && h >= nchunk) {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster_relaxed(release);
+    }
+#pragma unroll 1
+    for (int c = h, i = 0; c < nchunk; c += 2, ++i) {
+      if (C::SPLIT && owner(c) != static_cast<int>(lead >> 1)) continue;
+      uint32_t v[16];
+      ptx::tmem_ld16(tacc + c * 16, v);
+      ptx::tmem_wait_ld();
+      ptx::reg_fence(v);
+      if constexpr (C::SPLIT) {
+        const float *more = reinterpret_cast<const float *>(smem) + place(c) * 16 * 128 + q * 32 + lane;
+        for (int s = 1; s < p.pairs; ++s, more += C::NT / p.pairs * 128)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[r] = __float_as_uint(__uint_as_float(v[r]) + more[r * 128]);
       }
-      ok = __all_sync(0xffffffffu, wait(accf + 8u * abuf, aphase, WAIT_EPI_ACC_FULL));
-      if (!ok) break;
-      ptx::tc_fence_after();
-      const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * C::ACC_COLS;
-      const uint32_t release = ptx::mapa_shared(acce + 8u * abuf, 0);
-      if (h >= nchunk) {
+      if (!C::SPLIT && c + 2 >= nchunk) {
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster_relaxed(release);
       }
-#pragma unroll 1
-      for (int c = h, i = 0; c < nchunk; c += 2, ++i) {
-        uint32_t v[16];
-        ptx::tmem_ld16(tacc + c * 16, v);
-        ptx::tmem_wait_ld();
-        ptx::reg_fence(v);
-        if (c + 2 >= nchunk) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster_relaxed(release);
-        }
-        const float s16 = i < 2 ? sa[0] : i < 4 ? sa[1] : sa[2];
-        const unsigned ok16 = (i < 2 ? named[0] : i < 4 ? named[1] : named[2]) >> (16 * (i & 1));
-        if constexpr (C::FUSED) {
-          // even lanes finish the chunk's first 8 rows, odd lanes the last 8
-          const int first = up ? 8 : 0;
+      const float s16 = i < 2 ? sa[0] : i < 4 ? sa[1] : sa[2];
+      const unsigned ok16 = (i < 2 ? named[0] : i < 4 ? named[1] : named[2]) >> (16 * (i & 1));
+      if constexpr (C::FUSED) {
+        // even lanes finish the chunk's first 8 rows, odd lanes the last 8
+        const int first = up ? 8 : 0;
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const uint32_t give = up ? v[r] : v[8 + r];
-            const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, give, 9));
-            const float mine = __uint_as_float(up ? v[8 + r] : v[r]);
-            const float s = __shfl_sync(0xffffffffu, s16, 16 * (i & 1) + first + r);
-            const float y = silu_mul((up ? got : mine) * s * w1, (up ? mine : got) * s * w2);
-            const __nv_bfloat16 b = __float2bfloat16_rn(y);
-            // (rows 8-15 are 32 bytes further: their banks are not rows 0-7's)
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(stg + (first + r) * C::STG_PITCH + first * 4 + lcol * 2),
-                         "h"(*reinterpret_cast<const uint16_t *>(&b)) : "memory");
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float s = __shfl_sync(0xffffffffu, s16, 16 * (i & 1) + r);
-            const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(v[r]) * s * w1);
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(stg + r * C::STG_PITCH + lcol * 2),
-                         "h"(*reinterpret_cast<const uint16_t *>(&b)) : "memory");
-          }
+        for (int r = 0; r < 8; ++r) {
+          const uint32_t give = up ? v[r] : v[8 + r];
+          const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, give, 9));
+          const float mv = __uint_as_float(up ? v[8 + r] : v[r]);
+          const float s = __shfl_sync(0xffffffffu, s16, 16 * (i & 1) + first + r);
+          const float y = silu_mul((up ? got : mv) * s * w1, (up ? mv : got) * s * w2);
+          const __nv_bfloat16 b = __float2bfloat16_rn(y);
+          // (rows 8-15 are 32 bytes further: their banks are not rows 0-7's)
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(stg + (first + r) * C::STG_PITCH + first * 4 + lcol * 2),
+                       "h"(*reinterpret_cast<const uint16_t *>(&b)) : "memory");
         }
-        __syncwarp();
-        constexpr int PER_ROW = C::FUSED ? 2 : 4;  // 16-byte pieces
+      } else {
 #pragma unroll
-        for (int j = 0; j < PER_ROW / 2; ++j) {
-          const int t = j * (32 / PER_ROW) + lane / PER_ROW, col = col0 + lane % PER_ROW * 8;
-          const int row = un.row0 + c * 16 + t;
-          if (row < un.end && col < p.N) {
-            uint4 out = lds128(stg + t * C::STG_PITCH + (C::FUSED && t >= 8 ? 32 : 0) + lane % PER_ROW * 16);
-            if (!((ok16 >> t) & 1u)) out = make_uint4(0, 0, 0, 0);  // no row of A
-            *reinterpret_cast<uint4 *>(p.Y + int64_t(row) * p.N + col) = out;
-          }
+        for (int r = 0; r < 16; ++r) {
+          const float s = __shfl_sync(0xffffffffu, s16, 16 * (i & 1) + r);
+          const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(v[r]) * s * w1);
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(stg + r * C::STG_PITCH + lcol * 2),
+                       "h"(*reinterpret_cast<const uint16_t *>(&b)) : "memory");
         }
-        __syncwarp();
       }
+      __syncwarp();
+      constexpr int PER_ROW = C::FUSED ? 2 : 4;  // 16-byte pieces
+#pragma unroll
+      for (int j = 0; j < PER_ROW / 2; ++j) {
+        const int t = j * (32 / PER_ROW) + lane / PER_ROW, col = col0 + lane % PER_ROW * 8;
+        const int row = mine.row0 + c * 16 + t;
+        if (row < mine.end && col < p.N) {
+          uint4 out = lds128(stg + t * C::STG_PITCH + (C::FUSED && t >= 8 ? 32 : 0) + lane % PER_ROW * 16);
+          if (!((ok16 >> t) & 1u)) out = make_uint4(0, 0, 0, 0);  // no row of A
+          *reinterpret_cast<uint4 *>(p.Y + int64_t(row) * p.N + col) = out;
+        }
+      }
+      __syncwarp();
+    }
+  };
+
+  if (warp < C::EPI_WARPS) {
+    // ------------------------------------------------------------ epilogue
+    uint32_t abuf = 0, aphase = 0;
+    GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
+    bool ok = true;
+    while (units.next(mine, ok)) {
+      load_scales();
+      ok = __all_sync(0xffffffffu, wait(accf + 8u * abuf, aphase, WAIT_EPI_ACC_FULL));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if constexpr (C::SPLIT) {  // the only unit: its sums meet after the roles
+        have = true;
+        break;
+      }
+      finish(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * C::ACC_COLS,
+             ptx::mapa_shared(acce + 8u * abuf, lead));
       if (++abuf == 2) {
         abuf = 0;
         aphase ^= 1u;
@@ -292,7 +332,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   } else if (warp < C::PRODUCER_WARP) {
     // ------------------------------------------------------------ weights' codes into tensor memory (both CTAs)
-    const int q = warp & 3;
     // the lane's row of codes: a column of W1 or W2 (FUSED), of either half of W
     const int col = C::FUSED ? 16 * q + ((lane >> 1) ^ (lane & 1 ? 4 : 0)) : (32 * q + lane) & 63;
     const int box = C::FUSED ? lane & 1 : q >> 1;
@@ -303,7 +342,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
     GroupedUnit un;
     while (ok && units.next(un, ok)) {
-      for (end += 2 * nk; half < end; half += C::W_GROUPS) {
+      for (end += 2 * (kb1 - kb0); half < end; half += C::W_GROUPS) {
         const uint32_t step = half / 2, buf = step % C::BUFS, stage = step % C::W_STAGES;
         ok = __all_sync(0xffffffffu, wait(full_bar(stage), step / C::W_STAGES & 1u, WAIT_MMA_FULL));
         if (!ok) break;
@@ -329,7 +368,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ptx::tc_fence_before();
         __syncwarp();
         // (relaxed: the stores into tensor memory are complete)
-        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(op_bar(buf), 0));
+        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(op_bar(buf), lead));
       }
     }
     __syncwarp();
@@ -342,10 +381,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       GroupedUnit un;
       while (ok && units.next(un, ok)) {
         const int col0 = (un.nb * 2 + static_cast<int>(rank)) * C::COLS;
-        for (int kb = 0; kb < nk; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = wait(empty_bar(stage), phase ^ 1u, WAIT_PRODUCER_EMPTY))) break;
           const uint32_t sw = base + stage * C::W_BYTES;
-          const uint32_t fb = ptx::mapa_shared(full_bar(stage), rank);
+          const uint32_t fb = ptx::mapa_shared(full_bar(stage), crank);
           ptx::mbar_arrive_expect_tx(full_bar(stage), C::W_BYTES);
           ptx::tma_load_3d_pair(sw, &tmW1, fb, kb * C::BK, col0, un.e);
           if (C::FUSED)
@@ -373,7 +412,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!(ok = wait(acce + 8u * abuf, aphase ^ 1u, WAIT_MMA_ACC_EMPTY))) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + abuf * C::ACC_COLS;
-        for (int kb = 0; kb < nk; ++kb, ++step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++step) {
           const uint32_t buf = step % C::BUFS, slot = step % C::A_STAGES;
           ok = wait(rows_bar(slot), step / C::A_STAGES & 1u, WAIT_MMA_FULL) &&
                wait(op_bar(buf), step / C::BUFS & 1u, WAIT_MMA_FULL);
@@ -381,18 +420,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           ptx::tc_fence_after();
           const uint32_t op = tmem_base + C::OP_COL + buf * 64;
           const uint64_t rdesc = ptx::smem_desc(base + C::A_OFF + slot * C::A_BYTES, 16, 1024, ptx::SW_128B);
-          ptx::mma_f16_pair_tmem_a_k64(d, op, rdesc, idesc, kb == 0 ? 1u : 0u);
+          ptx::mma_f16_pair_tmem_a_k64(d, op, rdesc, idesc, kb == kb0 ? 1u : 0u);
           ptx::mma_f16_pair_tmem_a_k64(d, op + 32, rdesc + C::HALF_BYTES / 16, idesc, 0u);
-          ptx::mma_commit_pair_mc(done_bar(slot), 0x3);
+          ptx::mma_commit_pair_mc(done_bar(slot), both);
         }
         if (!ok) break;
-        ptx::mma_commit_pair_mc(accf + 8u * abuf, 0x3);
+        ptx::mma_commit_pair_mc(accf + 8u * abuf, both);
         if (++abuf == 2) {
           abuf = 0;
           aphase ^= 1u;
         }
       }
-      ptx::mma_commit_pair_mc(drain_bar, 0x1);
+      ptx::mma_commit_pair_mc(drain_bar, static_cast<uint16_t>(0x1u << lead));
       wait_quiet(drain_bar, 0, p.timeout_ns);
     }
     __syncwarp();
@@ -427,10 +466,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               idx[j][i] = min(max(__ldg(p.rows + at), 0), p.T - 1);
             }
         }
-        for (int kb = 0; kb < nk; ++kb, ++step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++step) {
           const uint32_t slot = step % C::A_STAGES;
           if (!(ok = wait(done_bar(slot), (step / C::A_STAGES & 1u) ^ 1u, WAIT_PRODUCER_EMPTY))) break;
-          const uint32_t fb = ptx::mapa_shared(rows_bar(slot), 0);
+          const uint32_t fb = ptx::mapa_shared(rows_bar(slot), lead);
           if (rank == 0 && w == 0) ptx::mbar_arrive_expect_tx(rows_bar(slot), bytes);
           ptx::mbar_arrive_cluster_relaxed(fb);
 #pragma unroll
@@ -462,6 +501,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     }
     __syncwarp();
+  }
+
+  if constexpr (C::SPLIT) {
+    // The pairs' sums: every copy into the rings and every MMA that reads them has
+    // completed; the epilogue warps write each chunk to the pair that finishes it.
+    ptx::tc_fence_before();
+    __syncwarp();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    if (have) {
+      const int pair = static_cast<int>(lead >> 1), nchunk = mine.n() / 16;
+#pragma unroll 1
+      for (int c = h; c < nchunk; c += 2) {
+        const int to_pair = owner(c);
+        if (to_pair == pair) continue;
+        uint32_t v[16];
+        ptx::tmem_ld16(tacc + c * 16, v);
+        ptx::tmem_wait_ld();
+        ptx::reg_fence(v);
+        const int slot = pair < to_pair ? pair : pair - 1;
+        const uint32_t to = ptx::mapa_shared(base, 2 * to_pair + rank) +
+                            ((slot * (C::NT / p.pairs) + place(c) * 16) * 128 + q * 32 + lane) * 4;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) ptx::st_shared_cluster_u32(to + r * 512, v[r]);
+      }
+    }
+    __syncwarp();
+    ptx::cluster_sync();
+    if (have) finish(tacc, 0);
   }
 
   // Both CTAs have passed their last use of the pair's resources before either
