@@ -171,11 +171,6 @@ __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t 
   }
 }
 
-__device__ __forceinline__ float logit(const RouteParams &p, bool fp32, int64_t at) {
-  return fp32 ? __ldg(static_cast<const float *>(p.logits) + at)
-              : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[at]);
-}
-
 // order_key in 64 bits.
 __device__ __forceinline__ unsigned long long order_key(double x) {
   const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));
@@ -212,31 +207,69 @@ __device__ __forceinline__ float score_of(bool sigmoid, float x, float m, float 
 __device__ __forceinline__ double score_of(bool sigmoid, double x, double m, double sum) {
   return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / sum;
 }
+// The same for the choice: the fast exp (2^-22 and |x| 2^-24 of itself) and
+// reciprocal.
+__device__ __forceinline__ float quick_score(bool sigmoid, float x, float m, float by_sum) {
+  return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x)) : __expf(x - m) * by_sum;
+}
+__device__ __forceinline__ double quick_score(bool sigmoid, double x, double m, double by_sum) {
+  return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) * by_sum;
+}
+__device__ __forceinline__ float quick_exp(float x) { return __expf(x); }
+__device__ __forceinline__ double quick_exp(double x) { return exp(x); }
 
-// Largest error of an FP32 score, as a part of the token's largest one.
-// Sigmoid: exp 2 ulp, sum and reciprocal half an ulp each.  Softmax: up to 32
-// additions in a lane and five across, on top of two exp.
+// Largest error of an FP32 score that the choice goes by, as a part of the token's
+// largest one.  Sigmoid: s (1 - s) (2^-22 + |x| 2^-24) <= 2^-23 of the exp, a sum
+// and a reciprocal.  Softmax: up to 32 additions in a lane and five across, on
+// top of two exp.
 __device__ __forceinline__ float score_error(bool sigmoid) { return sigmoid ? 0x1p-21f : 0x1p-18f; }
+
+// What a warp keeps from token to token: lane's group g is lane / L of L = 32 /
+// groups lanes, and its experts are first, first + L, ... below end = (g + 1) E /
+// groups.
+template <int EPL>
+struct ScorePlan {
+  int L, g, first, end;
+  float bias[EPL <= 8 ? EPL : 1];  // of the lane's experts
+  __device__ ScorePlan(const RouteParams &p, int lane) {
+    const int size = p.E / p.groups;
+    L = 32 / p.groups;
+    g = lane / L;
+    first = g * size + lane % L;
+    end = (g + 1) * size;
+    if (EPL <= 8) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) bias[EPL <= 8 ? i : 0] = p.bias && expert(i) < end ? __ldg(p.bias + expert(i)) : 0.0f;
+    }
+  }
+  __device__ int expert(int i) const { return first + L * i; }
+  __device__ float bias_of(const RouteParams &p, int i) const {
+    return EPL <= 8 ? bias[EPL <= 8 ? i : 0] : __ldg(p.bias + expert(i));
+  }
+};
 
 // One token by one warp, in V = float or double: the chosen experts, lane j
 // keeping choice j.  Returns whether V decided every comparison (FP64: always).
-//   lane: group lane / L of L = 32 / groups lanes, experts g E / groups + lane % L + L i
-// The values are read again where they are needed rather than kept: x and b
-// come from L1.
 template <class V, int EPL>
-__device__ __forceinline__ bool choose_exactly(const RouteParams &p, int64_t t, int lane,
+__device__ __forceinline__ bool choose_exactly(const RouteParams &p, const ScorePlan<EPL> &plan, int64_t t, int lane,
                                                int &my_id, float &my_weight) {
-  const bool sigmoid = p.sigmoid != 0, fp32 = p.fp32 != 0;
   using Key = decltype(order_key(V()));
   constexpr bool ROUNDED = sizeof(V) == 4;
-  const int L = 32 / p.groups, size = p.E / p.groups;
-  const int g = lane / L, li = lane % L;
-  const int64_t row = t * p.E;
-  auto expert = [&](int i) { return li + L * i < size ? g * size + li + L * i : -1; };
+  const bool sigmoid = p.sigmoid != 0, fp32 = p.fp32 != 0, biased = p.bias != nullptr;
+  const int L = plan.L, g = plan.g;
+  const float *row32 = static_cast<const float *>(p.logits) + (fp32 ? t * p.E : 0);
+  const __nv_bfloat16 *row16 = static_cast<const __nv_bfloat16 *>(p.logits) + (fp32 ? 0 : t * p.E);
+  auto logit = [&](int e) { return fp32 ? __ldg(row32 + e) : __bfloat162float(row16[e]); };
   float x[EPL];
+  if (fp32) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) x[i] = expert(i) >= 0 ? logit(p, fp32, row + expert(i)) : -INFINITY;
-  V m = 0, sum = 1;
+    for (int i = 0; i < EPL; ++i) x[i] = plan.expert(i) < plan.end ? __ldg(row32 + plan.expert(i)) : -INFINITY;
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      x[i] = plan.expert(i) < plan.end ? __bfloat162float(row16[plan.expert(i)]) : -INFINITY;
+  }
+  V m = 0, sum = 1, by_sum = 1;
   float largest = 1.0f;  // bound of the scores
   if (!sigmoid) {
     uint32_t top = 0;
@@ -245,19 +278,25 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, int64_t t, 
     m = key_value(__reduce_max_sync(kAll, top));
     sum = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) sum += x[i] == -INFINITY ? V(0) : static_cast<V>(exp(V(x[i]) - m));
+    for (int i = 0; i < EPL; ++i) sum += x[i] == -INFINITY ? V(0) : quick_exp(V(x[i]) - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    largest = 1.0f / static_cast<float>(sum);
+    by_sum = V(1) / sum;
+    largest = static_cast<float>(by_sum);
   }
   const float err = score_error(sigmoid) * largest;  // of one score
-  auto worth = [&](float xi, int e) -> V {           // s + b, or the logit where no bias is given
-    if (xi == -INFINITY) return V(-INFINITY);
-    return p.bias ? score_of(sigmoid, V(xi), m, sum) + V(__ldg(p.bias + e)) : V(xi);
-  };
+  // s + b, or the logit where no bias is given; 0 for no expert
   Key key[EPL];
+  if (biased) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) key[i] = expert(i) >= 0 ? order_key(worth(x[i], expert(i))) : Key(0);
+    for (int i = 0; i < EPL; ++i) {
+      const Key k = x[i] == -INFINITY ? Key(0) : order_key(quick_score(sigmoid, V(x[i]), m, by_sum) + V(plan.bias_of(p, i)));
+      key[i] = plan.expert(i) < plan.end ? k : Key(0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = order_key(V(x[i]));
+  }
   bool sure = true;
   if (p.kept < p.groups) {
     // the group's two largest
@@ -274,9 +313,9 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, int64_t t, 
     }
     V v1 = key_value(k1), v2 = key_value(k2);
     const bool summed = p.best == 2;
-    if (summed && !p.bias) {  // the logits' order, but the scores are added
-      v1 = k1 == 0 ? V(0) : score_of(sigmoid, v1, m, sum);
-      v2 = k2 == 0 ? V(0) : score_of(sigmoid, v2, m, sum);
+    if (summed && !biased) {  // the logits' order, but the scores are added
+      v1 = k1 == 0 ? V(0) : quick_score(sigmoid, v1, m, by_sum);
+      v2 = k2 == 0 ? V(0) : quick_score(sigmoid, v2, m, by_sum);
     }
     const V value = summed && k2 != 0 ? v1 + v2 : v1;
     const Key mine = k1 == 0 ? Key(0) : order_key(value);
@@ -287,16 +326,12 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, int64_t t, 
       rank += other > mine || (other == mine && h < g);
     }
     const bool keep = mine != 0 && rank < p.kept;
-    if (ROUNDED && (p.bias || summed)) {
-      const unsigned kept = __ballot_sync(kAll, keep);
-      for (int h = 0; h < p.groups; ++h) {
-        const V other = __shfl_sync(kAll, value, h * L);
-        const float s12 = fmaxf(size12, __shfl_sync(kAll, size12, h * L));
-        const bool there = __shfl_sync(kAll, mine, h * L) != 0;
-        if (mine != 0 && there && keep != ((kept >> (h * L)) & 1u) &&
-            fabsf(float(value - other)) <= 4.0f * err + 0x1p-21f * s12)
-          sure = false;
-      }
+    if (ROUNDED && (biased || summed)) {
+      // the least that a kept value can be against the most that another can
+      const float v = static_cast<float>(value), off = 2.0f * err + 0x1p-22f * size12;
+      const uint32_t low = __reduce_min_sync(kAll, keep ? order_key(v - off) : 0xffffffffu);
+      const uint32_t high = __reduce_max_sync(kAll, keep || mine == 0 ? 0u : order_key(v + off));
+      if (high >= low) sure = false;
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = keep ? key[i] : Key(0);
@@ -304,32 +339,34 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, int64_t t, 
   Key my_key = 0, next_key = 0;
   int next_id = -1;
   my_id = -1;
-  const int rounds = ROUNDED && p.bias ? p.k + 1 : p.k;
+  const int rounds = ROUNDED && biased ? p.k + 1 : p.k;
   for (int j = 0; j < rounds; ++j) {
-    Key b = 0;
-    int e = 0x7fffffff;
+    Key b = key[0];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const bool up = key[i] > b;
-      b = up ? key[i] : b;
-      e = up ? g * size + li + L * i : e;
-    }
+    for (int i = 1; i < EPL; ++i) b = max(b, key[i]);
+    // the lane's first expert that holds it; then the warp's lowest
+    int at = EPL - 1;
+#pragma unroll
+    for (int i = EPL - 2; i >= 0; --i) at = key[i] == b ? i : at;
+    int e = plan.expert(at);
+    const int own = e;
     warp_best(b, e);
-    if (b == 0) e = -1;
+    if (b == 0) break;  // none left: nor in the rounds to come
     my_key = lane == j ? b : my_key;
     my_id = lane == j ? e : my_id;
-    next_key = b;
-    next_id = e;
+    next_key = j == p.k ? b : Key(0);
+    next_id = j == p.k ? e : -1;
+    const int gone = own == e ? at : -1;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = g * size + li + L * i == e ? Key(0) : key[i];
+    for (int i = 0; i < EPL; ++i) key[i] = i == gone ? Key(0) : key[i];
   }
   if (lane >= p.k) my_id = -1;
-  const float mx = my_id >= 0 ? logit(p, fp32, row + my_id) : -INFINITY;
-  if (ROUNDED && p.bias) {
+  const float mx = my_id >= 0 ? logit(my_id) : -INFINITY;
+  if (ROUNDED && biased) {
     // each choice against the next one; equal logits with equal biases are a
     // true tie, which the expert's number has settled
     const float mb = my_id >= 0 ? __ldg(p.bias + my_id) : 0.0f;
-    const float nx = next_id >= 0 ? logit(p, fp32, row + next_id) : -INFINITY;
+    const float nx = next_id >= 0 ? logit(next_id) : -INFINITY;
     const float nb = next_id >= 0 ? __ldg(p.bias + next_id) : 0.0f;
     Key ok = __shfl_down_sync(kAll, my_key, 1);
     float ox = __shfl_down_sync(kAll, mx, 1), ob = __shfl_down_sync(kAll, mb, 1);
@@ -352,41 +389,36 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, int64_t t, 
 }
 
 template <int EPL>
-__device__ __noinline__ void choose_in_64(const RouteParams &p, int64_t t, int lane, int &id, float &weight) {
-  choose_exactly<double, EPL>(p, t, lane, id, weight);
-}
-
-// choose() by scores: the token t by a whole warp.
-template <int EPL>
-__device__ __forceinline__ void choose_scored(const RouteParams &p, int64_t t, int64_t end, int lane,
-                                              uint16_t *ids16) {
-  if (t >= end) return;
-  int id;
-  float weight;
-  if (!choose_exactly<float, EPL>(p, t, lane, id, weight)) choose_in_64<EPL>(p, t, lane, id, weight);
-  if (lane < p.k) {
-    p.ids[t * p.k + lane] = id;
-    p.weights[t * p.k + lane] = weight;
-    ids16[lane] = static_cast<uint16_t>(id);
-  }
+__device__ __noinline__ void choose_in_64(const RouteParams &p, const ScorePlan<EPL> &plan, int64_t t, int lane,
+                                          int &id, float &weight) {
+  choose_exactly<double, EPL>(p, plan, t, lane, id, weight);
 }
 
 // How a block chooses: by the logits, LPT lanes per token,
 template <int LPT, int EPL, bool FP32>
 struct ByLogit {
   static constexpr int LANES = LPT;
-  __device__ static __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane,
-                                                uint16_t *ids16) {
+  __device__ ByLogit(const RouteParams &, int) {}
+  __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane, uint16_t *ids16) {
     swiglu::choose<LPT, EPL, FP32>(p, t, end, lane, ids16);
   }
 };
-// or by scores.
+// or by scores, a warp per token.
 template <int EPL>
 struct ByScore {
   static constexpr int LANES = 32;
-  __device__ static __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane,
-                                                uint16_t *ids16) {
-    choose_scored<EPL>(p, t, end, lane, ids16);
+  ScorePlan<EPL> plan;
+  __device__ ByScore(const RouteParams &p, int lane) : plan(p, lane) {}
+  __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane, uint16_t *ids16) {
+    if (t >= end) return;
+    int id;
+    float weight;
+    if (!choose_exactly<float, EPL>(p, plan, t, lane, id, weight)) choose_in_64<EPL>(p, plan, t, lane, id, weight);
+    if (lane < p.k) {
+      p.ids[t * p.k + lane] = id;
+      p.weights[t * p.k + lane] = weight;
+      ids16[lane] = static_cast<uint16_t>(id);
+    }
   }
 };
 
@@ -470,8 +502,9 @@ __global__ void __launch_bounds__(1024, 1) route_choose_kernel(const __grid_cons
   constexpr int SIDE = 32 / How::LANES;
   const int per = (nt + warps * SIDE - 1) / (warps * SIDE) * SIDE;
   const int t0 = min(warp * per, nt), t1 = min(t0 + per, nt);
+  How how(p, lane);
   for (int t = t0; t < t1; t += SIDE)
-    How::choose(p, b0 + t + lane / How::LANES, b0 + t1, lane, sm.ids + (t + lane / How::LANES) * p.k);
+    how.choose(p, b0 + t + lane / How::LANES, b0 + t1, lane, sm.ids + (t + lane / How::LANES) * p.k);
   __syncwarp();
   walk(sm.ids, t0 * p.k, t1 * p.k, cnt, lane, [](int, unsigned, int) {});
   __syncthreads();
