@@ -495,15 +495,17 @@ int swiglu_quant_int8(const void *X, int32_t x_fp32, void *Q, float *scale, int6
  * All 256 codes are allowed.  Sums of products are exact below 2^24 and carry
  * FP32's rounding beyond (K up to 1024 never reaches it); scales are applied
  * in FP32, one rounding to BF16.  Equal calls give equal bits.
- *   workspace : device scratch of at least swiglu_int8_workspace_size(T, P, K)
- *       bytes (T = P = M for the dense forms; 0 for a few rows, then may be
- *       NULL), 16-byte aligned, overlapping no other buffer: the rows in 16 bits
- * K a multiple of 16 below 2^22, N a multiple of 8, N * K < 2^40; A, W and Y
+ *   workspace : device scratch of at least swiglu_int8_workspace_size() bytes
+ *       (dense: T = P = M, E = 0; 0 for a few rows, then may be NULL; 0 too for
+ *       sizes that the call refuses), 16-byte aligned, overlapping no other
+ *       buffer: the rows in 16 bits
+ * K a multiple of 16 below 2^20, N a multiple of 8, N * K < 2^40; A, W and Y
  * 16-byte aligned, scales 4-byte; Y overlaps no input; the rest as in
  * swiglu_fused_grouped (M or P = 0 enqueues nothing, K = 0 or T = 0 fills Y
  * with zeros, a row number outside [0, T) gives a row of zeros).
  */
-uint64_t swiglu_int8_workspace_size(int64_t T, int64_t P, int64_t K);
+uint64_t swiglu_int8_workspace_size(int64_t T, int64_t P, int64_t E, int64_t N, int64_t K,
+                                    int32_t fused);
 int swiglu_linear_int8(const void *X, const float *x_scale, const void *W, const float *w_scale,
                        void *Z, int64_t M, int64_t N, int64_t K,
                        void *workspace, uint64_t workspace_bytes, void *stream);

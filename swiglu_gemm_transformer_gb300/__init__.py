@@ -62,7 +62,7 @@ EXPORTS = {
     "swiglu_fused_grouped": ("ppp pp p lllll p", ctypes.c_int),
     "swiglu_linear_grouped": ("pp pp p lllll p", ctypes.c_int),
     "swiglu_quant_int8": ("p i pp ll p", ctypes.c_int),
-    "swiglu_int8_workspace_size": ("lll", ctypes.c_uint64),
+    "swiglu_int8_workspace_size": ("lllll i", ctypes.c_uint64),
     "swiglu_linear_int8": ("pp pp p lll pQ p", ctypes.c_int),
     "swiglu_fused_int8": ("pp pp pp p lll pQ p", ctypes.c_int),
     "swiglu_linear_grouped_int8": ("pp pp pp p lllll pQ p", ctypes.c_int),

@@ -17,7 +17,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 // Places and columns: the last tile's bounds, up to 256 past them, are 32-bit too.
 constexpr int64_t kMaxTiled = kMaxDim - 256;
-constexpr int64_t kMaxK = (int64_t(1) << 22) - 16;  // a lane's sum of 128 * 128 * K / 32
+constexpr int64_t kMaxK = (int64_t(1) << 20) - 16;  // a warp's sum of 128 * 128 * K / 8
 
 struct Int8Call {
   const void *A, *W1, *W2;  // W2 == nullptr: the linear form
@@ -31,8 +31,22 @@ struct Int8Call {
   void *stream;
 };
 
-// Places up to which the rows kernel runs (RULE).
-constexpr int64_t kFewRows = 16;
+// Whether the kernels for a few rows run.  They read a matrix once for 8 rows (from
+// L2 after the first time), the tensor-core form once for 192, but that begins with
+// a second kernel and ends with a longer tail, about 4 us together.
+// Dense, by tiles of 8 rows and bytes of weights (us, rows | tensor cores): 136 MB 8
+// rows 27.4 | 29.9, 16 rows 41 | 30; 68 MB 18.0 | 22.1, 27 | 22; 13 MB 16 rows 6.0 |
+// 11.2; 4.4 MB 32 rows 5.7 | 11.8; 8.7 MB 32 rows 9.0 | 9.2.
+// Grouped, where every place has blocks: 64 experts of 4 MB, 32 places 22.4 | 27.9,
+// 64 places 36.3 | 40.6, 128 places 56.3 | 52.8; of 2 MB, 16 places 8.5 | 14.2, 32
+// places 19.1 | 18.6; 8 experts of 13 MB, 32 places 28.4 | 30.1, 64 places 45.9 |
+// 30.2; of 2 MB, 16 places 8.3 | 9.4, 32 places 11.3 | 9.6.
+bool few_rows(int64_t P, int64_t E, int64_t N, int64_t K, bool fused) {
+  const int64_t bytes = N * K * (fused ? 2 : 1);
+  if (E > 0) return P <= 16 || (bytes >= 4000000 && P <= std::max<int64_t>(32, std::min<int64_t>(E, 64)));
+  const int64_t tiles = ceil_div(P, 8);
+  return tiles == 1 || (tiles <= 16 && bytes <= 200000000 / (9 * tiles - 11));
+}
 
 // The tensor-core form reads FP16 rows: A's, or, where there are fewer places
 // than rows, the places'.
@@ -46,8 +60,9 @@ constexpr int kWidenTurns = 4;
 
 __global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t *A, const int32_t *rows, __half *out,
                                                          int64_t count, int32_t per_row, int32_t T) {
-  ptx::grid_launch_dependents();
+  // (in this order: the product's kernel starts when nothing before this one runs)
   ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   const int64_t first = int64_t(blockIdx.x) * (256 * kWidenTurns) + threadIdx.x;
   uint2 v[kWidenTurns];
 #pragma unroll
@@ -88,22 +103,39 @@ cudaError_t launch_widen(const Int8Call &c, const int32_t *rows, int64_t n) {
                             static_cast<__half *>(c.workspace), count, int32_t(per_row), int32_t(c.T));
 }
 
-template <bool FUSED, int R, int NC>
-cudaError_t launch_rows(Int8RowsParams &p, cudaStream_t s) {
-  constexpr int WARPS = 8;
-  p.col_blocks = int32_t(ceil_div(p.N, WARPS * NC));
-  const int64_t tiles = p.offsets ? std::min(p.E, p.P) + p.P / R : ceil_div(p.P, R);
+// The kernel `kern` for `tiles` of rows and blocks of `cols` columns.
+cudaError_t launch_rows(void (*kern)(Int8RowsParams), Int8RowsParams &p, int64_t tiles, int cols, cudaStream_t s) {
+  p.col_blocks = int32_t(ceil_div(p.N, cols));
   if (tiles * p.col_blocks > kMaxDim) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.col_blocks));
-  cfg.blockDim = dim3(32 * WARPS);
+  cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, swiglu_int8_rows_kernel<FUSED, R, NC, WARPS>, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// The kernels for a few rows.
+cudaError_t run_rows(Int8RowsParams &p, bool fused, cudaStream_t s) {
+  // One row, or places that hardly share experts: a block for each place, whose
+  // warps take one, two or four columns of each matrix, as many as leave four blocks
+  // to each of the 152 SMs (one row of 18944 x 3584 with four columns 25.1 us, so
+  // 15.2).
+  if (p.P == 1 || (p.offsets && 4 * p.P <= p.E)) {
+    const int64_t work = int64_t(p.N) * p.P;  // columns
+    if (fused)
+      return work >= 16 * 608 ? launch_rows(swiglu_int8_token_kernel<true, 2, 8>, p, p.P, 16, s)
+                              : launch_rows(swiglu_int8_token_kernel<true, 1, 8>, p, p.P, 8, s);
+    return work >= 32 * 608   ? launch_rows(swiglu_int8_token_kernel<false, 4, 8>, p, p.P, 32, s)
+           : work >= 16 * 608 ? launch_rows(swiglu_int8_token_kernel<false, 2, 8>, p, p.P, 16, s)
+                              : launch_rows(swiglu_int8_token_kernel<false, 1, 8>, p, p.P, 8, s);
+  }
+  return launch_rows(fused ? swiglu_int8_rows_kernel<true, 8> : swiglu_int8_rows_kernel<false, 8>, p,
+                     p.offsets ? p.P : ceil_div(p.P, 8), 16, s);
 }
 
 struct TensorLaunch {
@@ -170,7 +202,9 @@ int run_tensor(const Int8Call &c, uint32_t *err, uint64_t timeout_ns, uint64_t c
   const int32_t k_blk = int32_t(ceil_div(c.K, Fused::BK)), n_blk = int32_t(ceil_div(c.N, c.fused ? 128 : 256));
   auto units = [&](int nt) { return (c.offsets ? std::min(c.E, c.P) + c.P / nt : ceil_div(c.P, nt)) * n_blk; };
   // Few units and enough K to share: several pairs to a unit.  A cluster of four
-  // or eight CTAs fits the GPU 36 or 15 times.  (MEASURE)
+  // or eight CTAs fits the GPU 36 or 15 times.  125 rows of 4864 x 896 22.7 -> 13.5
+  // us, 128 rows of 3584 x 3584 19.2 -> 13.8, of 2048 x 2048 13.9 -> 11.5; at 8 K
+  // steps (64 rows of 1024 x 2048) 9.6 and 9.7.
   const int64_t few = units(Split::NT);
   const int pairs = few > 36 || k_blk < 8 ? 1 : few > 15 ? 2 : Split::MAX_PAIRS;
   const int nt = pairs > 1 ? Split::NT : Fused::NT;
@@ -212,7 +246,7 @@ int run_int8(const Int8Call &c) {
   const int64_t T = c.T, P = c.P, E = c.E, N = c.N, K = c.K;
   if (T < 0 || P < 0 || E < 1 || N < 0 || K < 0) return SWIGLU_ERR_INVALID_ARG;
   if (!c.rows && T != P) return SWIGLU_ERR_INVALID_ARG;
-  if (T > kMaxDim || P > kMaxTiled || N > kMaxTiled || K > kMaxK || E > kRowsMaxExperts)
+  if (T > kMaxDim || P > kMaxTiled || N > kMaxTiled || K > kMaxK || E > kMaxExperts)
     return SWIGLU_ERR_UNSUPPORTED;
   if (P == 0 || N == 0) return SWIGLU_OK;
   // one expert's matrix: the tensor map's largest stride is 2^40 bytes
@@ -233,7 +267,7 @@ int run_int8(const Int8Call &c) {
       ranges_overlap(c.Y, y_bytes, c.offsets, uint64_t(E + 1) * 4) ||
       ranges_overlap(c.Y, y_bytes, c.rows, uint64_t(P) * 4))
     return SWIGLU_ERR_INVALID_ARG;
-  const uint64_t need = swiglu_int8_workspace_size(T, P, K);
+  const uint64_t need = swiglu_int8_workspace_size(T, P, c.grouped ? E : 0, N, K, c.fused);
   if (need > 0) {
     if (!c.workspace || c.workspace_bytes < need) return SWIGLU_ERR_INVALID_ARG;
     if (!ptr_aligned(c.workspace, 16)) return SWIGLU_ERR_MISALIGNED;
@@ -267,22 +301,21 @@ int run_int8(const Int8Call &c) {
   p.P = int32_t(P);
   p.E = int32_t(E);
   p.N = int32_t(N);
-  p.K = K;
-  if (P > kFewRows) return run_tensor(c, err, timeout_ns, gen);
-  cudaError_t e;
-  if (P <= E)
-    e = c.fused ? launch_rows<true, 1, 2>(p, s) : launch_rows<false, 1, 4>(p, s);
-  else
-    e = c.fused ? launch_rows<true, 8, 2>(p, s) : launch_rows<false, 8, 4>(p, s);
+  p.K = int32_t(K);
+  if (need > 0) return run_tensor(c, err, timeout_ns, gen);
+  const cudaError_t e = run_rows(p, c.fused, s);
   return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
 }
 
 }  // namespace
 }  // namespace swiglu
 
-extern "C" uint64_t swiglu_int8_workspace_size(int64_t T, int64_t P, int64_t K) {
+extern "C" uint64_t swiglu_int8_workspace_size(int64_t T, int64_t P, int64_t E, int64_t N, int64_t K,
+                                               int32_t fused) {
   using namespace swiglu;
-  if (T < 1 || T > kMaxDim || P <= kFewRows || P > kMaxTiled || K < 1 || K > kMaxK) return 0;
+  if (T < 1 || T > kMaxDim || P < 1 || P > kMaxTiled || E < 0 || E > kMaxExperts || N < 1 || N > kMaxTiled || K < 1 ||
+      K > kMaxK || few_rows(P, E, N, K, fused != 0))
+    return 0;
   return widened_bytes(T, P, K);
 }
 

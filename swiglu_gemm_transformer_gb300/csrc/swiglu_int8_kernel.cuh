@@ -22,7 +22,8 @@
 //     steps of weights, of 128 of K each.  A buffer of them is freed, filled,
 //     announced and read in turn, so the codes are widened before the wait for
 //     it.  Steps of 64 (four buffers) were bound by the MMA's thread, which a
-//     commit holds up for about 230 cycles: 480 a step however few rows it had;
+//     commit holds up for about 230 cycles: 480 a step however few rows it had (the
+//     7B projection 321 us, with steps of 128 306);
 //   * FUSED: gate and up of a column lie in lanes 2j and 2j ^ 9 of one warp (odd
 //     lanes take the up columns, in an order that keeps the loads of eight
 //     lanes on different banks), so shuffles bring them together.
@@ -195,8 +196,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // The kernel before this one widens the rows; its blocks let this one start once
+  // they have waited for all work before them.  So everything but the widened rows
+  // may be read, and Y written, without a wait for it: weights stream meanwhile.
   ptx::grid_launch_dependents();
-  ptx::grid_dependency_wait();
 
   auto wait = [&](uint32_t bar, uint32_t parity, uint32_t where) {
     return wait_bar(bar, parity, p.timeout_ns, abort_flag, p.err, where);
@@ -446,6 +449,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // thread arrives for every step.
     const int w = warp - C::LOAD_WARP;
     if (w < loaders && ptx::elect_one()) {
+      ptx::grid_dependency_wait();
       constexpr int PER = C::NT / 8 / C::LOAD_WARPS;  // gathers of a warp per step
       uint32_t step = 0;
       bool ok = true;

@@ -308,7 +308,7 @@ PyObject *int8_product(PyObject *, PyObject *const *a, Py_ssize_t n) {
     c10::cuda::OptionalCUDAStreamGuard pool;
     void *s = c.enter(a[10], pool);
     Tensor Y = c.output(a[8], "the output", ScalarType::BFloat16, {P, N});
-    uint64_t bytes = N > 0 ? swiglu_int8_workspace_size(T, P, K) : 0;
+    uint64_t bytes = swiglu_int8_workspace_size(T, P, grouped ? E : 0, N, K, fused);
     Tensor ws;
     if (a[9] != Py_None) {
       ws = c.tensor(a[9], "workspace", 1);

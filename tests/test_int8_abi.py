@@ -52,7 +52,7 @@ def test_quant_refusals(lib, kw, want):
     assert _quant(lib, **kw) == want
 
 
-def _product(lib, fused, grouped, A_=A, sa=B, W1=C, s1=D, W2=E, s2=F, off=G, rows=H, Y=I, T=64, P=128, E_=8, N=64, K=64, ws=J,
+def _product(lib, fused, grouped, A_=A, sa=B, W1=C, s1=D, W2=E, s2=F, off=G, rows=H, Y=I, T=512, P=1024, E_=8, N=64, K=64, ws=J,
              nbytes=1 << 20):
     if grouped:
         if fused:
@@ -64,11 +64,15 @@ def _product(lib, fused, grouped, A_=A, sa=B, W1=C, s1=D, W2=E, s2=F, off=G, row
 
 
 def test_workspace_size(lib):
-    assert lib.swiglu_int8_workspace_size(64, 128, 64) == 64 * 64 * 2   # A's rows
-    assert lib.swiglu_int8_workspace_size(128, 64, 64) == 64 * 64 * 2   # the places'
-    for T, P, K in ((1, 8, 64), (0, 64, 64), (64, 0, 64), (64, 64, 0), (-1, 64, 64), (64, -1, 64), (64, 64, -16), (1 << 31, 64, 64),
-                    (64, 1 << 31, 64), (64, 64, 1 << 22)):
-        assert lib.swiglu_int8_workspace_size(T, P, K) == 0
+    size = lib.swiglu_int8_workspace_size
+    assert size(512, 1024, 8, 64, 64, 0) == 512 * 64 * 2   # A's rows
+    assert size(1024, 512, 8, 64, 64, 1) == 512 * 64 * 2   # the places'
+    assert size(512, 512, 0, 64, 64, 1) == 512 * 64 * 2    # dense
+    for args in ((1, 8, 64, 64, 64, 0), (8, 8, 0, 64, 64, 1), (0, 512, 8, 64, 64, 0), (512, 0, 8, 64, 64, 0), (512, 512, 8, 64, 0, 0),
+                 (512, 512, 8, 0, 64, 0), (-1, 512, 8, 64, 64, 0), (512, -1, 8, 64, 64, 0), (512, 512, 8, 64, -16, 0), (512, 512, -1, 64, 64, 0),
+                 (1 << 31, 512, 8, 64, 64, 0), (512, 1 << 31, 8, 64, 64, 0), (512, 512, 8, 64, 1 << 20, 0), (512, 512, 1025, 64, 64, 0),
+                 (512, 512, 8, 1 << 31, 64, 0)):
+        assert size(*args) == 0
 
 
 FUSED = pytest.mark.parametrize("fused", [True, False], ids=["fused", "linear"])
@@ -83,7 +87,7 @@ GROUPED = pytest.mark.parametrize("grouped", [True, False], ids=["grouped", "den
     (dict(N=1 << 20, K=1 << 21), UNS), (dict(N=60), MIS), (dict(K=56), MIS), (dict(A_=A + 8), MIS), (dict(W1=C + 8), MIS),
     (dict(sa=B + 2), MIS), (dict(s1=D + 1), MIS), (dict(Y=I + 8), MIS),
     (dict(Y=A), INV), (dict(Y=B - 64), INV), (dict(Y=C + 64), INV), (dict(Y=D), INV),   # overlaps
-    (dict(ws=None), INV), (dict(nbytes=64 * 64 * 2 - 1), INV), (dict(ws=J + 8), MIS), (dict(ws=A), INV), (dict(ws=I - 64), INV),
+    (dict(ws=None), INV), (dict(nbytes=512 * 64 * 2 - 1), INV), (dict(ws=J + 8), MIS), (dict(ws=A), INV), (dict(ws=I - 64), INV),
     (dict(ws=B - 4096), INV), (dict(ws=C + 64), INV), (dict(ws=D), INV),
     (dict(N=0), OK),
 ])

@@ -222,6 +222,29 @@ def test_grouped(sg, fused, gather, sizes, NK):
 
 
 @FORMS
+@pytest.mark.parametrize("gather", [True, False], ids=["rows", "dense"])
+@pytest.mark.parametrize("sizes", [[33, 0], [0, 20, 0, 1], [5, 33, 0, 70], [128, 1], [300], [17, 0, 0, 0, 0, 0, 0, 0, 0, 1]],
+                         ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("NK", [(8, 1024), (72, 1040), (264, 1104), (520, 2064), (2600, 1120)], ids=lambda s: "x".join(map(str, s)))
+def test_grouped_few_units_share_k(sg, fused, gather, sizes, NK):
+    check_product(sg, fused, sizes, *NK, T=11 if gather else None)
+
+
+@FORMS
+@pytest.mark.parametrize("E,rows_each,N,K", [(1024, 3, 1024, 32), (16, 1300, 4096, 48)], ids=["short", "long"])
+def test_grouped_ring_of_units_wraps(sg, fused, E, rows_each, N, K):
+    check_product(sg, fused, [rows_each + (e % 3) for e in range(E)], N, K, T=100)
+
+
+@FORMS
+@pytest.mark.parametrize("E", [8, 64])
+@pytest.mark.parametrize("P", [15, 16, 17, 31, 32, 33, 64, 65])
+def test_grouped_few_places_of_large_matrices(sg, fused, E, P):
+    sizes = torch.bincount(torch.randint(0, E, (P,), generator=_gen("places", E, P)), minlength=E).tolist()
+    check_product(sg, fused, sizes, 1368, 3008, T=P // 2 + 1)
+
+
+@FORMS
 @pytest.mark.parametrize("E", [1, 2, 31, 32, 33, 64, 257, 1024])
 def test_grouped_expert_counts(sg, fused, E):
     sizes = torch.randint(0, 4, (E,), generator=_gen("experts", E)).tolist()
@@ -275,7 +298,7 @@ def test_sums_are_exact_up_to_24_bits(sg, M):
     assert torch.equal(Z.cpu(), (A2.long() @ W2.long().t()).float().to(BF))
 
 
-@pytest.mark.parametrize("M", [1, 40])
+@pytest.mark.parametrize("M", [1, 40, 200])
 def test_long_k(sg, M):
     # past 2^17 an FP32 or a 32-bit sum of the largest products would pass its range
     check_product(sg, False, [M], 16, (1 << 17) + 48, dense=True, full=True)
