@@ -404,3 +404,133 @@ def test_binding_refusals(sg):
         with pytest.raises(err):
             call()
     _status(sg)
+
+
+# ---- the calls together -----------------------------------------------------------
+
+
+@pytest.fixture(scope="module")
+def block(sg):
+    from examples import moe_block_int8
+    return moe_block_int8.SparseBlockInt8(272, 144, 16, 4, seed=3)
+
+
+def check_stages(block, R, H, stages, out):
+    """Every stage against the 64-bit form of its own inputs."""
+    route = stages["route"]
+    for x, q in ((H, stages["Hq"]), (stages["Y"], stages["Yq"])):
+        want, scale = quant_ref(x.cpu())
+        assert torch.equal(q[0].cpu(), want) and torch.equal(q[1].cpu(), scale)
+    offsets, rows = route.offsets.tolist(), route.rows.tolist()
+    assert sorted(rows) == sorted(list(range(R.shape[0])) * block.top_k) and offsets[-1] == len(rows)
+    for a, Ws, r, got in ((stages["Hq"], [block.Q1, block.Q2], rows, stages["Y"]), (stages["Yq"], [block.Q3], None, stages["Z"])):
+        ref, tol = product_ref(*a, Ws, offsets, r)
+        assert ((got.double() - ref).abs() <= tol).all()
+    # the norms: 128 roundings of 2^-24 of the terms' magnitudes, and one to BF16
+    w, z = route.weights.double(), stages["Z"].double()[route.slots.long()]
+    joined, size = (w[..., None] * z).sum(1), (w[..., None] * z).abs().sum(1)
+    gate = block.gate.double()
+    rms = torch.sqrt(joined.square().mean(1, keepdim=True) + block.eps)
+    r = R.double() + gate * joined / rms
+    tol = 128 * 2.0**-24 * (R.double().abs() + gate * (size + joined.abs()) / rms)
+    assert ((out[0].double() - r).abs() <= tol).all()
+    h = r / torch.sqrt(r.square().mean(1, keepdim=True) + block.eps)
+    assert ((out[1].double() - h).abs() <= 2.0**-8 * h.abs() + 4 * tol + 1e-30).all()
+
+
+@pytest.mark.parametrize("T", [1, 5, 300])
+def test_block_in_a_graph_replayed_on_new_inputs(sg, block, T):
+    R, H, stages = torch.zeros(T, 272, device=DEV), torch.zeros(T, 272, dtype=BF, device=DEV), {}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block(R, H)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = block(R, H, stages)
+    for i in range(3):
+        gen = _gen("block", T, i)
+        R.copy_(torch.randn(T, 272, generator=gen))
+        H.copy_(torch.randn(T, 272, generator=gen))
+        graph.replay()
+        torch.cuda.synchronize()
+        _status(sg)
+        check_stages(block, R, H, stages, out)
+
+
+def test_two_graphs_and_an_eager_call_in_turn(sg, block):
+    """Graphs captured one after the other, replayed in turn: each has workspaces of its own."""
+    ins = [(torch.randn(T, 272, generator=_gen("two", T)).to(DEV), torch.randn(T, 272, generator=_gen("2", T)).to(DEV, BF)) for T in (300, 180)]
+    want = [[t.clone() for t in block(*x)] for x in ins]
+    graphs = []
+    for x in ins:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, block(*x)))
+    for _ in range(3):
+        for (g, out), w in zip(graphs, want):
+            for t in out:
+                t.zero_()
+            g.replay()
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
+        assert all(torch.equal(a, b) for a, b in zip(block(*ins[0]), want[0]))
+    _status(sg)
+
+
+@pytest.mark.parametrize("stream", [lambda s: s, lambda s: s.cuda_stream], ids=["object", "handle"])
+def test_outputs_and_workspaces_belong_to_the_stream_of_the_call(sg, stream):
+    """Memory that the current stream has queued work for is not handed to a call
+    on another stream, nor the call's workspace to the current stream."""
+    T, E, k, N, K = 4096, 64, 8, 256, 128
+    s = torch.cuda.Stream()
+    gen = _gen("pools")
+    lg, x = torch.randn(T, E, generator=gen).to(DEV), torch.randn(T, K, generator=gen).to(DEV, BF)
+    W1, W2, W3 = (sg.swiglu_quant_int8(torch.randn(E, n, m, generator=gen).to(DEV)) for n, m in ((N, K), (N, K), (K, N)))
+    D = sg.swiglu_quant_int8(torch.randn(N, K, generator=gen).to(DEV))
+
+    def step(**kw):
+        r = sg.swiglu_moe_route_scored(lg, k, groups=8, kept_groups=4, **kw)
+        q = sg.swiglu_quant_int8(x, **kw)
+        y = sg.swiglu_fused_grouped_int8(*q, *W1, *W2, r.offsets, r.rows, **kw)
+        yq = sg.swiglu_quant_int8(y, **kw)
+        z = sg.swiglu_linear_grouped_int8(*yq, *W3, r.offsets, **kw)
+        return [*r, *q, y, *yq, z, sg.swiglu_linear_int8(*q, *D, **kw), sg.swiglu_fused_int8(*q, *D, *D, **kw)]
+
+    want = [t.cpu() for t in step()]
+    sizes = [t.numel() * t.element_size() for t in want] + [T * K * 2, T * k * N * 2]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    for n in sizes * 2:
+        torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0x7F)
+    got = step(stream=stream(s))
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+    late = step(stream=stream(s))
+    for n in sizes * 2:
+        torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0x7F)
+    torch.cuda.synchronize()
+    _status(sg)
+    for w, a, b in zip(want, got, late):
+        assert torch.equal(w, a.cpu()) and torch.equal(w, b.cpu())
+
+
+def test_given_workspaces_and_their_refusals(sg):
+    gen = _gen("workspace")
+    q = lambda *s: torch.randint(-127, 128, s, generator=gen).to(I8).to(DEV)  # noqa: E731
+    A, a, W, w = q(700, 256), torch.rand(700, generator=gen).to(DEV), q(512, 256), torch.rand(512, generator=gen).to(DEV)
+    need = sg.lib().swiglu_int8_workspace_size(700, 700, 0, 512, 256, 0)
+    assert need == 700 * 256 * 2
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    assert torch.equal(sg.swiglu_linear_int8(A, a, W, w, workspace=ws), sg.swiglu_linear_int8(A, a, W, w))
+    for bad in (ws[:-1], ws[8:], ws[:0]):
+        with pytest.raises(sg.SwigluError):
+            sg.swiglu_linear_int8(A, a, W, w, workspace=bad)
+    _status(sg)
+
+
+def test_example_block(sg):
+    from examples import moe_block_int8
+    worst, off = moe_block_int8.main(hidden=272, inner=144, experts=16, top_k=4, layers=2, prompt=90)
+    # BF16 roundings of Y and Z that fall the other way, a few in a thousand
+    assert worst < 2.0**-8 and off < 2.0**-8
