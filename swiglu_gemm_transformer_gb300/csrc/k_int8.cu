@@ -188,8 +188,8 @@ cudaError_t launch_tensor(TensorLaunch &t) {
 
 // The tensor-core form.
 int run_tensor(const Int8Call &c, uint32_t *err, uint64_t timeout_ns, uint64_t ctx_gen) {
-  using Fused = Int8Cfg<true>;
-  using Split = Int8Cfg<true, true>;
+  using Fused = Int8Cfg<true, 192>;
+  using Split = Int8Cfg<true, 128, true>;
   TensorLaunch t;
   std::memset(&t, 0, sizeof t);
   t.stream = static_cast<cudaStream_t>(c.stream);
@@ -207,7 +207,12 @@ int run_tensor(const Int8Call &c, uint32_t *err, uint64_t timeout_ns, uint64_t c
   // steps (64 rows of 1024 x 2048) 9.6 and 9.7.
   const int64_t few = units(Split::NT);
   const int pairs = few > 36 || k_blk < 8 ? 1 : few > 15 ? 2 : Split::MAX_PAIRS;
-  const int nt = pairs > 1 ? Split::NT : Fused::NT;
+  // Tiles of up to 128 rows leave shared memory for two more stages of codes, which
+  // counts where the weights' stream is the cost.  64 experts, gate/up of 2048 x 1024
+  // and down of 1024 x 2048, tiles of 128 | 192: 16 rows an expert 51.4 | 52.2 and
+  // 30.0 | 32.1 us, 96 rows 60.8 | 61.7 and 39.0 | 40.3, 128 rows (ragged) 86 | 66 and
+  // 47.5 | 42.4; the 7B projection of 128 rows 31.9 | 34.5.
+  const int nt = pairs > 1 || c.P <= (c.offsets ? 96 * c.E : Split::NT) ? Split::NT : Fused::NT;
   const uint64_t adim[2] = {K, R}, astr[1] = {K * 2};
   const uint32_t abox[2] = {64, gather ? 1u : 32u}, abox2[2] = {64, uint32_t(nt / 2)};
   const uint64_t wdim[3] = {K, N, E}, wstr[2] = {K, N * K};
@@ -236,9 +241,13 @@ int run_tensor(const Int8Call &c, uint32_t *err, uint64_t timeout_ns, uint64_t c
   p.err = err;
   p.pairs = pairs;
   t.units = units(nt);
-  const cudaError_t e = pairs > 1 ? c.fused ? launch_tensor<Int8Cfg<true, true>>(t) : launch_tensor<Int8Cfg<false, true>>(t)
-                        : c.fused ? launch_tensor<Fused>(t)
-                                  : launch_tensor<Int8Cfg<false>>(t);
+  cudaError_t e;
+  if (pairs > 1)
+    e = c.fused ? launch_tensor<Int8Cfg<true, 128, true>>(t) : launch_tensor<Int8Cfg<false, 128, true>>(t);
+  else if (nt == 128)
+    e = c.fused ? launch_tensor<Int8Cfg<true, 128>>(t) : launch_tensor<Int8Cfg<false, 128>>(t);
+  else
+    e = c.fused ? launch_tensor<Int8Cfg<true, 192>>(t) : launch_tensor<Int8Cfg<false, 192>>(t);
   return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
 }
 

@@ -201,22 +201,42 @@ __device__ __forceinline__ void warp_best(unsigned long long &key, int &e) {
   }
 }
 
+// The r-th largest (r < 32, from 0) of the warp's 32 keys: a bitonic sort.
+__device__ __forceinline__ uint32_t warp_rank(uint32_t key, int r, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int o = size / 2; o > 0; o >>= 1) {
+      const uint32_t other = __shfl_xor_sync(kAll, key, o);
+      const bool larger = ((lane & o) == 0) == ((lane & size) == 0 || size == 32);
+      key = larger ? max(key, other) : min(key, other);
+    }
+  return __shfl_sync(kAll, key, r);
+}
+
 __device__ __forceinline__ float score_of(bool sigmoid, float x, float m, float sum) {
   return sigmoid ? __frcp_rn(1.0f + expf(-x)) : __fdiv_rn(expf(x - m), sum);
 }
 __device__ __forceinline__ double score_of(bool sigmoid, double x, double m, double sum) {
   return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / sum;
 }
-// The same for the choice: the fast exp (2^-22 and |x| 2^-24 of itself) and
-// reciprocal.
+// The same for the choice: 2^x and the reciprocal of the special-function unit
+// (2^-22 of themselves, x's rounding 2^-24 |x|; what would be denormal is 0).
+__device__ __forceinline__ float quick_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+  return y;
+}
+__device__ __forceinline__ double quick_exp(double x) { return exp(x); }
 __device__ __forceinline__ float quick_score(bool sigmoid, float x, float m, float by_sum) {
-  return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-x)) : __expf(x - m) * by_sum;
+  if (!sigmoid) return quick_exp(x - m) * by_sum;
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + quick_exp(-x)));
+  return y;
 }
 __device__ __forceinline__ double quick_score(bool sigmoid, double x, double m, double by_sum) {
   return sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) * by_sum;
 }
-__device__ __forceinline__ float quick_exp(float x) { return __expf(x); }
-__device__ __forceinline__ double quick_exp(double x) { return exp(x); }
 
 // Largest error of an FP32 score that the choice goes by, as a part of the token's
 // largest one.  Sigmoid: s (1 - s) (2^-22 + |x| 2^-24) <= 2^-23 of the exp, a sum
@@ -224,14 +244,20 @@ __device__ __forceinline__ double quick_exp(double x) { return exp(x); }
 // top of two exp.
 __device__ __forceinline__ float score_error(bool sigmoid) { return sigmoid ? 0x1p-21f : 0x1p-18f; }
 
-// What a warp keeps from token to token: lane's group g is lane / L of L = 32 /
+// What a warp keeps from token to token: a lane's group is g = lane / L of L = 32 /
 // groups lanes, and its experts are first, first + L, ... below end = (g + 1) E /
-// groups.
+// groups; and 32 places of shared memory.
+struct Candidate {
+  uint32_t key;
+  int e;
+};
 template <int EPL>
 struct ScorePlan {
-  int L, g, first, end;
-  float bias[EPL <= 8 ? EPL : 1];  // of the lane's experts
-  __device__ ScorePlan(const RouteParams &p, int lane) {
+  static constexpr int KEPT = EPL <= 8 ? EPL : 1;  // biases in registers
+  int lane, L, g, first, end;
+  float bias[KEPT];
+  Candidate *found;
+  __device__ ScorePlan(const RouteParams &p, int lane_, Candidate *found_) : lane(lane_), found(found_) {
     const int size = p.E / p.groups;
     L = 32 / p.groups;
     g = lane / L;
@@ -239,24 +265,104 @@ struct ScorePlan {
     end = (g + 1) * size;
     if (EPL <= 8) {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) bias[EPL <= 8 ? i : 0] = p.bias && expert(i) < end ? __ldg(p.bias + expert(i)) : 0.0f;
+      for (int i = 0; i < KEPT; ++i) bias[i] = p.bias && expert(i) < end ? __ldg(p.bias + expert(i)) : 0.0f;
     }
   }
   __device__ int expert(int i) const { return first + L * i; }
   __device__ float bias_of(const RouteParams &p, int i) const {
-    return EPL <= 8 ? bias[EPL <= 8 ? i : 0] : __ldg(p.bias + expert(i));
+    return EPL <= 8 ? bias[EPL <= 8 ? i : 0] : expert(i) < end ? __ldg(p.bias + expert(i)) : 0.0f;
   }
 };
+
+// The `rounds` (at most 33) largest of the warp's keys (0: none), ties to the lowest
+// expert: lane j gets the j-th, every lane the last of 33.
+// A round takes the largest key and removes it.
+template <class Key, int EPL>
+__device__ __forceinline__ void choose_by_rounds(const ScorePlan<EPL> &plan, Key (&key)[EPL], int rounds, int k,
+                                                 Key &my_key, int &my_id, Key &next_key, int &next_id) {
+  my_key = next_key = 0;
+  my_id = next_id = -1;
+  for (int j = 0; j < rounds; ++j) {
+    Key b = key[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) b = max(b, key[i]);
+    // the lane's first expert that holds it; then the warp's lowest
+    int at = EPL - 1;
+#pragma unroll
+    for (int i = EPL - 2; i >= 0; --i) at = key[i] == b ? i : at;
+    int e = plan.expert(at);
+    const int own = e;
+    warp_best(b, e);
+    if (b == 0) break;  // none left: nor in the rounds to come
+    my_key = plan.lane == j ? b : my_key;
+    my_id = plan.lane == j ? e : my_id;
+    next_key = j == k ? b : Key(0);
+    next_id = j == k ? e : -1;
+    const int gone = own == e ? at : -1;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = i == gone ? Key(0) : key[i];
+  }
+}
+
+// The same by ranks, for FP32 keys and up to 32 rounds: none of the chosen lies below
+// the rounds-th largest of the lanes' own maxima, and those that do not are few; they
+// are moved to a lane each and ranked by comparing all with all.  False: more than 32.
+// (9 of 256: about 200 instructions instead of 510.)
+template <int EPL>
+__device__ __forceinline__ bool choose_by_ranks(const ScorePlan<EPL> &plan, const uint32_t (&key)[EPL], int rounds,
+                                                int k, uint32_t &my_key, int &my_id, uint32_t &next_key, int &next_id) {
+  const int lane = plan.lane;
+  uint32_t b = key[0];
+#pragma unroll
+  for (int i = 1; i < EPL; ++i) b = max(b, key[i]);
+  const uint32_t least = max(warp_rank(b, rounds - 1, lane), 1u);
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) mine += key[i] >= least;
+  int at = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int w = __shfl_up_sync(kAll, at, o);
+    if (lane >= o) at += w;
+  }
+  const int count = __shfl_sync(kAll, at, 31);
+  if (count > 32) return false;
+  at -= mine;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (key[i] >= least) plan.found[at++] = {key[i], plan.expert(i)};
+  __syncwarp();
+  const Candidate c = lane < count ? plan.found[lane] : Candidate{0u, 0x7fffffff};
+  int rank = 0;
+  for (int j = 0; j < count; ++j) {
+    const Candidate o = plan.found[j];
+    rank += o.key > c.key || (o.key == c.key && o.e < c.e);
+  }
+  __syncwarp();
+  if (lane < count) plan.found[rank] = c;
+  __syncwarp();
+  const int chosen = min(count, rounds);
+  const Candidate got = lane < chosen ? plan.found[lane] : Candidate{0u, -1};
+  const Candidate next = k < chosen ? plan.found[k] : Candidate{0u, -1};
+  __syncwarp();
+  my_key = got.key, my_id = got.e, next_key = next.key, next_id = next.e;
+  return true;
+}
+template <int EPL>
+__device__ __forceinline__ bool choose_by_ranks(const ScorePlan<EPL> &, const unsigned long long (&)[EPL], int, int,
+                                                unsigned long long &, int &, unsigned long long &, int &) {
+  return false;
+}
 
 // One token by one warp, in V = float or double: the chosen experts, lane j
 // keeping choice j.  Returns whether V decided every comparison (FP64: always).
 template <class V, int EPL>
-__device__ __forceinline__ bool choose_exactly(const RouteParams &p, const ScorePlan<EPL> &plan, int64_t t, int lane,
+__device__ __forceinline__ bool choose_exactly(const RouteParams &p, const ScorePlan<EPL> &plan, int64_t t,
                                                int &my_id, float &my_weight) {
   using Key = decltype(order_key(V()));
   constexpr bool ROUNDED = sizeof(V) == 4;
   const bool sigmoid = p.sigmoid != 0, fp32 = p.fp32 != 0, biased = p.bias != nullptr;
-  const int L = plan.L, g = plan.g;
+  const int lane = plan.lane, L = plan.L, g = plan.g;
   const float *row32 = static_cast<const float *>(p.logits) + (fp32 ? t * p.E : 0);
   const __nv_bfloat16 *row16 = static_cast<const __nv_bfloat16 *>(p.logits) + (fp32 ? 0 : t * p.E);
   auto logit = [&](int e) { return fp32 ? __ldg(row32 + e) : __bfloat162float(row16[e]); };
@@ -289,10 +395,9 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
   Key key[EPL];
   if (biased) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const Key k = x[i] == -INFINITY ? Key(0) : order_key(quick_score(sigmoid, V(x[i]), m, by_sum) + V(plan.bias_of(p, i)));
-      key[i] = plan.expert(i) < plan.end ? k : Key(0);
-    }
+    for (int i = 0; i < EPL; ++i)
+      key[i] = x[i] == -INFINITY ? Key(0)
+                                 : order_key(quick_score(sigmoid, V(x[i]), m, by_sum) + V(plan.bias_of(p, i)));
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = order_key(V(x[i]));
@@ -320,12 +425,15 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
     const V value = summed && k2 != 0 ? v1 + v2 : v1;
     const Key mine = k1 == 0 ? Key(0) : order_key(value);
     const float size12 = fmaxf(fabsf(float(v1)), k2 != 0 ? fabsf(float(v2)) : 0.0f);
-    int rank = 0;
-    for (int h = 0; h < p.groups; ++h) {
-      const Key other = __shfl_sync(kAll, mine, h * L);
-      rank += other > mine || (other == mine && h < g);
+    // the best group, kept times over
+    bool keep = false;
+    for (int j = 0; j < p.kept; ++j) {
+      Key b = keep ? Key(0) : mine;
+      int h = g;
+      warp_best(b, h);
+      if (b == 0) break;
+      keep = keep || h == g;
     }
-    const bool keep = mine != 0 && rank < p.kept;
     if (ROUNDED && (biased || summed)) {
       // the least that a kept value can be against the most that another can
       const float v = static_cast<float>(value), off = 2.0f * err + 0x1p-22f * size12;
@@ -336,30 +444,11 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = keep ? key[i] : Key(0);
   }
-  Key my_key = 0, next_key = 0;
-  int next_id = -1;
-  my_id = -1;
+  Key my_key, next_key;
+  int next_id;
   const int rounds = ROUNDED && biased ? p.k + 1 : p.k;
-  for (int j = 0; j < rounds; ++j) {
-    Key b = key[0];
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) b = max(b, key[i]);
-    // the lane's first expert that holds it; then the warp's lowest
-    int at = EPL - 1;
-#pragma unroll
-    for (int i = EPL - 2; i >= 0; --i) at = key[i] == b ? i : at;
-    int e = plan.expert(at);
-    const int own = e;
-    warp_best(b, e);
-    if (b == 0) break;  // none left: nor in the rounds to come
-    my_key = lane == j ? b : my_key;
-    my_id = lane == j ? e : my_id;
-    next_key = j == p.k ? b : Key(0);
-    next_id = j == p.k ? e : -1;
-    const int gone = own == e ? at : -1;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = i == gone ? Key(0) : key[i];
-  }
+  if (!ROUNDED || rounds > 32 || !choose_by_ranks(plan, key, rounds, p.k, my_key, my_id, next_key, next_id))
+    choose_by_rounds(plan, key, rounds, p.k, my_key, my_id, next_key, next_id);
   if (lane >= p.k) my_id = -1;
   const float mx = my_id >= 0 ? logit(my_id) : -INFINITY;
   if (ROUNDED && biased) {
@@ -389,16 +478,16 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
 }
 
 template <int EPL>
-__device__ __noinline__ void choose_in_64(const RouteParams &p, const ScorePlan<EPL> &plan, int64_t t, int lane,
-                                          int &id, float &weight) {
-  choose_exactly<double, EPL>(p, plan, t, lane, id, weight);
+__device__ __noinline__ void choose_in_64(const RouteParams &p, const ScorePlan<EPL> &plan, int64_t t, int &id,
+                                          float &weight) {
+  choose_exactly<double, EPL>(p, plan, t, id, weight);
 }
 
 // How a block chooses: by the logits, LPT lanes per token,
 template <int LPT, int EPL, bool FP32>
 struct ByLogit {
   static constexpr int LANES = LPT;
-  __device__ ByLogit(const RouteParams &, int) {}
+  __device__ ByLogit(const RouteParams &, int, void *) {}
   __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane, uint16_t *ids16) {
     swiglu::choose<LPT, EPL, FP32>(p, t, end, lane, ids16);
   }
@@ -408,12 +497,13 @@ template <int EPL>
 struct ByScore {
   static constexpr int LANES = 32;
   ScorePlan<EPL> plan;
-  __device__ ByScore(const RouteParams &p, int lane) : plan(p, lane) {}
+  __device__ ByScore(const RouteParams &p, int lane, void *spare)
+      : plan(p, lane, static_cast<Candidate *>(spare) + (threadIdx.x >> 5) * 32) {}
   __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane, uint16_t *ids16) {
     if (t >= end) return;
     int id;
     float weight;
-    if (!choose_exactly<float, EPL>(p, plan, t, lane, id, weight)) choose_in_64<EPL>(p, plan, t, lane, id, weight);
+    if (!choose_exactly<float, EPL>(p, plan, t, id, weight)) choose_in_64<EPL>(p, plan, t, id, weight);
     if (lane < p.k) {
       p.ids[t * p.k + lane] = id;
       p.weights[t * p.k + lane] = weight;
@@ -442,7 +532,7 @@ __device__ __forceinline__ void walk(const uint16_t *ids16, int i0, int i1, uint
 
 struct RouteSmem {
   uint16_t cnt[kCounters];  // [warp][E]
-  int32_t base[kMaxE];      // first place of each expert's entries
+  alignas(8) int32_t base[kMaxE];      // first place of each expert's entries
   int32_t total[kMaxE];     // entries of this block (read by the cluster's other blocks), or of the blocks before
   uint16_t ids[kBlockTokens * kMaxK];
   int32_t carry[32];
@@ -502,7 +592,9 @@ __global__ void __launch_bounds__(1024, 1) route_choose_kernel(const __grid_cons
   constexpr int SIDE = 32 / How::LANES;
   const int per = (nt + warps * SIDE - 1) / (warps * SIDE) * SIDE;
   const int t0 = min(warp * per, nt), t1 = min(t0 + per, nt);
-  How how(p, lane);
+  // (base and total, 256 bytes a warp, are not in use yet)
+  static_assert(sizeof(sm.base) + sizeof(sm.total) == 32 * 32 * sizeof(Candidate), "32 candidates a warp");
+  How how(p, lane, sm.base);
   for (int t = t0; t < t1; t += SIDE)
     how.choose(p, b0 + t + lane / How::LANES, b0 + t1, lane, sm.ids + (t + lane / How::LANES) * p.k);
   __syncwarp();

@@ -58,17 +58,17 @@ struct Int8Params {
   uint32_t *err;
 };
 
-template <bool FUSED_, bool SPLIT_ = false>
+template <bool FUSED_, int NT_, bool SPLIT_ = false>
 struct Int8Cfg {
   static constexpr bool FUSED = FUSED_;
   static constexpr bool SPLIT = SPLIT_;
   static constexpr int MAX_PAIRS = 4;            // SPLIT: pairs of a cluster
-  static constexpr int NT = SPLIT ? 128 : 192;   // most rows of a tile
+  static constexpr int NT = NT_;                 // most rows of a tile
   static constexpr int BK = 128;                 // K of a step
   static constexpr int COLS = FUSED ? 64 : 128;  // output columns per CTA
   static constexpr int BOX_BYTES = 64 * BK;      // 64 columns' codes
   static constexpr int W_BYTES = 2 * BOX_BYTES;  // W1 | W2, or two boxes of W
-  static constexpr int W_STAGES = 6;
+  static constexpr int W_STAGES = NT == 128 ? 8 : 6;
   static constexpr int HALF_BYTES = NT / 2 * 64 * 2;  // the rows' FP16 values, 64 of K
   static constexpr int A_BYTES = 2 * HALF_BYTES;
   static constexpr int A_STAGES = 4;
