@@ -39,9 +39,12 @@
 // in the `kept` groups of experts whose largest c (or two largest added) are
 // largest.  A warp per token; a group's experts lie in neighbouring lanes.  The
 // choice is that of the exact values: FP32 decides where the values compared
-// lie further apart than their rounding errors together, and a token where two
-// do not is chosen once more in FP64 (without a bias the logits' own order
-// decides, and only sums of two scores are compared).
+// lie further apart than their rounding errors together, and where two do not,
+// which is so for about a token in a thousand, FP64 settles the few values
+// concerned (without a bias the logits' own order decides, and only sums of two
+// scores are compared).  Bound by instructions: 16384 tokens, 256 experts in 8
+// groups, 39 us (55 with all scores of such a token in FP64 and a round over all
+// experts for each choice; 8 lanes of 32 experts a token instead of a warp 70).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -305,17 +308,23 @@ __device__ __forceinline__ void choose_by_rounds(const ScorePlan<EPL> &plan, Key
 }
 
 // The same by ranks, for FP32 keys and up to 32 rounds: none of the chosen lies below
-// the rounds-th largest of the lanes' own maxima, and those that do not are few; they
-// are moved to a lane each and ranked by comparing all with all.  False: more than 32.
+// the rounds-th largest of the lanes' own maxima (or, with `margin`, more than that
+// below it), and those that do not are few; they are moved to a lane each (all: how
+// many, in order), ranked by comparing all with all.  False: more than 32.
 // (9 of 256: about 200 instructions instead of 510.)
 template <int EPL>
 __device__ __forceinline__ bool choose_by_ranks(const ScorePlan<EPL> &plan, const uint32_t (&key)[EPL], int rounds,
-                                                int k, uint32_t &my_key, int &my_id, uint32_t &next_key, int &next_id) {
+                                                int k, float margin, uint32_t &my_key, int &my_id, uint32_t &next_key,
+                                                int &next_id, int &all, int &id_of_all) {
   const int lane = plan.lane;
   uint32_t b = key[0];
 #pragma unroll
   for (int i = 1; i < EPL; ++i) b = max(b, key[i]);
-  const uint32_t least = max(warp_rank(b, rounds - 1, lane), 1u);
+  uint32_t least = max(warp_rank(b, rounds - 1, lane), 1u);
+  if (margin > 0.0f && least > 1u && least != 0xffffffffu) {
+    const float v = key_value(least);
+    least = max(order_key(v - margin - 0x1p-22f * fabsf(v)), 1u);
+  }
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) mine += key[i] >= least;
@@ -341,17 +350,88 @@ __device__ __forceinline__ bool choose_by_ranks(const ScorePlan<EPL> &plan, cons
   __syncwarp();
   if (lane < count) plan.found[rank] = c;
   __syncwarp();
-  const int chosen = min(count, rounds);
-  const Candidate got = lane < chosen ? plan.found[lane] : Candidate{0u, -1};
-  const Candidate next = k < chosen ? plan.found[k] : Candidate{0u, -1};
+  const Candidate none = {0u, -1};
+  const Candidate got = lane < count ? plan.found[lane] : none, next = k < min(count, rounds) ? plan.found[k] : none;
   __syncwarp();
-  my_key = got.key, my_id = got.e, next_key = next.key, next_id = next.e;
+  all = count, id_of_all = got.e;
+  my_key = lane < rounds ? got.key : 0u, my_id = lane < rounds ? got.e : -1;
+  next_key = next.key, next_id = next.e;
   return true;
 }
+// What FP32 leaves open is settled in FP64 for the values concerned alone, one a lane
+// at a time: a warp's FP64 instruction takes about 60 cycles here, and all of 256
+// experts' scores 17 us.
+
+struct Token {  // where its logits are, and what its scores need
+  const float *row32;
+  const __nv_bfloat16 *row16;
+  double m, sum;  // softmax
+  __device__ float logit(bool fp32, int e) const { return fp32 ? __ldg(row32 + e) : __bfloat162float(row16[e]); }
+};
+
+// Expert e's score, with its bias.
+__device__ __forceinline__ double worth_in_64(const RouteParams &p, const Token &token, int e) {
+  const double s = score_of(p.sigmoid != 0, double(token.logit(p.fp32 != 0, e)), token.m, token.sum);
+  return p.bias ? s + double(__ldg(p.bias + e)) : s;
+}
+
 template <int EPL>
-__device__ __forceinline__ bool choose_by_ranks(const ScorePlan<EPL> &, const unsigned long long (&)[EPL], int, int,
-                                                unsigned long long &, int &, unsigned long long &, int &) {
-  return false;
+__device__ __noinline__ void sum_in_64(const RouteParams &p, const ScorePlan<EPL> &plan, Token &token) {
+  double sum = 0;
+  for (int i = 0; i < EPL; ++i)
+    if (plan.expert(i) < plan.end) sum += exp(double(token.logit(p.fp32 != 0, plan.expert(i))) - token.m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  token.sum = sum;
+}
+
+// Whether the lane's group is kept; `close`: which of the lane's experts may be among
+// the group's best (one or two).
+template <int EPL>
+__device__ __noinline__ bool keep_in_64(const RouteParams &p, const ScorePlan<EPL> &plan, const Token &token,
+                                        unsigned close) {
+  unsigned long long k1 = 0, k2 = 0;
+  while (__any_sync(kAll, close != 0)) {
+    unsigned long long k = 0;
+    if (close != 0) k = order_key(worth_in_64(p, token, plan.expert(__ffs(close) - 1)));
+    close &= close - 1;
+    k2 = max(k2, min(k1, k));
+    k1 = max(k1, k);
+  }
+  for (int o = 1; o < plan.L; o <<= 1) {
+    const unsigned long long j1 = __shfl_xor_sync(kAll, k1, o), j2 = __shfl_xor_sync(kAll, k2, o);
+    k2 = max(min(k1, j1), max(k2, j2));
+    k1 = max(k1, j1);
+  }
+  unsigned long long mine = k1;
+  if (p.best == 2 && k1 != 0 && k2 != 0) mine = order_key(key_value(k1) + key_value(k2));
+  bool keep = false;
+  for (int j = 0; j < p.kept; ++j) {
+    unsigned long long b = keep ? 0ull : mine;
+    int h = plan.g;
+    warp_best(b, h);
+    if (b == 0) break;
+    keep = keep || h == plan.g;
+  }
+  return keep;
+}
+
+// The candidates (lane i < all has expert id) in order: lane j gets the j-th.
+__device__ __noinline__ int rank_in_64(const RouteParams &p, const Token &token, Candidate *found, int lane, int all,
+                                       int id) {
+  const unsigned long long key = lane < all ? order_key(worth_in_64(p, token, id)) : 0ull;
+  int rank = 0;
+  for (int j = 0; j < all; ++j) {
+    const unsigned long long k = __shfl_sync(kAll, key, j);
+    const int e = __shfl_sync(kAll, id, j);
+    rank += k > key || (k == key && e < id);
+  }
+  __syncwarp();
+  if (lane < all) found[rank].e = id;
+  __syncwarp();
+  const int e = lane < all ? found[lane].e : -1;
+  __syncwarp();
+  return e;
 }
 
 // One token by one warp, in V = float or double: the chosen experts, lane j
@@ -391,6 +471,7 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
     largest = static_cast<float>(by_sum);
   }
   const float err = score_error(sigmoid) * largest;  // of one score
+  [[maybe_unused]] Token token = {row32, row16, double(m), 0.0};
   // s + b, or the logit where no bias is given; 0 for no expert
   Key key[EPL];
   if (biased) {
@@ -434,12 +515,25 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
       if (b == 0) break;
       keep = keep || h == g;
     }
-    if (ROUNDED && (biased || summed)) {
-      // the least that a kept value can be against the most that another can
-      const float v = static_cast<float>(value), off = 2.0f * err + 0x1p-22f * size12;
-      const uint32_t low = __reduce_min_sync(kAll, keep ? order_key(v - off) : 0xffffffffu);
-      const uint32_t high = __reduce_max_sync(kAll, keep || mine == 0 ? 0u : order_key(v + off));
-      if (high >= low) sure = false;
+    if constexpr (ROUNDED) {
+      if (biased || summed) {
+        // the least that a kept value can be against the most that another can
+        const float off = 2.0f * err + 0x1p-22f * size12;
+        const uint32_t low = __reduce_min_sync(kAll, keep ? order_key(value - off) : 0xffffffffu);
+        const uint32_t high = __reduce_max_sync(kAll, keep || mine == 0 ? 0u : order_key(value + off));
+        if (high >= low) {  // (of the whole warp)
+          if (!sigmoid && token.sum == 0.0) sum_in_64(p, plan, token);
+          // experts within two errors of the group's last that counts; without a bias
+          // the keys are logits, in whose order nothing is open
+          const Key last = summed && k2 != 0 ? k2 : k1;
+          const float v = key_value(last);
+          const Key least = biased ? order_key(v - 2.0f * err - 0x1p-22f * fabsf(v)) : last;
+          unsigned close = 0;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) close |= key[i] != 0 && key[i] >= least ? 1u << i : 0u;
+          keep = keep_in_64(p, plan, token, close);
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = keep ? key[i] : Key(0);
@@ -447,10 +541,14 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
   Key my_key, next_key;
   int next_id;
   const int rounds = ROUNDED && biased ? p.k + 1 : p.k;
-  if (!ROUNDED || rounds > 32 || !choose_by_ranks(plan, key, rounds, p.k, my_key, my_id, next_key, next_id))
-    choose_by_rounds(plan, key, rounds, p.k, my_key, my_id, next_key, next_id);
+  int all = 0, id_of_all = -1;  // of the candidates
+  bool ranked = false;
+  if constexpr (ROUNDED)
+    ranked = rounds <= 32 && choose_by_ranks(plan, key, rounds, p.k, biased ? 2.0f * err : 0.0f, my_key, my_id,
+                                             next_key, next_id, all, id_of_all);
+  if (!ranked) choose_by_rounds(plan, key, rounds, p.k, my_key, my_id, next_key, next_id);
   if (lane >= p.k) my_id = -1;
-  const float mx = my_id >= 0 ? logit(my_id) : -INFINITY;
+  float mx = my_id >= 0 ? logit(my_id) : -INFINITY;
   if (ROUNDED && biased) {
     // each choice against the next one; equal logits with equal biases are a
     // true tie, which the expert's number has settled
@@ -463,6 +561,15 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
     if (lane < p.k && my_key != 0 && ok != 0 && !(ox == mx && ob == mb)) {
       const float a = float(key_value(my_key)), b = float(key_value(ok));
       if (a - b <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(a), fabsf(b))) sure = false;
+    }
+    if constexpr (ROUNDED) {
+      if (ranked && !__all_sync(kAll, sure)) {
+        if (!sigmoid && token.sum == 0.0) sum_in_64(p, plan, token);
+        my_id = rank_in_64(p, token, plan.found, lane, all, id_of_all);
+        if (lane >= p.k) my_id = -1;
+        mx = my_id >= 0 ? logit(my_id) : -INFINITY;
+        sure = true;
+      }
     }
   }
   V w = my_id >= 0 ? score_of(sigmoid, V(mx), m, sum) : V(0);
