@@ -13,8 +13,8 @@
 //     16-bit operands, and widened straight into tensor memory, as the MMA's A
 //     operand: K-major codes give a thread its lane's K in 16-byte loads, and
 //     shared memory, which feeds copies, loads and the MMA's B operand alike, is
-//     spared their 16-bit form.  Groups of four warps take halves of 64 of K in
-//     turn;
+//     spared their 16-bit form.  Two groups of four warps take a half of 64 of K
+//     each;
 //   * the rows come as FP16, widened once per call by a small kernel before this
 //     one (k_int8.cu): widened here they cost as many instructions as the
 //     weights, once for each column tile (7B projection, 2047 rows: MEASURE);
@@ -78,17 +78,20 @@ struct Int8Cfg {
   // 16-byte reads of eight rows touch every bank once), FUSED 16 x 16 (48 apart)
   static constexpr int STG_PITCH = FUSED ? 48 : 80;
   static constexpr int STG_BYTES = 1280;
+  static constexpr int SCALE_BYTES = 96 * 4;     // and the scales of the rows it finishes
   static constexpr int A_OFF = W_STAGES * W_BYTES;
   static constexpr int STG_OFF = A_OFF + A_STAGES * A_BYTES;
-  static constexpr int TAB_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
+  static constexpr int SCALE_OFF = STG_OFF + EPI_WARPS * STG_BYTES;
+  static constexpr int TAB_OFF = SCALE_OFF + EPI_WARPS * SCALE_BYTES;
   static constexpr int TAB_BYTES = 2 * (kMaxExperts + 1) * 4;
   static constexpr int UNIT_OFF = (TAB_OFF + TAB_BYTES + 15) / 16 * 16;  // two blocks of 32 units
   static constexpr int BAR_OFF = UNIT_OFF + 2 * 32 * 16;
   static constexpr int NUM_BARS = 2 * W_STAGES + 2 * A_STAGES + BUFS + 9;
   static constexpr int SMEM_BYTES = BAR_OFF + NUM_BARS * 8 + 16 + 1024;
   static constexpr int W_WARP = EPI_WARPS;       // first of those that widen weights
-  static constexpr int W_GROUPS = 3;             // of four warps
-  static constexpr int PRODUCER_WARP = W_WARP + 4 * W_GROUPS;
+  // Two groups of four: gate/up of 8192 tokens 363 us, three 368, four (and four
+  // warps that copy rows) 437; the 7B projection 300 all.
+  static constexpr int PRODUCER_WARP = W_WARP + 8;
   static constexpr int MMA_WARP = PRODUCER_WARP + 1;
   static constexpr int UNIT_WARP = MMA_WARP + 1;
   static constexpr int LOAD_WARP = UNIT_WARP + 1;  // first of those that copy rows
@@ -123,6 +126,16 @@ __device__ __forceinline__ static uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
+// SiLU(g) u with the special-function unit's 2^x and reciprocal as they are: the
+// range handling of __expf and __fdividef is a fifth of the epilogue's instructions.
+// exp(-g) beyond FP32 gives 0 (g < -88, where |SiLU| < 1e-36).
+__device__ __forceinline__ static float quick_silu_mul(float g, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r * u;
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     swiglu_int8_kernel(const __grid_constant__ CUtensorMap tmA,   // dense: boxes of 32 rows; gathered: one row
@@ -178,7 +191,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       ptx::mbar_init(unitf_bar + 8u * b, 1);
       // readers of the units: epilogue, widening warps, weights' thread, rows'
       // threads and, in the leader, the MMA's
-      ptx::mbar_init(unite_bar + 8u * b, C::EPI_WARPS + 4 * C::W_GROUPS + 1 + loaders + (rank == 0 ? 1 : 0));
+      ptx::mbar_init(unite_bar + 8u * b, C::EPI_WARPS + 8 + 1 + loaders + (rank == 0 ? 1 : 0));
     }
     ptx::mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -214,14 +227,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const int lcol = C::FUSED ? (lane >> 1) ^ (up ? 4 : 0) : lane;  // the lane's column in the warp's
   GroupedUnit mine = {-1, -1, 0, 0};  // the tile at hand
   bool have = false;                  // SPLIT: its sums are complete
-  float w1 = 0.0f, w2 = 0.0f, sa[3];
+  float w1 = 0.0f, w2 = 0.0f;
   unsigned named[3];
+  float *const scales = reinterpret_cast<float *>(smem + C::SCALE_OFF + (warp & 7) * C::SCALE_BYTES);
   auto tile_col = [&] {  // the warp's first column
     return (mine.nb * 2 + static_cast<int>(rank)) * C::COLS + (C::FUSED ? 16 * q : 32 * q);
   };
-  // The scales of the lane's column, and of the rows of this warp's chunks: lane
-  // l, word j is row l % 16 of the warp's chunk 2 j + l / 16, and a bit that
-  // tells whether it names a row of A.
+  // The scales of the lane's column and, in shared memory, of the rows of this
+  // warp's chunks (16 each), with a bit that tells whether one names a row of A.
   auto load_scales = [&] {
     w1 = w2 = 0.0f;
     if (tile_col() + lcol < p.N) {
@@ -235,9 +248,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int src = -1;
       if (row < mine.end) src = p.rows ? __ldg(p.rows + row) : row;
       const bool valid = src >= 0 && src < p.T;
-      sa[j] = valid ? __ldg(p.sa + src) : 0.0f;
+      scales[32 * j + lane] = valid ? __ldg(p.sa + src) : 0.0f;
       named[j] = __ballot_sync(0xffffffffu, valid);
     }
+    __syncwarp();
   };
   // SPLIT: the pair that finishes chunk c, and the chunk's number there.
   auto owner = [&](int c) { return (c >> 1) % p.pairs; };
@@ -270,28 +284,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_cluster_relaxed(release);
       }
-      const float s16 = i < 2 ? sa[0] : i < 4 ? sa[1] : sa[2];
       const unsigned ok16 = (i < 2 ? named[0] : i < 4 ? named[1] : named[2]) >> (16 * (i & 1));
       if constexpr (C::FUSED) {
         // even lanes finish the chunk's first 8 rows, odd lanes the last 8
         const int first = up ? 8 : 0;
+        const float4 sl = *reinterpret_cast<const float4 *>(scales + 16 * i + first);
+        const float4 sh = *reinterpret_cast<const float4 *>(scales + 16 * i + first + 4);
+        const float s[8] = {sl.x, sl.y, sl.z, sl.w, sh.x, sh.y, sh.z, sh.w};
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const uint32_t give = up ? v[r] : v[8 + r];
           const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, give, 9));
           const float mv = __uint_as_float(up ? v[8 + r] : v[r]);
-          const float s = __shfl_sync(0xffffffffu, s16, 16 * (i & 1) + first + r);
-          const float y = silu_mul((up ? got : mv) * s * w1, (up ? mv : got) * s * w2);
+          const float y = quick_silu_mul((up ? got : mv) * s[r] * w1, (up ? mv : got) * s[r] * w2);
           const __nv_bfloat16 b = __float2bfloat16_rn(y);
           // (rows 8-15 are 32 bytes further: their banks are not rows 0-7's)
           asm volatile("st.shared.b16 [%0], %1;" ::"r"(stg + (first + r) * C::STG_PITCH + first * 4 + lcol * 2),
                        "h"(*reinterpret_cast<const uint16_t *>(&b)) : "memory");
         }
       } else {
+        float4 s[4];  // (loaded before any store, which they would wait for)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[r] = *reinterpret_cast<const float4 *>(scales + 16 * i + 4 * r);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const float s = __shfl_sync(0xffffffffu, s16, 16 * (i & 1) + r);
-          const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(v[r]) * s * w1);
+          const float4 &s4 = s[r / 4];
+          const float sr = r % 4 == 0 ? s4.x : r % 4 == 1 ? s4.y : r % 4 == 2 ? s4.z : s4.w;
+          const __nv_bfloat16 b = __float2bfloat16_rn(__uint_as_float(v[r]) * sr * w1);
           asm volatile("st.shared.b16 [%0], %1;" ::"r"(stg + r * C::STG_PITCH + lcol * 2),
                        "h"(*reinterpret_cast<const uint16_t *>(&b)) : "memory");
         }
@@ -338,25 +357,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // the lane's row of codes: a column of W1 or W2 (FUSED), of either half of W
     const int col = C::FUSED ? 16 * q + ((lane >> 1) ^ (lane & 1 ? 4 : 0)) : (32 * q + lane) & 63;
     const int box = C::FUSED ? lane & 1 : q >> 1;
-    const uint32_t src = base + box * C::BOX_BYTES + col * C::BK;
-    const uint32_t dst = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + C::OP_COL;
-    uint32_t half = (warp - C::W_WARP) >> 2, end = 0;  // this group's half steps: every W_GROUPS-th
+    const uint32_t half = (warp - C::W_WARP) >> 2;
+    uint32_t src[4];  // 16 codes each, in the first stage
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      src[i] = base + box * C::BOX_BYTES + col * C::BK + (((4 * half + i) ^ (col & 7)) << 4);
+    const uint32_t dst = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + C::OP_COL + half * 32;
+    uint32_t stage = 0, phase = 0, step = 0;
     bool ok = true;
     GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
     GroupedUnit un;
     while (ok && units.next(un, ok)) {
-      for (end += 2 * (kb1 - kb0); half < end; half += C::W_GROUPS) {
-        const uint32_t step = half / 2, buf = step % C::BUFS, stage = step % C::W_STAGES;
-        ok = __all_sync(0xffffffffu, wait(full_bar(stage), step / C::W_STAGES & 1u, WAIT_MMA_FULL));
+      for (int kb = kb0; kb < kb1; ++kb, ++step) {
+        const uint32_t buf = step % C::BUFS;
+        ok = __all_sync(0xffffffffu, wait(full_bar(stage), phase, WAIT_MMA_FULL));
         if (!ok) break;
         uint32_t o[32];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint4 v = lds128(src + stage * C::W_BYTES + (((4 * (half & 1u) + t) ^ (col & 7)) << 4));
-          widen4(v.x, o[8 * t], o[8 * t + 1]);
-          widen4(v.y, o[8 * t + 2], o[8 * t + 3]);
-          widen4(v.z, o[8 * t + 4], o[8 * t + 5]);
-          widen4(v.w, o[8 * t + 6], o[8 * t + 7]);
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = lds128(src[i] + stage * C::W_BYTES);
+          widen4(v.x, o[8 * i], o[8 * i + 1]);
+          widen4(v.y, o[8 * i + 2], o[8 * i + 3]);
+          widen4(v.z, o[8 * i + 4], o[8 * i + 5]);
+          widen4(v.w, o[8 * i + 6], o[8 * i + 7]);
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(empty_bar(stage));
@@ -366,12 +389,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (!ok) break;
           ptx::tc_fence_after();
         }
-        ptx::tmem_st32(dst + buf * 64 + (half & 1u) * 32, o);
+        ptx::tmem_st32(dst + buf * 64, o);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
         // (relaxed: the stores into tensor memory are complete)
         if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(op_bar(buf), lead));
+        if (++stage == C::W_STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
     __syncwarp();
@@ -476,21 +503,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint32_t fb = ptx::mapa_shared(rows_bar(slot), lead);
           if (rank == 0 && w == 0) ptx::mbar_arrive_expect_tx(rows_bar(slot), bytes);
           ptx::mbar_arrive_cluster_relaxed(fb);
+          const uint32_t sa = base + C::A_OFF + slot * C::A_BYTES;
+          const int k = kb * C::BK;
+          if (gather) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t sa = base + C::A_OFF + slot * C::A_BYTES + h * C::HALF_BYTES;
-            const int k = kb * C::BK + 64 * h;
-            if (gather) {
-#pragma unroll
-              for (int j = 0; j < PER; ++j) {
-                const int g = w + j * C::LOAD_WARPS;
-                if (4 * g < rows)
-                  ptx::tma_gather4_pair(sa + g * 512, &tmA, fb, k, idx[j][0], idx[j][1], idx[j][2], idx[j][3]);
+            for (int j = 0; j < PER; ++j) {
+              const int g = w + j * C::LOAD_WARPS;
+              if (4 * g < rows) {
+                ptx::tma_gather4_pair(sa + g * 512, &tmA, fb, k, idx[j][0], idx[j][1], idx[j][2], idx[j][3]);
+                ptx::tma_gather4_pair(sa + C::HALF_BYTES + g * 512, &tmA, fb, k + 64, idx[j][0], idx[j][1], idx[j][2],
+                                      idx[j][3]);
               }
-            } else if (rows > C::NT / 2 - 32) {
-              ptx::tma_load_2d_pair(sa, &tmA2, fb, k, row0);
-            } else {
-              for (int i = 0; i < rows; i += 32) ptx::tma_load_2d_pair(sa + i * 128, &tmA, fb, k, row0 + i);
+            }
+          } else if (rows > C::NT / 2 - 32) {
+            ptx::tma_load_2d_pair(sa, &tmA2, fb, k, row0);
+            ptx::tma_load_2d_pair(sa + C::HALF_BYTES, &tmA2, fb, k + 64, row0);
+          } else {
+            for (int i = 0; i < rows; i += 32) {
+              ptx::tma_load_2d_pair(sa + i * 128, &tmA, fb, k, row0 + i);
+              ptx::tma_load_2d_pair(sa + C::HALF_BYTES + i * 128, &tmA, fb, k + 64, row0 + i);
             }
           }
         }
