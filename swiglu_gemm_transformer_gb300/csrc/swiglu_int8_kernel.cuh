@@ -230,28 +230,46 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   float w1 = 0.0f, w2 = 0.0f;
   unsigned named[3];
   float *const scales = reinterpret_cast<float *>(smem + C::SCALE_OFF + (warp & 7) * C::SCALE_BYTES);
-  auto tile_col = [&] {  // the warp's first column
-    return (mine.nb * 2 + static_cast<int>(rank)) * C::COLS + (C::FUSED ? 16 * q : 32 * q);
+  auto tile_col = [&](const GroupedUnit &u) {  // the warp's first column
+    return (u.nb * 2 + static_cast<int>(rank)) * C::COLS + (C::FUSED ? 16 * q : 32 * q);
   };
-  // The scales of the lane's column and, in shared memory, of the rows of this
-  // warp's chunks (16 each), with a bit that tells whether one names a row of A.
-  auto load_scales = [&] {
-    w1 = w2 = 0.0f;
-    if (tile_col() + lcol < p.N) {
-      const int64_t at = int64_t(mine.e) * p.N + tile_col() + lcol;
-      w1 = __ldg(p.s1 + at);
-      if (C::FUSED) w2 = __ldg(p.s2 + at);
+  // The next tile's scales: of the lane's column, and of the rows of this warp's
+  // chunks (16 each; lane l, word j is row l % 16 of the warp's chunk 2 j + l / 16),
+  // with a bit that tells whether one names a row of A.  They are loaded while a
+  // tile is finished: the two trips to memory took as long as half a tile of 1024
+  // of K.
+  GroupedUnit next = {-1, -1, 0, 0};
+  float next_w1 = 0.0f, next_w2 = 0.0f, next_sa[3];
+  int next_src[3];
+  auto load_names = [&] {
+    const int col = tile_col(next) + lcol;
+    next_w1 = next_w2 = 0.0f;
+    if (col < p.N) {
+      next_w1 = __ldg(p.s1 + int64_t(next.e) * p.N + col);
+      if (C::FUSED) next_w2 = __ldg(p.s2 + int64_t(next.e) * p.N + col);
     }
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-      const int row = mine.row0 + 16 * (h + 2 * (2 * j + (lane >> 4))) + (lane & 15);
-      int src = -1;
-      if (row < mine.end) src = p.rows ? __ldg(p.rows + row) : row;
-      const bool valid = src >= 0 && src < p.T;
-      scales[32 * j + lane] = valid ? __ldg(p.sa + src) : 0.0f;
-      named[j] = __ballot_sync(0xffffffffu, valid);
+      const int row = next.row0 + 16 * (h + 2 * (2 * j + (lane >> 4))) + (lane & 15);
+      next_src[j] = -1;
+      if (row < next.end) next_src[j] = p.rows ? __ldg(p.rows + row) : row;
+    }
+  };
+  auto load_scales = [&] {
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      next_sa[j] = next_src[j] >= 0 && next_src[j] < p.T ? __ldg(p.sa + next_src[j]) : 0.0f;
+  };
+  auto take_scales = [&] {
+    w1 = next_w1;
+    w2 = next_w2;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      scales[32 * j + lane] = next_sa[j];
+      named[j] = __ballot_sync(0xffffffffu, next_src[j] >= 0 && next_src[j] < p.T);
     }
     __syncwarp();
+    mine = next;
   };
   // SPLIT: the pair that finishes chunk c, and the chunk's number there.
   auto owner = [&](int c) { return (c >> 1) % p.pairs; };
@@ -260,7 +278,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   // `release` (cluster address) once the warp has read it.
   auto finish = [&](uint32_t tacc, uint32_t release) {
     const uint32_t stg = base + C::STG_OFF + warp * C::STG_BYTES;
-    const int nchunk = mine.n() / 16, col0 = tile_col();
+    const int nchunk = mine.n() / 16, col0 = tile_col(mine);
     if (!C::SPLIT && h >= nchunk) {
       ptx::tc_fence_before();
       __syncwarp();
@@ -335,16 +353,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // ------------------------------------------------------------ epilogue
     uint32_t abuf = 0, aphase = 0;
     GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
-    bool ok = true;
-    while (units.next(mine, ok)) {
+    bool ok = true, more = units.next(next, ok);
+    if (more) {
+      load_names();
       load_scales();
-      ok = __all_sync(0xffffffffu, wait(accf + 8u * abuf, aphase, WAIT_EPI_ACC_FULL));
+    }
+    while (more) {
+      take_scales();
+      more = !C::SPLIT && units.next(next, ok);
+      if (more) load_names();
+      ok = __all_sync(0xffffffffu, ok && wait(accf + 8u * abuf, aphase, WAIT_EPI_ACC_FULL));
       if (!ok) break;
       ptx::tc_fence_after();
       if constexpr (C::SPLIT) {  // the only unit: its sums meet after the roles
         have = true;
         break;
       }
+      if (more) load_scales();
       finish(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + abuf * C::ACC_COLS,
              ptx::mapa_shared(acce + 8u * abuf, lead));
       if (++abuf == 2) {
