@@ -124,15 +124,17 @@ cudaError_t run_rows(Int8RowsParams &p, bool fused, cudaStream_t s) {
   // One row, or places that hardly share experts: a block for each place, whose
   // warps take one, two or four columns of each matrix, as many as leave four blocks
   // to each of the 152 SMs (one row of 18944 x 3584 with four columns 25.1 us, so
-  // 15.2).
+  // 15.2; of 4096 x 8192 11.0 and 8.4).  Grouped, two blocks: a block begins with
+  // the search for its expert (one token, 8 of 64 experts, 2048 x 1024, gate/up 9.3
+  // and 8.5 us, down 7.2 and 5.8).
   if (p.P == 1 || (p.offsets && 4 * p.P <= p.E)) {
-    const int64_t work = int64_t(p.N) * p.P;  // columns
+    const int64_t cols = int64_t(p.N) * p.P / (8 * 152 * (p.offsets ? 2 : 4));  // of a warp
     if (fused)
-      return work >= 16 * 608 ? launch_rows(swiglu_int8_token_kernel<true, 2, 8>, p, p.P, 16, s)
-                              : launch_rows(swiglu_int8_token_kernel<true, 1, 8>, p, p.P, 8, s);
-    return work >= 32 * 608   ? launch_rows(swiglu_int8_token_kernel<false, 4, 8>, p, p.P, 32, s)
-           : work >= 16 * 608 ? launch_rows(swiglu_int8_token_kernel<false, 2, 8>, p, p.P, 16, s)
-                              : launch_rows(swiglu_int8_token_kernel<false, 1, 8>, p, p.P, 8, s);
+      return cols >= 2 ? launch_rows(swiglu_int8_token_kernel<true, 2, 8>, p, p.P, 16, s)
+                       : launch_rows(swiglu_int8_token_kernel<true, 1, 8>, p, p.P, 8, s);
+    return cols >= 4   ? launch_rows(swiglu_int8_token_kernel<false, 4, 8>, p, p.P, 32, s)
+           : cols >= 2 ? launch_rows(swiglu_int8_token_kernel<false, 2, 8>, p, p.P, 16, s)
+                       : launch_rows(swiglu_int8_token_kernel<false, 1, 8>, p, p.P, 8, s);
   }
   return launch_rows(fused ? swiglu_int8_rows_kernel<true, 8> : swiglu_int8_rows_kernel<false, 8>, p,
                      p.offsets ? p.P : ceil_div(p.P, 8), 16, s);
