@@ -499,7 +499,7 @@ int swiglu_quant_int8(const void *X, int32_t x_fp32, void *Q, float *scale, int6
  *       (dense: T = P = M, E = 0; 0 for a few rows, then may be NULL; 0 too for
  *       sizes that the call refuses), 16-byte aligned, overlapping no other
  *       buffer: the rows in 16 bits
- * K a multiple of 16 below 2^20, N a multiple of 8, N * K < 2^40; A, W and Y
+ * K a multiple of 16 up to 2^20 - 1024, N a multiple of 8, N * K < 2^40; A, W and Y
  * 16-byte aligned, scales 4-byte; Y overlaps no input; the rest as in
  * swiglu_fused_grouped (M or P = 0 enqueues nothing, K = 0 or T = 0 fills Y
  * with zeros, a row number outside [0, T) gives a row of zeros).

@@ -17,7 +17,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 // Places and columns: the last tile's bounds, up to 256 past them, are 32-bit too.
 constexpr int64_t kMaxTiled = kMaxDim - 256;
-constexpr int64_t kMaxK = (int64_t(1) << 20) - 16;  // a warp's sum of 128 * 128 * K / 8
+// A warp of the rows kernel adds 128 * 128 * K / 8 at most, in whole turns of 1024 of K.
+constexpr int64_t kMaxK = (int64_t(1) << 20) - 1024;
 
 struct Int8Call {
   const void *A, *W1, *W2;  // W2 == nullptr: the linear form
@@ -43,7 +44,9 @@ struct Int8Call {
 // 30.2; of 2 MB, 16 places 8.3 | 9.4, 32 places 11.3 | 9.6.
 bool few_rows(int64_t P, int64_t E, int64_t N, int64_t K, bool fused) {
   const int64_t bytes = N * K * (fused ? 2 : 1);
-  if (E > 0) return P <= 16 || (bytes >= 4000000 && P <= std::max<int64_t>(32, std::min<int64_t>(E, 64)));
+  if (E > 0)
+    return (P <= 16 || (bytes >= 4000000 && P <= std::max<int64_t>(32, std::min<int64_t>(E, 64)))) &&
+           P * ceil_div(N, 8) <= kMaxDim;  // blocks
   const int64_t tiles = ceil_div(P, 8);
   return tiles == 1 || (tiles <= 16 && bytes <= 200000000 / (9 * tiles - 11));
 }

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(32 * WARPS) swiglu_int8_token_kernel(const __g
       for (int c = 0; c < NC; ++c) acc[m][c] = dot16(v[m][c], x, acc[m][c]);
   }
   __syncwarp();
-  // (a lane's sum stays below 2^31 for K < 2^20, the warp's for K < 2^17)
+  // (a lane's sum stays below 2^31 up to the largest K, the warp's for K < 2^17)
   const bool wide = p.K >= 1 << 17;
   float z[MATS] = {};
 #pragma unroll
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(32 * WARPS) swiglu_int8_token_kernel(const __g
     }
   if (mine) {
     float y = 0.0f;  // a row number that names no row of A gives zeros
-    if (named) y = FUSED ? silu_mul(z[0] * s * s1, z[MATS - 1] * s * s2) : z[0] * s * s1;
+    if (named) y = FUSED ? quick_silu_mul(z[0] * s * s1, z[MATS - 1] * s * s2) : z[0] * s * s1;
     p.Y[int64_t(row) * p.N + col0 + lane] = __float2bfloat16_rn(y);
   }
 }
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(32 * WARPS, 3) swiglu_int8_rows_kernel(const _
     const int from = row_of(r);
     float y = 0.0f;  // a row number that names no row of A gives zeros
     if (from >= 0 && from < p.T) {
-      // (a warp's sum stays below 2^31 for K < 2^20, the block's perhaps not)
+      // (a warp's sum stays below 2^31 up to the largest K, the block's perhaps not)
       long long z[MATS] = {};
 #pragma unroll
       for (int m = 0; m < MATS; ++m)
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(32 * WARPS, 3) swiglu_int8_rows_kernel(const _
       const float s = __ldg(p.sa + from);
       const int64_t at = int64_t(e) * p.N + col;
       y = static_cast<float>(z[0]) * s * __ldg(p.s1 + at);
-      if (FUSED) y = silu_mul(y, static_cast<float>(z[MATS - 1]) * s * __ldg(p.s2 + at));
+      if (FUSED) y = quick_silu_mul(y, static_cast<float>(z[MATS - 1]) * s * __ldg(p.s2 + at));
     }
     p.Y[int64_t(row0 + r) * p.N + col] = __float2bfloat16_rn(y);
   }

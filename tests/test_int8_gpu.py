@@ -278,7 +278,7 @@ def test_sums_past_24_bits(sg, fused, M):
     check_product(sg, fused, [M], 136, 9216, dense=True, full=True)
 
 
-@pytest.mark.parametrize("M", [2, 40])
+@pytest.mark.parametrize("M", [1, 2, 40, 200])
 def test_sums_are_exact_up_to_24_bits(sg, M):
     """K = 1024 products of 127 or 128 squared, told apart by one: scales of one make Z the rounded integer."""
     K, N = 1024, 64
@@ -404,6 +404,82 @@ def test_binding_refusals(sg):
         with pytest.raises(err):
             call()
     _status(sg)
+
+
+def test_the_longest_k_of_the_largest_codes(sg):
+    K = (1 << 20) - 1024
+    A, W = torch.full((8, K), -128, dtype=I8, device=DEV), torch.full((16, K), -128, dtype=I8, device=DEV)
+    a, w = torch.full((8,), 2.0**-20, device=DEV), torch.full((16,), 2.0**-14, device=DEV)
+    for M in (1, 8):
+        assert (sg.swiglu_linear_int8(A[:M], a[:M], W, w).float() == torch.tensor(K * 2.0**-20).to(BF).float()).all()
+    with pytest.raises(sg.SwigluError):
+        sg.swiglu_linear_int8(torch.zeros(1, K + 16, dtype=I8, device=DEV), a[:1], torch.zeros(16, K + 16, dtype=I8, device=DEV), w)
+
+
+def test_rows_alone_and_together_give_the_same_bits(sg):
+    """A row's result does not depend on how many rows the call has (sums below 2^24 are exact in every form)."""
+    gen = _gen("alone")
+    q = lambda *s: torch.randint(-127, 128, s, generator=gen).to(I8).to(DEV)  # noqa: E731
+    A, a = q(400, 1024), (torch.rand(400, generator=gen) * 0.01).to(DEV)
+    W1, W2 = ((q(520, 1024), (torch.rand(520, generator=gen) * 0.01).to(DEV)) for _ in range(2))
+    for fn, ws in ((sg.swiglu_fused_int8, (*W1, *W2)), (sg.swiglu_linear_int8, W1)):
+        whole = fn(A, a, *ws)
+        for m in (1, 7, 30, 150):
+            assert torch.equal(fn(A[:m], a[:m], *ws), whole[:m])
+
+
+@pytest.mark.parametrize("K", [16, 48])
+def test_output_past_32_bits(sg, K):
+    P, N = 70016, 32768          # 2.3e9 outputs
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    A = torch.randint(-127, 128, (P, K), generator=gen, device=DEV).to(I8)
+    W = torch.randint(-127, 128, (2, N, K), generator=gen, device=DEV).to(I8)
+    a, w = torch.rand(P, generator=gen, device=DEV) * 0.01, torch.rand(2, N, generator=gen, device=DEV) * 0.01
+    off = torch.tensor([0, 40000, P], dtype=torch.int32, device=DEV)
+    Z = sg.swiglu_linear_grouped_int8(A, a, W, w, off)
+    _status(sg)
+    for i, j, e in ((0, 3, 0), (39998, 40000, 0), (40000, 40002, 1), (65530, 65545, 1), (P - 3, P, 1)):
+        ref, tol = product_ref(A[i:j], a[i:j], [(W[e:e + 1], w[e:e + 1])], [0, j - i], None)
+        assert ((Z[i:j].double() - ref).abs() <= tol).all(), (i, j)
+
+
+@pytest.mark.parametrize("P", [6, 70, 3000])
+def test_weights_past_32_bits(sg, P):
+    E, N, K = 40, 28672, 2048    # 2.3e9 weights
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    W, w = torch.empty(E, N, K, dtype=I8, device=DEV), torch.rand(E, N, generator=gen, device=DEV) * 1e-3
+    for e in range(E):
+        W[e] = torch.randint(-127, 128, (N, K), generator=gen, device=DEV)
+    A, a = torch.randint(-127, 128, (P, K), generator=gen, device=DEV).to(I8), torch.rand(P, generator=gen, device=DEV) * 0.01
+    cut = [0, P // 3, P // 3 + 3 * P // 6, P]
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[36:], off[38:], off[40:] = cut[1], cut[2], cut[3]
+    Z = sg.swiglu_linear_grouped_int8(A, a, W, w, off.to(DEV))
+    _status(sg)
+    for i, e in zip(range(3), (35, 37, 39)):
+        x, y = cut[i], min(cut[i + 1], cut[i] + 40)
+        ref, tol = product_ref(A[x:y], a[x:y], [(W[e:e + 1], w[e:e + 1])], [0, y - x], None)
+        assert ((Z[x:y].double() - ref).abs() <= tol).all(), e
+
+
+def test_rows_past_32_bits(sg):
+    T, K = 70016, 32768          # 2.3e9 codes, quantised and multiplied
+    X = torch.zeros(T, K, dtype=BF, device=DEV)
+    at = [0, 1, 65534, 65535, 65536, 65537, T - 1]
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    for t in at:
+        X[t] = torch.randn(K, generator=gen, device=DEV)
+    q, s = sg.swiglu_quant_int8(X)
+    want, scale = quant_ref(X[at].cpu())
+    assert torch.equal(q[at].cpu(), want) and torch.equal(s[at].cpu(), scale)
+    assert int((q != 0).any(1).sum()) == len(at)
+    del X
+    W, w = torch.randint(-127, 128, (72, K), generator=gen, device=DEV).to(I8), torch.rand(72, generator=gen, device=DEV) * 1e-3
+    Z = sg.swiglu_linear_int8(q, s, W, w)
+    _status(sg)
+    ref, tol = product_ref(q[at], s[at], [(W[None], w[None])], [0, len(at)], None)
+    assert ((Z[at].double() - ref).abs() <= tol).all()
+    assert int((Z != 0).any(1).sum()) == len(at)
 
 
 # ---- the calls together -----------------------------------------------------------

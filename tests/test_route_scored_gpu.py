@@ -132,11 +132,10 @@ def test_ties_go_to_the_lowest(sg, score, best):
 
 
 @SCORES
-@pytest.mark.parametrize("T", [40, 700])
-def test_choices_closer_than_fp32_tells(sg, score, T):
+@pytest.mark.parametrize("T,E", [(40, 64), (700, 64), (30, 512)])
+def test_choices_closer_than_fp32_tells(sg, score, T, E):
     """Biases that make the scores of a token equal up to FP32's last bits, for every token."""
     g = _gen("close", score, T)
-    E = 64
     row = torch.randn(E, generator=g)
     s = torch.sigmoid(row.double()) if score == "sigmoid" else torch.softmax(row.double(), 0)
     b = (1.0 - s).float()  # every c is 1 within 2^-25: FP64 alone orders them
