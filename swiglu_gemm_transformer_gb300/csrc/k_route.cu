@@ -43,7 +43,7 @@
 // which is so for about a token in a thousand, FP64 settles the few values
 // concerned (without a bias the logits' own order decides, and only sums of two
 // scores are compared).  Bound by instructions: 16384 tokens, 256 experts in 8
-// groups, 39 us (55 with all scores of such a token in FP64 and a round over all
+// groups, 37 us (55 with all scores of such a token in FP64 and a round over all
 // experts for each choice; 8 lanes of 32 experts a token instead of a warp 70).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -204,17 +204,15 @@ __device__ __forceinline__ void warp_best(unsigned long long &key, int &e) {
   }
 }
 
-// The r-th largest (r < 32, from 0) of the warp's 32 keys: a bitonic sort.
-__device__ __forceinline__ uint32_t warp_rank(uint32_t key, int r, int lane) {
-#pragma unroll
-  for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-    for (int o = size / 2; o > 0; o >>= 1) {
-      const uint32_t other = __shfl_xor_sync(kAll, key, o);
-      const bool larger = ((lane & o) == 0) == ((lane & size) == 0 || size == 32);
-      key = larger ? max(key, other) : min(key, other);
-    }
-  return __shfl_sync(kAll, key, r);
+// The largest that is left of the warp's keys when the largest has been removed r
+// times, equal ones at once: at most the r-th largest (from 0).
+__device__ __forceinline__ uint32_t warp_rank(uint32_t key, int r) {
+  uint32_t top = __reduce_max_sync(kAll, key);
+  for (int i = 0; i < r; ++i) {
+    key = key == top ? 0u : key;
+    top = __reduce_max_sync(kAll, key);
+  }
+  return top;
 }
 
 __device__ __forceinline__ float score_of(bool sigmoid, float x, float m, float sum) {
@@ -320,7 +318,7 @@ __device__ __forceinline__ bool choose_by_ranks(const ScorePlan<EPL> &plan, cons
   uint32_t b = key[0];
 #pragma unroll
   for (int i = 1; i < EPL; ++i) b = max(b, key[i]);
-  uint32_t least = max(warp_rank(b, rounds - 1, lane), 1u);
+  uint32_t least = max(warp_rank(b, rounds - 1), 1u);
   if (margin > 0.0f && least > 1u && least != 0xffffffffu) {
     const float v = key_value(least);
     least = max(order_key(v - margin - 0x1p-22f * fabsf(v)), 1u);
@@ -769,22 +767,46 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
   int64_t i = b0 * p.k + threadIdx.x;
   int e_next = i < end ? __ldg(p.ids + i) : -1, s_next = i < end ? p.slots[i] : 0;
   __syncthreads();
-  // Thread (g, e) sums blocks g, g + G, ... of expert e (integer sums in
-  // shared memory: their order does not matter).
-  const int G = max(1, static_cast<int>(blockDim.x) / p.E);
-  for (int e0 = 0; e0 < p.E; e0 += blockDim.x) {
-    const int e = e0 + static_cast<int>(threadIdx.x) % p.E;  // E > blockDim.x: e0 + threadIdx.x
-    const int g = threadIdx.x / p.E;
-    if (e < p.E && g < G) {
-      int all = 0, before = 0;
+  // Thread (g, e) sums blocks g, g + G, ... of expert e, or of four from e on where
+  // the blocks' counts are whole pieces of 16 bytes (256 experts: 12.2 -> 9.3 us);
+  // integer sums in shared memory: their order does not matter.
+  if (p.E % 4 == 0 && (reinterpret_cast<uintptr_t>(p.counts) & 15u) == 0) {
+    const int quads = p.E / 4, G4 = static_cast<int>(blockDim.x) / quads, g = threadIdx.x / quads;
+    const int e = 4 * (static_cast<int>(threadIdx.x) % quads);
+    if (g < G4) {
+      int all[4] = {}, before[4] = {};
 #pragma unroll 8
-      for (int i = g; i < p.blocks; i += G) {
-        const int c = __ldg(p.counts + int64_t(i) * p.E + e);
-        all += c;
-        before += i < b ? c : 0;
+      for (int i = g; i < p.blocks; i += G4) {
+        const int4 c = __ldg(reinterpret_cast<const int4 *>(p.counts + int64_t(i) * p.E + e));
+        const int v[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          all[j] += v[j];
+          before[j] += i < b ? v[j] : 0;
+        }
       }
-      atomicAdd(&sm.base[e], all);
-      atomicAdd(&mine[e], before);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        atomicAdd(&sm.base[e + j], all[j]);
+        atomicAdd(&mine[e + j], before[j]);
+      }
+    }
+  } else {
+    const int G = max(1, static_cast<int>(blockDim.x) / p.E);
+    for (int e0 = 0; e0 < p.E; e0 += blockDim.x) {
+      const int e = e0 + static_cast<int>(threadIdx.x) % p.E;  // E > blockDim.x: e0 + threadIdx.x
+      const int g = threadIdx.x / p.E;
+      if (e < p.E && g < G) {
+        int all = 0, before = 0;
+#pragma unroll 8
+        for (int i = g; i < p.blocks; i += G) {
+          const int c = __ldg(p.counts + int64_t(i) * p.E + e);
+          all += c;
+          before += i < b ? c : 0;
+        }
+        atomicAdd(&sm.base[e], all);
+        atomicAdd(&mine[e], before);
+      }
     }
   }
   __syncthreads();
