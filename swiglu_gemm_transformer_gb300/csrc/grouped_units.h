@@ -61,14 +61,10 @@ SWIGLU_UNITS_FN int row_tiles(int cnt) {
 // mt - 1 may pass 2^31, so the quotient is rounded up from cnt - 1.)
 SWIGLU_UNITS_FN int tile_rows(int cnt, int mt) { return ((cnt - 1) / mt + 32) & ~31; }
 
-// Unit u >= 0 of the call, or {-1, ...} past the last one.  off[E + 1]: the
-// groups' bounds, not decreasing; tiles[E + 1]: row tiles before each group.
-// Within an expert, GROUP row tiles walk the column tiles together.
-template <int GROUP>
-SWIGLU_UNITS_FN GroupedUnit grouped_unit(int64_t u, const int *off, const int *tiles, int E,
-                                         int num_n_blk) {
-  GroupedUnit r = {-1, -1, 0, 0};
-  if (u >= int64_t(tiles[E]) * num_n_blk) return r;
+// Unit u of the call (below the last), counted in I.
+template <int GROUP, class I>
+SWIGLU_UNITS_FN GroupedUnit unit_at(I u, const int *off, const int *tiles, int E, int num_n_blk) {
+  GroupedUnit r;
   // the expert whose row tiles hold tile u / num_n_blk
   const int tt = static_cast<int>(u / num_n_blk);
   int lo = 0, hi = E;  // tiles[lo] <= tt < tiles[hi]
@@ -77,17 +73,34 @@ SWIGLU_UNITS_FN GroupedUnit grouped_unit(int64_t u, const int *off, const int *t
     if (tiles[mid] <= tt) lo = mid; else hi = mid;
   }
   const int mt = tiles[lo + 1] - tiles[lo];
-  const int64_t local = u - int64_t(tiles[lo]) * num_n_blk;
-  const int64_t per_group = int64_t(GROUP) * num_n_blk;
+  const I local = u - static_cast<I>(tiles[lo]) * num_n_blk;
+  const I per_group = static_cast<I>(GROUP) * num_n_blk;
   const int first = static_cast<int>(local / per_group) * GROUP;
   const int span = units_min(GROUP, mt - first);
-  const int64_t w = local % per_group;
+  const I w = local - per_group * (first / GROUP);
   const int rows = tile_rows(off[lo + 1] - off[lo], mt);
   r.e = lo;
   r.nb = static_cast<int>(w / span);
-  r.row0 = off[lo] + (first + static_cast<int>(w % span)) * rows;
+  r.row0 = off[lo] + (first + static_cast<int>(w - static_cast<I>(r.nb) * span)) * rows;
   r.end = units_min(r.row0 + rows, off[lo + 1]);
   return r;
+}
+
+// Unit u >= 0 of the call, or {-1, ...} past the last one.  off[E + 1]: the
+// groups' bounds, not decreasing; tiles[E + 1]: row tiles before each group.
+// Within an expert, GROUP row tiles walk the column tiles together.
+// (Counted in 32 bits where they suffice: the quotients in 64 took a few hundred
+// instructions before a call's first copy.)
+template <int GROUP>
+SWIGLU_UNITS_FN GroupedUnit grouped_unit(int64_t u, const int *off, const int *tiles, int E,
+                                         int num_n_blk) {
+  const GroupedUnit none = {-1, -1, 0, 0};
+  const int64_t total = int64_t(tiles[E]) * num_n_blk;
+  if (u >= total) return none;
+  // (the largest product below is GROUP * num_n_blk, or below the total)
+  if (total < (int64_t(1) << 31) && num_n_blk < (1 << 30) / GROUP)
+    return unit_at<GROUP, int>(static_cast<int>(u), off, tiles, E, num_n_blk);
+  return unit_at<GROUP, int64_t>(u, off, tiles, E, num_n_blk);
 }
 
 // The units of one of two warps that finish them together (they trade values

@@ -62,10 +62,12 @@ uint64_t widened_bytes(int64_t T, int64_t P, int64_t K) { return uint64_t(std::m
 constexpr int kWidenTurns = 4;
 
 __global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t *A, const int32_t *rows, __half *out,
-                                                         int64_t count, int32_t per_row, int32_t T) {
-  // (in this order: the product's kernel starts when nothing before this one runs)
+                                                         int64_t count, int32_t per_row, int32_t T, bool early) {
+  // In this order the product's kernel starts when nothing before this one runs;
+  // early: at once, and waits for this one's end itself.
+  if (early) ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
-  ptx::grid_launch_dependents();
+  if (!early) ptx::grid_launch_dependents();
   const int64_t first = int64_t(blockIdx.x) * (256 * kWidenTurns) + threadIdx.x;
   uint2 v[kWidenTurns];
 #pragma unroll
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t *A, const 
   }
 }
 
-cudaError_t launch_widen(const Int8Call &c, const int32_t *rows, int64_t n) {
+cudaError_t launch_widen(const Int8Call &c, const int32_t *rows, int64_t n, bool early) {
   const int64_t per_row = c.K / 8, count = n * per_row, blocks = ceil_div(count, 256 * kWidenTurns);
   if (blocks > kMaxDim) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -103,7 +105,7 @@ cudaError_t launch_widen(const Int8Call &c, const int32_t *rows, int64_t n) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, widen_rows_kernel, static_cast<const int8_t *>(c.A), rows,
-                            static_cast<__half *>(c.workspace), count, int32_t(per_row), int32_t(c.T));
+                            static_cast<__half *>(c.workspace), count, int32_t(per_row), int32_t(c.T), early);
 }
 
 // The kernel `kern` for `tiles` of rows and blocks of `cols` columns.
@@ -227,7 +229,8 @@ int run_tensor(const Int8Call &c, uint32_t *err, uint64_t timeout_ns, uint64_t c
   if (rc == SWIGLU_OK) rc = encode_u8_map(&t.w1, c.W1, 3, wdim, wstr, wbox);
   if (rc == SWIGLU_OK) rc = encode_u8_map(&t.w2, c.fused ? c.W2 : c.W1, 3, wdim, wstr, wbox);
   if (rc != SWIGLU_OK) return rc;
-  if (launch_widen(c, gather ? nullptr : c.rows, int64_t(R)) != cudaSuccess) return SWIGLU_ERR_CUDA;
+  if (launch_widen(c, gather ? nullptr : c.rows, int64_t(R), pairs > 1) != cudaSuccess)
+    return SWIGLU_ERR_CUDA;
   Int8Params &p = t.p;
   p.sa = c.sa;
   p.s1 = c.s1;

@@ -863,9 +863,13 @@ bool supported(int64_t T, int64_t E, int64_t k) {
 
 template <class How>
 cudaError_t launch_route(const RouteParams &p, cudaStream_t s) {
-  // warps: as many as there are groups of tokens and counters for
+  // warps: as many as there are groups of tokens, or experts for the scans of a few
+  // tokens, and counters for (one token, 256 experts by scores, in a graph: 8.7 us
+  // with a warp, 6.7 with 8)
   constexpr int SIDE = 32 / How::LANES;
-  auto warps = [&](int tokens) { return std::min({32, kCounters / p.E, (tokens + SIDE - 1) / SIDE}); };
+  auto warps = [&](int tokens) {
+    return std::min({32, kCounters / p.E, std::max((tokens + SIDE - 1) / SIDE, (p.E + 31) / 32)});
+  };
   if (p.T <= kOneTokens) {
     int blocks = 1;  // a power of two
     while (blocks * kOneBlockTokens < p.T) blocks *= 2;

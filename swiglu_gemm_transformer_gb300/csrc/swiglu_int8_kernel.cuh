@@ -204,7 +204,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   // The kernel before this one widens the rows; its blocks let this one start once
   // they have waited for all work before them.  So everything but the widened rows
   // may be read, and Y written, without a wait for it: weights stream meanwhile.
+  // SPLIT, it lets this one start at once, to set up beside the work before, which
+  // for a short call is worth more: every role waits for that work (after()) before
+  // its first bar, so that no clock runs meanwhile; the finder only for offsets.
   ptx::grid_launch_dependents();
+  auto after = [] {
+    if (C::SPLIT) ptx::grid_dependency_wait();
+  };
 
   auto wait = [&](uint32_t bar, uint32_t parity, uint32_t where) {
     return wait_bar(bar, parity, p.timeout_ns, abort_flag, p.err, where);
@@ -345,6 +351,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // ------------------------------------------------------------ epilogue
     uint32_t abuf = 0, aphase = 0;
     GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
+    after();
     bool ok = true, more = units.next(next, ok);
     if (more) {
       load_names();
@@ -384,6 +391,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     bool ok = true;
     GroupedUnits<false> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
     GroupedUnit un;
+    after();
     while (ok && units.next(un, ok)) {
       for (int kb = kb0; kb < kb1; ++kb, ++step) {
         const uint32_t buf = step % C::BUFS;
@@ -426,6 +434,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       bool ok = true;
       GroupedUnits<true> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
       GroupedUnit un;
+      after();
       while (ok && units.next(un, ok)) {
         const int col0 = (un.nb * 2 + static_cast<int>(rank)) * C::COLS;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -454,6 +463,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       bool ok = true;
       GroupedUnits<true> units(ring, unitf_bar, unite_bar, p.timeout_ns, p.err, abort_flag);
       GroupedUnit un;
+      after();
       while (ok && units.next(un, ok)) {
         const uint32_t idesc = ptx::idesc_f16(256, un.n());
         if (!(ok = wait(acce + 8u * abuf, aphase ^ 1u, WAIT_MMA_ACC_EMPTY))) break;
@@ -484,6 +494,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __syncwarp();
   } else if (warp == C::UNIT_WARP) {
     // ------------------------------------------------------------ unit finder
+    if (p.offsets) after();
     find_units<C::NT, C::GROUP>(ring, off, tiles, unitf_bar, unite_bar, p.offsets, p.P, p.E, p.num_n_blk,
                                 static_cast<int>(ptx::cluster_id_x()), static_cast<int>(ptx::num_clusters_x()),
                                 p.timeout_ns, p.err, abort_flag);
