@@ -22,17 +22,19 @@
 // match_any), the warps' counts are summed in order, and each warp walks its
 // entries again and numbers them within the block.
 //
-// Up to kOneTokens tokens are one launch of one cluster, 32 tokens a block: one
-// SM issues the choices of 128 tokens in about 6 us, so a few tokens are spread
-// over several; the blocks read each other's counts through distributed shared
-// memory (128 tokens: 5.4 us, in one block 9.1 us).  Beyond that a first kernel
+// Up to kOneTokens tokens are one launch of one cluster of at most eight blocks, 8
+// tokens a block or as many as it takes: one SM issues the choices of 128 tokens in
+// about 6 us, so a few tokens are spread over several; the blocks read each other's
+// counts through distributed shared memory, which costs 0.8 us.  In a graph, 256
+// experts: 64 tokens by logit 5.7 us, by scores 8.6 (32 tokens a block: 10.1 and
+// 13.4); 8 tokens 4.4 and 7.1 (one a block: 5.1 and 8.1).  Beyond that a first kernel
 // numbers the entries within each block of 32 to 128 tokens (in slots) and writes
 // the block's counts to the workspace, and a second one, overlapped by
 // programmatic dependent launch, sums the counts of the blocks before its own
 // and adds them (16384 tokens: 14.0 us; in clusters of eight blocks of 32
 // tokens about a fifth more).  Every block of the second launch reads the counts
 // of all blocks, which is little at such sizes but grows with the square of the
-// tokens: 131072 tokens take 100 us with 64 experts and 292 us with 256.
+// tokens: 131072 tokens take 90 us with 64 experts and 250 us with 256.
 //
 // swiglu_moe_route_scored chooses by a score instead of the logit (choose_scored):
 //     s = sigmoid(l) or softmax(l),  c = s + bias,
@@ -43,7 +45,7 @@
 // which is so for about a token in a thousand, FP64 settles the few values
 // concerned (without a bias the logits' own order decides, and only sums of two
 // scores are compared).  Bound by instructions: 16384 tokens, 256 experts in 8
-// groups, 37 us (55 with all scores of such a token in FP64 and a round over all
+// groups, 36 us (55 with all scores of such a token in FP64 and a round over all
 // experts for each choice; 8 lanes of 32 experts a token instead of a warp 70).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -63,7 +65,8 @@ namespace {
 constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
 constexpr int kOneTokens = 256;          // tokens of the one-launch form,
-constexpr int kOneBlockTokens = 32;      // per block of its cluster (at most eight)
+constexpr int kOneBlocks = 8;            // blocks of its cluster, at most
+constexpr int kOneLeast = 8;             // tokens of a block, a power of two, at least
 constexpr int kBlockTokens = 128;        // most tokens per block otherwise
 // Warps of a block x experts: 32 warps up to 510 experts, and RouteSmem is the 48 KB
 // that a kernel may hold without asking.
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(1024, 1) route_choose_kernel(const __grid_cons
   __shared__ RouteSmem sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int rank = blockIdx.x, ranks = ONE ? gridDim.x : 1;
-  const int tokens = ONE ? kOneBlockTokens : p.block_tokens;
+  const int tokens = p.block_tokens;
   uint16_t *cnt = sm.cnt + warp * p.E;
   ptx::grid_launch_dependents();
   for (int e = lane; e < p.E; e += 32) cnt[e] = 0;
@@ -871,10 +874,13 @@ cudaError_t launch_route(const RouteParams &p, cudaStream_t s) {
     return std::min({32, kCounters / p.E, std::max((tokens + SIDE - 1) / SIDE, (p.E + 31) / 32)});
   };
   if (p.T <= kOneTokens) {
-    int blocks = 1;  // a power of two
-    while (blocks * kOneBlockTokens < p.T) blocks *= 2;
-    return launch_pdl(route_choose_kernel<How, true>, blocks, blocks, 32 * warps(std::min(p.T, kOneBlockTokens)),
-                      p, s);
+    RouteParams one = p;
+    one.block_tokens = kOneLeast;
+    while (one.block_tokens * kOneBlocks < p.T) one.block_tokens *= 2;
+    one.blocks = 1;  // a power of two
+    while (one.blocks * one.block_tokens < p.T) one.blocks *= 2;
+    return launch_pdl(route_choose_kernel<How, true>, one.blocks, one.blocks,
+                      32 * warps(std::min(p.T, one.block_tokens)), one, s);
   }
   const cudaError_t e =
       launch_pdl(route_choose_kernel<How, false>, p.blocks, 1, 32 * warps(p.block_tokens), p, s);
