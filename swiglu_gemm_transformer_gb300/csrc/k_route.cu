@@ -89,15 +89,15 @@ struct RouteParams {
 
 // Unsigned number with the order of the floats; -inf -> 0 (masked), NaN above
 // +inf (it is chosen first and its weight comes out NaN, so it stays visible).
+constexpr uint32_t kInfKey = 0x007fffffu;  // -inf's in the plain order (a negative NaN, below it, wraps to the top)
 __device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));  // -0 becomes +0
-  const uint32_t k = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-  return x != x ? 0xffffffffu : k == 0x007fffffu ? 0u : k;
+  const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));  // -0 becomes +0, every NaN the same
+  return (b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u)) - kInfKey;
 }
 
 __device__ __forceinline__ float key_value(uint32_t key) {
-  const uint32_t b = key ^ ((key & 0x80000000u) ? 0x80000000u : 0xffffffffu);
-  return key == 0u ? -INFINITY : __uint_as_float(b);  // all ones -> a NaN
+  const uint32_t k = key + kInfKey;
+  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xffffffffu));
 }
 
 // The token t of this lane's group of LPT >= k lanes (or none: t >= end), its

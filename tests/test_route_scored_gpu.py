@@ -121,6 +121,15 @@ def test_choices(sg, shape, score, bias):
     check(sg, x.to(BF), k, b, score=score, groups=groups, kept=kept, best=best, renorm=bool(E & 4), scale=1.0)
 
 
+@pytest.mark.parametrize("T", [2, 7, 8, 9, 16, 17, 32, 33, 63, 64, 65, 129, 255, 256])
+def test_calls_of_one_launch(sg, T):
+    """Blocks of 8 to 32 tokens, full and ragged, some without a token."""
+    x = torch.randn(T, 300, generator=_gen("one", T))
+    x[T // 2] = -math.inf
+    b = torch.randn(300, generator=_gen("oneb")) * 0.1
+    check(sg, x, 5, b, groups=4, kept=2)
+
+
 @SCORES
 @pytest.mark.parametrize("best", [1, 2])
 def test_ties_go_to_the_lowest(sg, score, best):
