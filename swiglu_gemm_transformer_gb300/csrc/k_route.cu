@@ -45,7 +45,7 @@
 // which is so for about a token in a thousand, FP64 settles the few values
 // concerned (without a bias the logits' own order decides, and only sums of two
 // scores are compared).  Bound by instructions: 16384 tokens, 256 experts in 8
-// groups, 36 us (55 with all scores of such a token in FP64 and a round over all
+// groups, 35 us (55 with all scores of such a token in FP64 and a round over all
 // experts for each choice; 8 lanes of 32 experts a token instead of a warp 70).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -79,12 +79,13 @@ struct RouteParams {
   float *weights;
   int32_t *offsets, *rows, *slots;
   int32_t *counts;  // [blocks][E], two launches only
-  int32_t T, E, k, blocks, block_tokens;
+  int32_t T, E, k, blocks, block_tokens, warp_tokens;
   int32_t renormalize;
   float scale;
   // scored form only
   const float *bias;  // [E] or null
   int32_t sigmoid, fp32, groups, kept, best;
+  int32_t group_size, lane_bits;  // E / groups; 2^lane_bits = 32 / groups
 };
 
 // Unsigned number with the order of the floats; -inf -> 0 (masked), NaN above
@@ -250,23 +251,22 @@ __device__ __forceinline__ float score_error(bool sigmoid) { return sigmoid ? 0x
 
 // What a warp keeps from token to token: a lane's group is g = lane / L of L = 32 /
 // groups lanes, and its experts are first, first + L, ... below end = (g + 1) E /
-// groups; and 32 places of shared memory.
-struct Candidate {
-  uint32_t key;
-  int e;
+// groups; and shared memory for 32 candidates.
+struct Candidates {
+  uint32_t key[32];
+  int e[32];
 };
 template <int EPL>
 struct ScorePlan {
   static constexpr int KEPT = EPL <= 8 ? EPL : 1;  // biases in registers
   int lane, L, g, first, end;
   float bias[KEPT];
-  Candidate *found;
-  __device__ ScorePlan(const RouteParams &p, int lane_, Candidate *found_) : lane(lane_), found(found_) {
-    const int size = p.E / p.groups;
-    L = 32 / p.groups;
-    g = lane / L;
-    first = g * size + lane % L;
-    end = (g + 1) * size;
+  Candidates *found;
+  __device__ ScorePlan(const RouteParams &p, int lane_, Candidates *found_) : lane(lane_), found(found_) {
+    L = 1 << p.lane_bits;
+    g = lane >> p.lane_bits;
+    first = g * p.group_size + (lane & (L - 1));
+    end = (g + 1) * p.group_size;
     if (EPL <= 8) {
 #pragma unroll
       for (int i = 0; i < KEPT; ++i) bias[i] = p.bias && expert(i) < end ? __ldg(p.bias + expert(i)) : 0.0f;
@@ -338,25 +338,38 @@ __device__ __forceinline__ bool choose_by_ranks(const ScorePlan<EPL> &plan, cons
   const int count = __shfl_sync(kAll, at, 31);
   if (count > 32) return false;
   at -= mine;
+  Candidates &found = *plan.found;
+  found.key[lane] = 0u;
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < EPL; ++i)
-    if (key[i] >= least) plan.found[at++] = {key[i], plan.expert(i)};
+    if (key[i] >= least) {
+      found.key[at] = key[i];
+      found.e[at++] = plan.expert(i);
+    }
   __syncwarp();
-  const Candidate c = lane < count ? plan.found[lane] : Candidate{0u, 0x7fffffff};
+  const bool there = lane < count;
+  const uint32_t c = found.key[lane];
+  const int e = found.e[lane];
   int rank = 0;
-  for (int j = 0; j < count; ++j) {
-    const Candidate o = plan.found[j];
-    rank += o.key > c.key || (o.key == c.key && o.e < c.e);
+  for (int j = 0; j < count; j += 4) {
+    const uint4 o = *reinterpret_cast<const uint4 *>(found.key + j);
+    rank += (o.x > c) + (o.y > c) + (o.z > c) + (o.w > c);
+  }
+  // equal keys have one rank: the lowest expert is first
+  if (__popc(__reduce_or_sync(kAll, there ? 1u << rank : 0u)) != count)
+    for (int j = 0; j < count; ++j) rank += found.key[j] == c && found.e[j] < e;
+  __syncwarp();
+  if (there) {
+    found.key[rank] = c;
+    found.e[rank] = e;
   }
   __syncwarp();
-  if (lane < count) plan.found[rank] = c;
+  const bool more = k < min(count, rounds);
+  all = count, id_of_all = there ? found.e[lane] : -1;
+  my_key = there && lane < rounds ? found.key[lane] : 0u, my_id = lane < rounds ? id_of_all : -1;
+  next_key = more ? found.key[k] : 0u, next_id = more ? found.e[k] : -1;
   __syncwarp();
-  const Candidate none = {0u, -1};
-  const Candidate got = lane < count ? plan.found[lane] : none, next = k < min(count, rounds) ? plan.found[k] : none;
-  __syncwarp();
-  all = count, id_of_all = got.e;
-  my_key = lane < rounds ? got.key : 0u, my_id = lane < rounds ? got.e : -1;
-  next_key = next.key, next_id = next.e;
   return true;
 }
 // What FP32 leaves open is settled in FP64 for the values concerned alone, one a lane
@@ -418,7 +431,7 @@ __device__ __noinline__ bool keep_in_64(const RouteParams &p, const ScorePlan<EP
 }
 
 // The candidates (lane i < all has expert id) in order: lane j gets the j-th.
-__device__ __noinline__ int rank_in_64(const RouteParams &p, const Token &token, Candidate *found, int lane, int all,
+__device__ __noinline__ int rank_in_64(const RouteParams &p, const Token &token, Candidates &found, int lane, int all,
                                        int id) {
   const unsigned long long key = lane < all ? order_key(worth_in_64(p, token, id)) : 0ull;
   int rank = 0;
@@ -428,9 +441,9 @@ __device__ __noinline__ int rank_in_64(const RouteParams &p, const Token &token,
     rank += k > key || (k == key && e < id);
   }
   __syncwarp();
-  if (lane < all) found[rank].e = id;
+  if (lane < all) found.e[rank] = id;
   __syncwarp();
-  const int e = lane < all ? found[lane].e : -1;
+  const int e = lane < all ? found.e[lane] : -1;
   __syncwarp();
   return e;
 }
@@ -475,11 +488,16 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
   [[maybe_unused]] Token token = {row32, row16, double(m), 0.0};
   // s + b, or the logit where no bias is given; 0 for no expert
   Key key[EPL];
-  if (biased) {
+  auto keys_of = [&](bool sigmoid) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
       key[i] = x[i] == -INFINITY ? Key(0)
                                  : order_key(quick_score(sigmoid, V(x[i]), m, by_sum) + V(plan.bias_of(p, i)));
+  };
+  if (biased && sigmoid) {  // (two loops: a choice within one takes both sides' instructions)
+    keys_of(true);
+  } else if (biased) {
+    keys_of(false);
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = order_key(V(x[i]));
@@ -553,20 +571,25 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
   if (ROUNDED && biased) {
     // each choice against the next one; equal logits with equal biases are a
     // true tie, which the expert's number has settled
-    const float mb = my_id >= 0 ? __ldg(p.bias + my_id) : 0.0f;
-    const float nx = next_id >= 0 ? logit(next_id) : -INFINITY;
-    const float nb = next_id >= 0 ? __ldg(p.bias + next_id) : 0.0f;
     Key ok = __shfl_down_sync(kAll, my_key, 1);
-    float ox = __shfl_down_sync(kAll, mx, 1), ob = __shfl_down_sync(kAll, mb, 1);
-    if (lane == p.k - 1) ok = next_key, ox = nx, ob = nb;
-    if (lane < p.k && my_key != 0 && ok != 0 && !(ox == mx && ob == mb)) {
+    if (lane == p.k - 1) ok = next_key;
+    bool open = false;
+    if (lane < p.k && my_key != 0 && ok != 0) {
       const float a = float(key_value(my_key)), b = float(key_value(ok));
-      if (a - b <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(a), fabsf(b))) sure = false;
+      open = a - b <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(a), fabsf(b));
+    }
+    if (__any_sync(kAll, open)) {
+      const float mb = my_id >= 0 ? __ldg(p.bias + my_id) : 0.0f;
+      const float nx = next_id >= 0 ? logit(next_id) : -INFINITY;
+      const float nb = next_id >= 0 ? __ldg(p.bias + next_id) : 0.0f;
+      float ox = __shfl_down_sync(kAll, mx, 1), ob = __shfl_down_sync(kAll, mb, 1);
+      if (lane == p.k - 1) ox = nx, ob = nb;
+      sure = !(open && !(ox == mx && ob == mb));
     }
     if constexpr (ROUNDED) {
       if (ranked && !__all_sync(kAll, sure)) {
         if (!sigmoid && token.sum == 0.0) sum_in_64(p, plan, token);
-        my_id = rank_in_64(p, token, plan.found, lane, all, id_of_all);
+        my_id = rank_in_64(p, token, *plan.found, lane, all, id_of_all);
         if (lane >= p.k) my_id = -1;
         mx = my_id >= 0 ? logit(my_id) : -INFINITY;
         sure = true;
@@ -606,7 +629,7 @@ struct ByScore {
   static constexpr int LANES = 32;
   ScorePlan<EPL> plan;
   __device__ ByScore(const RouteParams &p, int lane, void *spare)
-      : plan(p, lane, static_cast<Candidate *>(spare) + (threadIdx.x >> 5) * 32) {}
+      : plan(p, lane, static_cast<Candidates *>(spare) + (threadIdx.x >> 5)) {}
   __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane, uint16_t *ids16) {
     if (t >= end) return;
     int id;
@@ -640,7 +663,7 @@ __device__ __forceinline__ void walk(const uint16_t *ids16, int i0, int i1, uint
 
 struct RouteSmem {
   uint16_t cnt[kCounters];  // [warp][E]
-  alignas(8) int32_t base[kMaxE];      // first place of each expert's entries
+  alignas(16) int32_t base[kMaxE];     // first place of each expert's entries
   int32_t total[kMaxE];     // entries of this block (read by the cluster's other blocks), or of the blocks before
   uint16_t ids[kBlockTokens * kMaxK];
   int32_t carry[32];
@@ -698,10 +721,9 @@ __global__ void __launch_bounds__(1024, 1) route_choose_kernel(const __grid_cons
   const int nt = static_cast<int>(max(int64_t(0), min(int64_t(tokens), p.T - b0)));
   // each warp takes a run of tokens, 32 / LPT at a time
   constexpr int SIDE = 32 / How::LANES;
-  const int per = (nt + warps * SIDE - 1) / (warps * SIDE) * SIDE;
-  const int t0 = min(warp * per, nt), t1 = min(t0 + per, nt);
+  const int t0 = min(warp * p.warp_tokens, nt), t1 = min(t0 + p.warp_tokens, nt);
   // (base and total, 256 bytes a warp, are not in use yet)
-  static_assert(sizeof(sm.base) + sizeof(sm.total) == 32 * 32 * sizeof(Candidate), "32 candidates a warp");
+  static_assert(sizeof(sm.base) + sizeof(sm.total) == 32 * sizeof(Candidates), "32 candidates a warp");
   How how(p, lane, sm.base);
   for (int t = t0; t < t1; t += SIDE)
     how.choose(p, b0 + t + lane / How::LANES, b0 + t1, lane, sm.ids + (t + lane / How::LANES) * p.k);
@@ -873,17 +895,23 @@ cudaError_t launch_route(const RouteParams &p, cudaStream_t s) {
   auto warps = [&](int tokens) {
     return std::min({32, kCounters / p.E, std::max((tokens + SIDE - 1) / SIDE, (p.E + 31) / 32)});
   };
+  // a warp's run of tokens
+  auto shared_out = [&](RouteParams q, int tokens) {
+    q.warp_tokens = (tokens + warps(tokens) * SIDE - 1) / (warps(tokens) * SIDE) * SIDE;
+    return q;
+  };
   if (p.T <= kOneTokens) {
     RouteParams one = p;
     one.block_tokens = kOneLeast;
     while (one.block_tokens * kOneBlocks < p.T) one.block_tokens *= 2;
     one.blocks = 1;  // a power of two
     while (one.blocks * one.block_tokens < p.T) one.blocks *= 2;
-    return launch_pdl(route_choose_kernel<How, true>, one.blocks, one.blocks,
-                      32 * warps(std::min(p.T, one.block_tokens)), one, s);
+    const int tokens = std::min(p.T, one.block_tokens);
+    return launch_pdl(route_choose_kernel<How, true>, one.blocks, one.blocks, 32 * warps(tokens),
+                      shared_out(one, tokens), s);
   }
-  const cudaError_t e =
-      launch_pdl(route_choose_kernel<How, false>, p.blocks, 1, 32 * warps(p.block_tokens), p, s);
+  const cudaError_t e = launch_pdl(route_choose_kernel<How, false>, p.blocks, 1, 32 * warps(p.block_tokens),
+                                   shared_out(p, p.block_tokens), s);
   return e != cudaSuccess ? e : launch_pdl(route_place_kernel, p.blocks, 1, 1024, p, s);
 }
 
@@ -1000,6 +1028,8 @@ extern "C" int swiglu_moe_route_scored(const void *logits, int32_t logits_fp32, 
   p.fp32 = logits_fp32;
   // experts of a lane: a group's lie in 32 / groups lanes
   const int64_t lanes = 32 / groups, per_lane = (E / groups + lanes - 1) / lanes;
+  p.group_size = static_cast<int32_t>(E / groups);
+  while ((1 << p.lane_bits) < lanes) ++p.lane_bits;
   return run_route(p, logits_fp32 != 0, T, E, k, workspace, workspace_bytes, stream, [=](const RouteParams &q, cudaStream_t s) {
     return per_lane <= 2    ? launch_route<ByScore<2>>(q, s)
            : per_lane <= 8  ? launch_route<ByScore<8>>(q, s)
