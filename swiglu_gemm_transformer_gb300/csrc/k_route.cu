@@ -34,7 +34,7 @@
 // and adds them (16384 tokens: 14.0 us; in clusters of eight blocks of 32
 // tokens about a fifth more).  Every block of the second launch reads the counts
 // of all blocks, which is little at such sizes but grows with the square of the
-// tokens: 131072 tokens take 90 us with 64 experts and 250 us with 256.
+// tokens: 131072 tokens take 89 us with 64 experts and 243 us with 256.
 //
 // swiglu_moe_route_scored chooses by a score instead of the logit (choose_scored):
 //     s = sigmoid(l) or softmax(l),  c = s + bias,
@@ -45,7 +45,7 @@
 // which is so for about a token in a thousand, FP64 settles the few values
 // concerned (without a bias the logits' own order decides, and only sums of two
 // scores are compared).  Bound by instructions: 16384 tokens, 256 experts in 8
-// groups, 35 us (55 with all scores of such a token in FP64 and a round over all
+// groups, 34 us (55 with all scores of such a token in FP64 and a round over all
 // experts for each choice; 8 lanes of 32 experts a token instead of a warp 70).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
