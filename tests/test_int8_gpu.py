@@ -591,6 +591,35 @@ def test_outputs_and_workspaces_belong_to_the_stream_of_the_call(sg, stream):
         assert torch.equal(w, a.cpu()) and torch.equal(w, b.cpu())
 
 
+@pytest.mark.parametrize("M", [1, 8, 33, 125, 700])
+def test_calls_wait_for_the_makers_of_all_their_operands(sg, M):
+    """Codes and scales of rows and weights made anew, in the same buffers, right before each
+    product; a large product in front keeps the GPU busy while all are launched."""
+    K, N, turns = 4864, 896, 6
+    g = _gen("chain", M)
+    Xs = [torch.randn(M, K, generator=g).to(BF).to(DEV) for _ in range(turns)]
+    Ws = [torch.randn(N, K, generator=g).to(BF).to(DEV) for _ in range(turns)]
+    big, bs = sg.swiglu_quant_int8(torch.randn(4096, K, generator=g).to(BF).to(DEV))
+    A, sa = sg.swiglu_quant_int8(Xs[0])
+    W, sw = sg.swiglu_quant_int8(Ws[0])
+    want = []
+    for X, V in zip(Xs, Ws):
+        one = (*sg.swiglu_quant_int8(X), *sg.swiglu_quant_int8(V))
+        torch.cuda.synchronize()
+        want.append(sg.swiglu_linear_int8(*one))
+        torch.cuda.synchronize()
+    Y = torch.zeros(M, N, dtype=BF, device=DEV)
+    got = []
+    sg.swiglu_linear_int8(big, bs, big, bs)
+    for X, V in zip(Xs, Ws):
+        sg.swiglu_quant_int8(X, A, sa)
+        sg.swiglu_quant_int8(V, W, sw)
+        got.append(sg.swiglu_linear_int8(A, sa, W, sw, Y).clone())
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_given_workspaces_and_their_refusals(sg):
     gen = _gen("workspace")
     q = lambda *s: torch.randint(-127, 128, s, generator=gen).to(I8).to(DEV)  # noqa: E731
