@@ -322,9 +322,10 @@ __device__ __forceinline__ bool choose_by_ranks(const ScorePlan<EPL> &plan, cons
 #pragma unroll
   for (int i = 1; i < EPL; ++i) b = max(b, key[i]);
   uint32_t least = max(warp_rank(b, rounds - 1), 1u);
-  if (margin > 0.0f && least > 1u && least != 0xffffffffu) {
+  if (margin > 0.0f && least > 1u) {
     const float v = key_value(least);
-    least = max(order_key(v - margin - 0x1p-22f * fabsf(v)), 1u);
+    if (v < INFINITY)  // (nothing is within a margin of +inf or NaN but its like)
+      least = max(order_key(v - margin - 0x1p-22f * fabsf(v)), 1u);
   }
   int mine = 0;
 #pragma unroll
@@ -543,10 +544,11 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
         if (high >= low) {  // (of the whole warp)
           if (!sigmoid && token.sum == 0.0) sum_in_64(p, plan, token);
           // experts within two errors of the group's last that counts; without a bias
-          // the keys are logits, in whose order nothing is open
+          // the keys are logits, in whose order nothing is open, nor is it below a
+          // last that is +inf or NaN
           const Key last = summed && k2 != 0 ? k2 : k1;
           const float v = key_value(last);
-          const Key least = biased ? order_key(v - 2.0f * err - 0x1p-22f * fabsf(v)) : last;
+          const Key least = biased && v < INFINITY ? order_key(v - 2.0f * err - 0x1p-22f * fabsf(v)) : last;
           unsigned close = 0;
 #pragma unroll
           for (int i = 0; i < EPL; ++i) close |= key[i] != 0 && key[i] >= least ? 1u << i : 0u;

@@ -257,3 +257,32 @@ def test_binding_refusals(sg):
         sg.swiglu_moe_route_scored(x, 0)
     with pytest.raises(ValueError):
         sg.swiglu_moe_route_scored(x.t(), 2)
+
+
+@SCORES
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("pin", [math.inf, math.nan], ids=["inf", "nan"])
+@pytest.mark.parametrize("T,E", [(40, 32), (300, 64), (20, 512)])
+def test_a_pinned_expert_keeps_its_group_where_other_groups_are_close(sg, score, best, pin, T, E):
+    """Experts of a bias of +inf, one to three of them, beside groups whose values FP64 alone tells apart."""
+    row = torch.randn(E, generator=_gen("pinned", E))
+    s = torch.sigmoid(row.double()) if score == "sigmoid" else torch.softmax(row.double(), 0)
+    x = row.repeat(T, 1)
+    x[1::4] = torch.randn(len(x[1::4]), E, generator=_gen("pinned rows", E))
+    size = E // 8
+    for pinned in ((5 * size + 1,), (5 * size, 5 * size + 1), (2 * size, 5 * size + 2, 7 * size + 1)):
+        b = (1.0 - s).float()
+        b[list(pinned)] = pin
+        r = check(sg, x, 4, b, score=score, groups=8, kept=3, best=best)
+        assert (r.ids.cpu()[:, : len(pinned)] == torch.tensor(pinned)).all()
+
+
+@pytest.mark.parametrize("bias", [math.inf, math.nan], ids=["inf", "nan"])
+def test_more_pinned_experts_than_choices(sg, bias):
+    """Equal infinities are ties: the lowest experts."""
+    x = torch.randn(70, 64, generator=_gen("many pinned"))
+    b = torch.randn(64, generator=_gen("many pinned b")) * 0.1
+    b[3::5] = bias
+    for groups, kept, best in ((1, 1, 2), (8, 3, 1), (8, 3, 2)):
+        check(sg, x, 6, b, groups=groups, kept=kept, best=best)
+    check(sg, x, 6, torch.full((64,), bias), groups=8, kept=3)
