@@ -67,7 +67,7 @@ __device__ __forceinline__ static void find_units(GroupedUnit *ring, int *off, i
         if (slot == 0) {
 #pragma unroll
           for (int i = 0; i < AHEAD; ++i)
-            raw[i] = e + 32 * i <= E ? (offsets ? __ldg(offsets + e + 32 * i) : e == 0 ? 0 : P) : 0;
+            raw[i] = e + 32 * i <= E ? (offsets ? ptx::load(offsets + e + 32 * i) : e == 0 ? 0 : P) : 0;
         }
         int v = raw[0];
 #pragma unroll

@@ -77,9 +77,9 @@ __global__ void __launch_bounds__(256) widen_rows_kernel(const int8_t *A, const 
     int64_t from = i;
     if (rows) {
       const int64_t r = i / per_row;
-      from = int64_t(min(max(__ldg(rows + r), 0), T - 1)) * per_row + (i - r * per_row);
+      from = int64_t(min(max(ptx::load(rows + r), 0), T - 1)) * per_row + (i - r * per_row);
     }
-    v[j] = __ldg(reinterpret_cast<const uint2 *>(A) + from);
+    v[j] = ptx::load(reinterpret_cast<const uint2 *>(A) + from);
   }
 #pragma unroll
   for (int j = 0; j < kWidenTurns; ++j) {

@@ -71,17 +71,17 @@ cudaError_t launch_linear_sk(int cs, int bn, const LaunchArgs &la) {
 // slices' loads unrolled so they are in flight together.  Launched as a
 // programmatic dependent of the linear kernel: its blocks are resident while
 // that kernel ends and read the partial sums only after it has completed.
-__global__ void __launch_bounds__(256) splitk_reduce_kernel(const float4 *__restrict__ ws,
+__global__ void __launch_bounds__(256) splitk_reduce_kernel(const float4 *ws,
                                                             int splits, int64_t slice_vec4,
-                                                            const uint2 *__restrict__ R,
-                                                            uint2 *__restrict__ Z, int64_t n_vec4) {
+                                                            const uint2 *R,
+                                                            uint2 *Z, int64_t n_vec4) {
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n_vec4;
        i += (int64_t)gridDim.x * blockDim.x) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (R != nullptr) {
-      const uint2 r = __ldg(R + i);
+      const uint2 r = ptx::load(R + i);
       const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&r.x));
       const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&r.y));
       acc = make_float4(lo.x, lo.y, hi.x, hi.y);
@@ -90,14 +90,14 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const float4 *__rest
     for (; s + 4 <= splits; s += 4) {
       float4 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __ldg(ws + (s + j) * slice_vec4 + i);
+      for (int j = 0; j < 4; ++j) v[j] = ptx::load(ws + (s + j) * slice_vec4 + i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         acc.x += v[j].x; acc.y += v[j].y; acc.z += v[j].z; acc.w += v[j].w;
       }
     }
     for (; s < splits; ++s) {
-      const float4 v = __ldg(ws + s * slice_vec4 + i);
+      const float4 v = ptx::load(ws + s * slice_vec4 + i);
       acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
     }
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);

@@ -48,7 +48,7 @@ template <>
 struct Eight<false> {
   uint32_t w[4];
   __device__ __forceinline__ void load(const void *X, int64_t at) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(X) + at));
+    const uint4 a = ptx::load(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(X) + at));
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
   }
   __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
@@ -76,7 +76,7 @@ struct Eight<true> {
   float v[8];
   __device__ __forceinline__ void load(const void *X, int64_t at) {
     const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(X) + at);
-    const float4 a = __ldg(s), b = __ldg(s + 1);
+    const float4 a = ptx::load(s), b = ptx::load(s + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
   __device__ __forceinline__ void clear() {

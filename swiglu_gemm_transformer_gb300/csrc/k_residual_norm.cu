@@ -88,7 +88,7 @@ __device__ __forceinline__ float inv_root(float sum, float inv_d, float eps) {
 }
 
 template <int THREADS, int VPT, bool R32>
-__global__ void __launch_bounds__(THREADS) residual_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) residual_norm_kernel(const NormParams p) {
   __shared__ float red[2][32];
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
@@ -97,6 +97,14 @@ __global__ void __launch_bounds__(THREADS) residual_norm_kernel(const NormParams
   float z[VPT][8];
   uint4 rb[VPT], gb[VPT];
   float4 rf[R32 ? VPT : 1][2];
+  // The norms' weights: loaded at once where registers suffice, else a vector ahead of
+  // its use (loads do not pass the stores before them).
+  constexpr bool EARLY = VPT == 1;
+  uint4 gpost[VPT], gpre[VPT];
+  auto load_gamma = [&](uint4 (&g)[VPT], const __nv_bfloat16 *gamma, int i) {
+    const int v = threadIdx.x + i * THREADS;
+    if (i < VPT && gamma && v < nv) g[i] = ptx::load(reinterpret_cast<const uint4 *>(gamma) + v);
+  };
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * THREADS;
@@ -110,14 +118,16 @@ __global__ void __launch_bounds__(THREADS) residual_norm_kernel(const NormParams
     } else {
       rb[i] = static_cast<const uint4 *>(p.R)[t * nv + v];
     }
-    if (p.gate) gb[i] = __ldg(reinterpret_cast<const uint4 *>(p.gate + t * p.gate_stride) + v);
+    if (p.gate) gb[i] = ptx::load(reinterpret_cast<const uint4 *>(p.gate + t * p.gate_stride) + v);
+    if (EARLY) load_gamma(gpost, p.gamma_post, i);
+    if (EARLY) load_gamma(gpre, p.gamma_pre, i);
   }
   const uint4 *Z = reinterpret_cast<const uint4 *>(p.Z);
   if (p.slots == nullptr) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * THREADS;
-      if (v < nv) bf16x8(__ldg(Z + t * nv + v), z[i]);
+      if (v < nv) bf16x8(ptx::load(Z + t * nv + v), z[i]);
     }
   } else {
     // CH choices at a time, all their loads issued before the first use; a
@@ -128,9 +138,13 @@ __global__ void __launch_bounds__(THREADS) residual_norm_kernel(const NormParams
       float w[CH];
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        slot[j] = j0 + j < p.k ? __ldg(p.slots + t * p.k + j0 + j) : -1;
+        slot[j] = j0 + j < p.k ? ptx::load(p.slots + t * p.k + j0 + j) : -1;
+        w[j] = j0 + j < p.k ? ptx::load(p.weights + t * p.k + j0 + j) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
         if (slot[j] >= p.P) slot[j] = -1;
-        w[j] = slot[j] >= 0 ? __ldg(p.weights + t * p.k + j0 + j) : 0.0f;
+        if (slot[j] < 0) w[j] = 0.0f;
       }
       uint4 x[CH][VPT];
 #pragma unroll
@@ -138,7 +152,7 @@ __global__ void __launch_bounds__(THREADS) residual_norm_kernel(const NormParams
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
           const int v = threadIdx.x + i * THREADS;
-          x[j][i] = slot[j] >= 0 && v < nv ? __ldg(Z + int64_t(slot[j]) * nv + v)
+          x[j][i] = slot[j] >= 0 && v < nv ? ptx::load(Z + int64_t(slot[j]) * nv + v)
                                            : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
@@ -163,15 +177,17 @@ __global__ void __launch_bounds__(THREADS) residual_norm_kernel(const NormParams
     scale = inv_root(block_sum<THREADS>(ss, red[0]), inv_d, p.eps);
   }
   float ss = 0.0f;
+  if (!EARLY) load_gamma(gpost, p.gamma_post, 0);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * THREADS;
     if (v >= nv) continue;
+    if (!EARLY) load_gamma(gpost, p.gamma_post, i + 1);
     float f[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) z[i][c] *= scale;
     if (p.gamma_post) {
-      bf16x8(__ldg(reinterpret_cast<const uint4 *>(p.gamma_post) + v), f);
+      bf16x8(gpost[i], f);
 #pragma unroll
       for (int c = 0; c < 8; ++c) z[i][c] *= f[c];
     }
@@ -202,14 +218,16 @@ __global__ void __launch_bounds__(THREADS) residual_norm_kernel(const NormParams
     }
   }
   if (p.H == nullptr) return;
+  if (!EARLY) load_gamma(gpre, p.gamma_pre, 0);
   scale = inv_root(block_sum<THREADS>(ss, red[1]), inv_d, p.eps);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * THREADS;
     if (v >= nv) continue;
+    if (!EARLY) load_gamma(gpre, p.gamma_pre, i + 1);
     float f[8];
     if (p.gamma_pre) {
-      bf16x8(__ldg(reinterpret_cast<const uint4 *>(p.gamma_pre) + v), f);
+      bf16x8(gpre[i], f);
 #pragma unroll
       for (int c = 0; c < 8; ++c) f[c] *= z[i][c] * scale;
     } else {
@@ -295,9 +313,9 @@ __global__ void __launch_bounds__(THREADS + 32, ring_most_blocks(THREADS, VPT))
       slot = -1;
       w = 0.0f;
       if (t >= p.T || lane >= kr) return;
-      slot = p.slots ? __ldg(p.slots + t * p.k + lane) : static_cast<int>(t);
+      slot = p.slots ? ptx::load(p.slots + t * p.k + lane) : static_cast<int>(t);
       if (slot < 0 || slot >= p.P) slot = -1;
-      if (p.slots && slot >= 0) w = __ldg(p.weights + t * p.k + lane);
+      if (p.slots && slot >= 0) w = ptx::load(p.weights + t * p.k + lane);
     };
     int slot;
     float w;
@@ -356,15 +374,15 @@ __global__ void __launch_bounds__(THREADS + 32, ring_most_blocks(THREADS, VPT))
   // The norms' weights and a gate of one row stay in registers where these
   // suffice; longer rows read them again (from L1 or L2) for every row.
   constexpr bool HOLD = VPT <= 2;
-  uint4 gpost[VPT], gpre[VPT], gvec[VPT];
+  uint4 gpost[VPT], gpre[VPT], gb[VPT];  // gb: the gate, of one row or of the row at hand
   const bool gate_vec = p.gate && !l.g_bytes;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = threadIdx.x + i * THREADS;
     if (!HOLD || v >= nv) continue;
-    if (p.gamma_post) gpost[i] = __ldg(reinterpret_cast<const uint4 *>(p.gamma_post) + v);
-    if (p.gamma_pre) gpre[i] = __ldg(reinterpret_cast<const uint4 *>(p.gamma_pre) + v);
-    if (gate_vec) gvec[i] = __ldg(reinterpret_cast<const uint4 *>(p.gate) + v);
+    if (p.gamma_post) gpost[i] = ptx::load(reinterpret_cast<const uint4 *>(p.gamma_post) + v);
+    if (p.gamma_pre) gpre[i] = ptx::load(reinterpret_cast<const uint4 *>(p.gamma_pre) + v);
+    if (gate_vec) gb[i] = ptx::load(reinterpret_cast<const uint4 *>(p.gate) + v);
   }
   const float inv_d = 1.0f / p.D;
   int parity = 0;
@@ -378,7 +396,6 @@ __global__ void __launch_bounds__(THREADS + 32, ring_most_blocks(THREADS, VPT))
     float z[VPT][8], f[8];
     float ss = 0.0f;
     float r[VPT][8];
-    uint4 gb[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * THREADS;
@@ -417,12 +434,12 @@ __global__ void __launch_bounds__(THREADS + 32, ring_most_blocks(THREADS, VPT))
 #pragma unroll
       for (int c = 0; c < 8; ++c) z[i][c] *= scale;
       if (p.gamma_post) {
-        bf16x8(HOLD ? gpost[i] : __ldg(reinterpret_cast<const uint4 *>(p.gamma_post) + v), f);
+        bf16x8(HOLD ? gpost[i] : ptx::load(reinterpret_cast<const uint4 *>(p.gamma_post) + v), f);
 #pragma unroll
         for (int c = 0; c < 8; ++c) z[i][c] *= f[c];
       }
       if (p.gate) {
-        bf16x8(!gate_vec ? gb[i] : HOLD ? gvec[i] : __ldg(reinterpret_cast<const uint4 *>(p.gate) + v), f);
+        bf16x8(HOLD || !gate_vec ? gb[i] : ptx::load(reinterpret_cast<const uint4 *>(p.gate) + v), f);
 #pragma unroll
         for (int c = 0; c < 8; ++c) z[i][c] *= f[c];
       }
@@ -450,7 +467,7 @@ __global__ void __launch_bounds__(THREADS + 32, ring_most_blocks(THREADS, VPT))
       const int v = threadIdx.x + i * THREADS;
       if (v >= nv) continue;
       if (p.gamma_pre) {
-        bf16x8(HOLD ? gpre[i] : __ldg(reinterpret_cast<const uint4 *>(p.gamma_pre) + v), f);
+        bf16x8(HOLD ? gpre[i] : ptx::load(reinterpret_cast<const uint4 *>(p.gamma_pre) + v), f);
 #pragma unroll
         for (int c = 0; c < 8; ++c) f[c] *= z[i][c] * scale;
       } else {

@@ -118,7 +118,7 @@ __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t 
     x[i] = -INFINITY;
     if (live && e < p.E) {
       const int64_t at = t * p.E + e;
-      x[i] = FP32 ? __ldg(static_cast<const float *>(p.logits) + at)
+      x[i] = FP32 ? ptx::load(static_cast<const float *>(p.logits) + at)
                   : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[at]);
     }
   }
@@ -269,12 +269,12 @@ struct ScorePlan {
     end = (g + 1) * p.group_size;
     if (EPL <= 8) {
 #pragma unroll
-      for (int i = 0; i < KEPT; ++i) bias[i] = p.bias && expert(i) < end ? __ldg(p.bias + expert(i)) : 0.0f;
+      for (int i = 0; i < KEPT; ++i) bias[i] = p.bias && expert(i) < end ? ptx::load(p.bias + expert(i)) : 0.0f;
     }
   }
   __device__ int expert(int i) const { return first + L * i; }
   __device__ float bias_of(const RouteParams &p, int i) const {
-    return EPL <= 8 ? bias[EPL <= 8 ? i : 0] : expert(i) < end ? __ldg(p.bias + expert(i)) : 0.0f;
+    return EPL <= 8 ? bias[EPL <= 8 ? i : 0] : expert(i) < end ? ptx::load(p.bias + expert(i)) : 0.0f;
   }
 };
 
@@ -381,13 +381,13 @@ struct Token {  // where its logits are, and what its scores need
   const float *row32;
   const __nv_bfloat16 *row16;
   double m, sum;  // softmax
-  __device__ float logit(bool fp32, int e) const { return fp32 ? __ldg(row32 + e) : __bfloat162float(row16[e]); }
+  __device__ float logit(bool fp32, int e) const { return fp32 ? ptx::load(row32 + e) : __bfloat162float(row16[e]); }
 };
 
 // Expert e's score, with its bias.
 __device__ __forceinline__ double worth_in_64(const RouteParams &p, const Token &token, int e) {
   const double s = score_of(p.sigmoid != 0, double(token.logit(p.fp32 != 0, e)), token.m, token.sum);
-  return p.bias ? s + double(__ldg(p.bias + e)) : s;
+  return p.bias ? s + double(ptx::load(p.bias + e)) : s;
 }
 
 template <int EPL>
@@ -460,11 +460,11 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
   const int lane = plan.lane, L = plan.L, g = plan.g;
   const float *row32 = static_cast<const float *>(p.logits) + (fp32 ? t * p.E : 0);
   const __nv_bfloat16 *row16 = static_cast<const __nv_bfloat16 *>(p.logits) + (fp32 ? 0 : t * p.E);
-  auto logit = [&](int e) { return fp32 ? __ldg(row32 + e) : __bfloat162float(row16[e]); };
+  auto logit = [&](int e) { return fp32 ? ptx::load(row32 + e) : __bfloat162float(row16[e]); };
   float x[EPL];
   if (fp32) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = plan.expert(i) < plan.end ? __ldg(row32 + plan.expert(i)) : -INFINITY;
+    for (int i = 0; i < EPL; ++i) x[i] = plan.expert(i) < plan.end ? ptx::load(row32 + plan.expert(i)) : -INFINITY;
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
@@ -581,9 +581,9 @@ __device__ __forceinline__ bool choose_exactly(const RouteParams &p, const Score
       open = a - b <= 2.0f * err + 0x1p-22f * fmaxf(fabsf(a), fabsf(b));
     }
     if (__any_sync(kAll, open)) {
-      const float mb = my_id >= 0 ? __ldg(p.bias + my_id) : 0.0f;
+      const float mb = my_id >= 0 ? ptx::load(p.bias + my_id) : 0.0f;
       const float nx = next_id >= 0 ? logit(next_id) : -INFINITY;
-      const float nb = next_id >= 0 ? __ldg(p.bias + next_id) : 0.0f;
+      const float nb = next_id >= 0 ? ptx::load(p.bias + next_id) : 0.0f;
       float ox = __shfl_down_sync(kAll, mx, 1), ob = __shfl_down_sync(kAll, mb, 1);
       if (lane == p.k - 1) ox = nx, ob = nb;
       sure = !(open && !(ox == mx && ob == mb));
@@ -619,16 +619,19 @@ __device__ __noinline__ void choose_in_64(const RouteParams &p, const ScorePlan<
 // How a block chooses: by the logits, LPT lanes per token,
 template <int LPT, int EPL, bool FP32>
 struct ByLogit {
-  static constexpr int LANES = LPT;
+  static constexpr int LANES = LPT, WARPS = 32;  // of a token; most of a block
   __device__ ByLogit(const RouteParams &, int, void *) {}
   __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane, uint16_t *ids16) {
     swiglu::choose<LPT, EPL, FP32>(p, t, end, lane, ids16);
   }
 };
-// or by scores, a warp per token.
+// or by scores, a warp per token.  With 32 experts a lane 64 registers (32 warps) do
+// not hold the lane's keys: 16 warps (32 warps in brackets) take for sigmoid with a bias
+// 3000 x 1024 40.7 us (55.2), 16384 x 1024 101 (157), 16384 x 768 80.6 (81.8),
+// 16384 x 576 70.2 (61.8), 65536 x 1024 407 (405).
 template <int EPL>
 struct ByScore {
-  static constexpr int LANES = 32;
+  static constexpr int LANES = 32, WARPS = EPL > 16 ? 16 : 32;
   ScorePlan<EPL> plan;
   __device__ ByScore(const RouteParams &p, int lane, void *spare)
       : plan(p, lane, static_cast<Candidates *>(spare) + (threadIdx.x >> 5)) {}
@@ -710,7 +713,7 @@ __device__ __forceinline__ int scan_experts(RouteSmem &sm, int E, int32_t *offse
 // One block of tokens; ONE: a block of the only cluster, which does the whole
 // call, otherwise the first pass of it.
 template <class How, bool ONE>
-__global__ void __launch_bounds__(1024, 1) route_choose_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(32 * How::WARPS, 1) route_choose_kernel(const __grid_constant__ RouteParams p) {
   __shared__ RouteSmem sm;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int rank = blockIdx.x, ranks = ONE ? gridDim.x : 1;
@@ -792,7 +795,7 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
   const int64_t end = min(b0 + p.block_tokens, int64_t(p.T)) * p.k;
   // the thread's first entry, on its way while the counts are summed
   int64_t i = b0 * p.k + threadIdx.x;
-  int e_next = i < end ? __ldg(p.ids + i) : -1, s_next = i < end ? p.slots[i] : 0;
+  int e_next = i < end ? ptx::load(p.ids + i) : -1, s_next = i < end ? p.slots[i] : 0;
   __syncthreads();
   // Thread (g, e) sums blocks g, g + G, ... of expert e, or of four from e on where
   // the blocks' counts are whole pieces of 16 bytes (256 experts: 12.2 -> 9.3 us);
@@ -804,7 +807,7 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
       int all[4] = {}, before[4] = {};
 #pragma unroll 8
       for (int i = g; i < p.blocks; i += G4) {
-        const int4 c = __ldg(reinterpret_cast<const int4 *>(p.counts + int64_t(i) * p.E + e));
+        const int4 c = ptx::load(reinterpret_cast<const int4 *>(p.counts + int64_t(i) * p.E + e));
         const int v[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -827,7 +830,7 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
         int all = 0, before = 0;
 #pragma unroll 8
         for (int i = g; i < p.blocks; i += G) {
-          const int c = __ldg(p.counts + int64_t(i) * p.E + e);
+          const int c = ptx::load(p.counts + int64_t(i) * p.E + e);
           all += c;
           before += i < b ? c : 0;
         }
@@ -848,7 +851,7 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const RouteParams p) 
     }
     i += blockDim.x;
     if (i < end) {
-      e_next = __ldg(p.ids + i);
+      e_next = ptx::load(p.ids + i);
       s_next = p.slots[i];
     }
   }
@@ -895,7 +898,7 @@ cudaError_t launch_route(const RouteParams &p, cudaStream_t s) {
   // with a warp, 6.7 with 8)
   constexpr int SIDE = 32 / How::LANES;
   auto warps = [&](int tokens) {
-    return std::min({32, kCounters / p.E, std::max((tokens + SIDE - 1) / SIDE, (p.E + 31) / 32)});
+    return std::min({How::WARPS, kCounters / p.E, std::max((tokens + SIDE - 1) / SIDE, (p.E + 31) / 32)});
   };
   // a warp's run of tokens
   auto shared_out = [&](RouteParams q, int tokens) {

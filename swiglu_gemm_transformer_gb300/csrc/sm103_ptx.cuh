@@ -510,12 +510,22 @@ __device__ __forceinline__ void mma_commit_pair_mc(uint32_t bar, uint16_t cta_ma
 
 // Programmatic dependent launch: wait for the preceding grid's results / let
 // the next grid start its prologue.
+// Grids of a chain of such launches are resident together, so what a call reads may be
+// written while the kernel that reads it is running already.  After the wait the
+// writes are visible to ordinary loads (load()); the read-only path (__ldg,
+// ld.global.nc, const __restrict__ arguments) is for memory that nothing writes
+// during a kernel's life, and could return a line that an earlier grid left in the SM.
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class T>
+__device__ __forceinline__ T load(const T *p) {
+  return *p;
 }
 
 // ---- descriptors ----------------------------------------------------------------------

@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           uint4 out = *reinterpret_cast<const uint4 *>(stg + t * C::STG_PITCH + (lane & 3) * 16);
           if (p.rows != nullptr) {
             // a row number that names no row of A gives zeros
-            const int src = __ldg(p.rows + row);
+            const int src = ptx::load(p.rows + row);
             if (src < 0 || src >= p.T) out = make_uint4(0, 0, 0, 0);
           }
           *reinterpret_cast<uint4 *>(p.Y + int64_t(row) * p.N + scol) = out;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int at = min(row0 + 4 * (w + j * C::ROW_WARPS) + i, un.end - 1);
-              idx[j][i] = min(max(__ldg(p.rows + at), 0), p.T - 1);
+              idx[j][i] = min(max(ptx::load(p.rows + at), 0), p.T - 1);
             }
         }
         for (int kb = kb0; kb < kb1; ++kb) {

@@ -243,20 +243,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int col = tile_col(next) + lcol;
     next_w1 = next_w2 = 0.0f;
     if (col < p.N) {
-      next_w1 = __ldg(p.s1 + int64_t(next.e) * p.N + col);
-      if (C::FUSED) next_w2 = __ldg(p.s2 + int64_t(next.e) * p.N + col);
+      next_w1 = ptx::load(p.s1 + int64_t(next.e) * p.N + col);
+      if (C::FUSED) next_w2 = ptx::load(p.s2 + int64_t(next.e) * p.N + col);
     }
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
       const int row = next.row0 + 16 * (h + 2 * (2 * j + (lane >> 4))) + (lane & 15);
       next_src[j] = -1;
-      if (row < next.end) next_src[j] = p.rows ? __ldg(p.rows + row) : row;
+      if (row < next.end) next_src[j] = p.rows ? ptx::load(p.rows + row) : row;
     }
   };
   auto load_scales = [&] {
 #pragma unroll
     for (int j = 0; j < 3; ++j)
-      next_sa[j] = next_src[j] >= 0 && next_src[j] < p.T ? __ldg(p.sa + next_src[j]) : 0.0f;
+      next_sa[j] = next_src[j] >= 0 && next_src[j] < p.T ? ptx::load(p.sa + next_src[j]) : 0.0f;
   };
   auto take_scales = [&] {
     w1 = next_w1;
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int at = min(row0 + 4 * (w + j * C::LOAD_WARPS) + i, un.end - 1);
-              idx[j][i] = min(max(__ldg(p.rows + at), 0), p.T - 1);
+              idx[j][i] = min(max(ptx::load(p.rows + at), 0), p.T - 1);
             }
         }
         for (int kb = kb0; kb < kb1; ++kb, ++step) {

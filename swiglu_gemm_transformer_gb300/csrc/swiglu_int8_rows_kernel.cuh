@@ -42,7 +42,7 @@ struct Int8RowsParams {
 // 16 bytes of weights, not kept in L1.
 __device__ __forceinline__ static uint4 load_weights16(const int8_t *p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -81,7 +81,7 @@ struct FindGroup {
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int i = threadIdx.x + 32 * WARPS * j;
-      bound[j] = i <= p.E ? __ldg(p.offsets + i) : INT32_MIN;
+      bound[j] = i <= p.E ? ptx::load(p.offsets + i) : INT32_MIN;
     }
 #pragma unroll
     for (int j = 0; j < PER; ++j)
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(32 * WARPS) swiglu_int8_token_kernel(const __g
   const int col0 = (static_cast<int>(blockIdx.x % p.col_blocks) * WARPS + warp) * NC;
   ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
-  const int src = p.rows ? __ldg(p.rows + row) : row;
+  const int src = p.rows ? ptx::load(p.rows + row) : row;
   int e = 0;
   if (p.offsets) {
     FindGroup<WARPS> group;
@@ -145,9 +145,9 @@ __global__ void __launch_bounds__(32 * WARPS) swiglu_int8_token_kernel(const __g
   const bool mine = lane < NC && col0 + lane < p.N;
   float s = 0.0f, s1 = 0.0f, s2 = 0.0f;
   if (mine && named) {
-    s = __ldg(p.sa + src);
-    s1 = __ldg(p.s1 + int64_t(e) * p.N + col0 + lane);
-    if (FUSED) s2 = __ldg(p.s2 + int64_t(e) * p.N + col0 + lane);
+    s = ptx::load(p.sa + src);
+    s1 = ptx::load(p.s1 + int64_t(e) * p.N + col0 + lane);
+    if (FUSED) s2 = ptx::load(p.s2 + int64_t(e) * p.N + col0 + lane);
   }
   int acc[MATS][NC] = {};
 #pragma unroll(NC == 1 ? 4 : 2)
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(32 * WARPS) swiglu_int8_token_kernel(const __g
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
       for (int c = 0; c < NC; ++c) v[m][c] = load_weights16(w[m][c] + k);
-    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a + k));
+    const uint4 x = ptx::load(reinterpret_cast<const uint4 *>(a + k));
 #pragma unroll
     for (int m = 0; m < MATS; ++m)
 #pragma unroll
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(32 * WARPS, 3) swiglu_int8_rows_kernel(const _
   // the row of A of place row0 + r, or any where that is past the last place
   auto row_of = [&](int r) {
     const int row = min(row0 + r, p.P - 1);
-    return p.rows ? __ldg(p.rows + row) : row;
+    return p.rows ? ptx::load(p.rows + row) : row;
   };
   const int src = row_of(g);
   int e = 0, end = p.P;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(32 * WARPS, 3) swiglu_int8_rows_kernel(const _
     uint4 x[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      x[h] = live && k + 64 * h + 16 * t < p.K ? __ldg(reinterpret_cast<const uint4 *>(a + k + 64 * h)) : zero;
+      x[h] = live && k + 64 * h + 16 * t < p.K ? ptx::load(reinterpret_cast<const uint4 *>(a + k + 64 * h)) : zero;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -286,10 +286,10 @@ __global__ void __launch_bounds__(32 * WARPS, 3) swiglu_int8_rows_kernel(const _
       for (int m = 0; m < MATS; ++m)
 #pragma unroll
         for (int v = 0; v < WARPS; ++v) z[m] += sums[v][m][r][threadIdx.x % 16];
-      const float s = __ldg(p.sa + from);
+      const float s = ptx::load(p.sa + from);
       const int64_t at = int64_t(e) * p.N + col;
-      y = static_cast<float>(z[0]) * s * __ldg(p.s1 + at);
-      if (FUSED) y = quick_silu_mul(y, static_cast<float>(z[MATS - 1]) * s * __ldg(p.s2 + at));
+      y = static_cast<float>(z[0]) * s * ptx::load(p.s1 + at);
+      if (FUSED) y = quick_silu_mul(y, static_cast<float>(z[MATS - 1]) * s * ptx::load(p.s2 + at));
     }
     p.Y[int64_t(row0 + r) * p.N + col] = __float2bfloat16_rn(y);
   }

@@ -265,7 +265,7 @@ __device__ __forceinline__ static void epilogue_tile_linear(uint32_t tacc, int r
           static_cast<const __nv_bfloat16 *>(p.R) + static_cast<int64_t>(row) * p.N + ccol);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (ccol + 8 * j < p.N) rv[j] = __ldg(rp + j);
+        if (ccol + 8 * j < p.N) rv[j] = ptx::load(rp + j);
     }
     uint32_t v[32];
     ptx::tmem_ld32(tacc + c * 32, v);

@@ -639,3 +639,86 @@ def test_example_block(sg):
     worst, off = moe_block_int8.main(hidden=272, inner=144, experts=16, top_k=4, layers=2, prompt=90)
     # BF16 roundings of Y and Z that fall the other way, a few in a thousand
     assert worst < 2.0**-8 and off < 2.0**-8
+
+
+@pytest.mark.parametrize("M", [1, 8, 33, 125, 700])
+def test_operands_made_anew_in_an_unbroken_chain(sg, M):
+    """As test_calls_wait_for_the_makers_of_all_their_operands, each turn with an output of its own, so
+    that no ordinary launch parts the turns: several of these kernels are resident together."""
+    K, N, turns = 4864, 896, 6
+    g = _gen("unbroken", M)
+    Xs = [torch.randn(M, K, generator=g).to(BF).to(DEV) for _ in range(turns)]
+    Ws = [torch.randn(N, K, generator=g).to(BF).to(DEV) for _ in range(turns)]
+    want = []
+    for X, V in zip(Xs, Ws):
+        one = (*sg.swiglu_quant_int8(X), *sg.swiglu_quant_int8(V))
+        torch.cuda.synchronize()
+        want.append(sg.swiglu_fused_int8(*one, *one[2:]))
+        torch.cuda.synchronize()
+    A, sa = sg.swiglu_quant_int8(Xs[0])
+    W, sw = sg.swiglu_quant_int8(Ws[0])
+    ws = torch.empty(max(sg.lib().swiglu_int8_workspace_size(M, M, 0, N, K, 1), 16), dtype=torch.uint8, device=DEV)
+    for _ in range(3):
+        got = [torch.zeros(M, N, dtype=BF, device=DEV) for _ in range(turns)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(4_000_000)
+        for X, V, Y in zip(Xs, Ws, got):
+            sg.swiglu_quant_int8(X, A, sa)
+            sg.swiglu_quant_int8(V, W, sw)
+            sg.swiglu_fused_int8(A, sa, W, sw, W, sw, Y, workspace=ws)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    _status(sg)
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 300, 700])
+def test_a_block_of_buffers_used_again_in_an_unbroken_chain(sg, T):
+    """Routing, codes, offsets, rows and outputs written anew in the same buffers turn by turn,
+    by kernels that are resident together; only the last norm's outputs are a turn's own."""
+    E, k, N, K, turns = 32, 4, 256, 384, 6
+    g = _gen("unbroken block", T)
+    W1, W2, W3 = (sg.swiglu_quant_int8(torch.randn(E, n, m, generator=g).to(DEV)) for n, m in ((N, K), (N, K), (K, N)))
+    bias = (torch.randn(E, generator=g) * 0.1).to(DEV)
+    ins = [(torch.randn(T, E, generator=g).to(DEV), torch.randn(T, K, generator=g).to(BF).to(DEV), torch.randn(T, K, generator=g).to(DEV))
+           for _ in range(turns)]
+    size = sg.lib().swiglu_int8_workspace_size
+    e = lambda *s, d=F32: torch.zeros(*s, dtype=d, device=DEV)  # noqa: E731
+
+    def buffers():
+        P = T * k
+        return dict(ids=e(T, k, d=torch.int32), weights=e(T, k), offsets=e(E + 1, d=torch.int32), rows=e(P, d=torch.int32),
+                    slots=e(T, k, d=torch.int32), workspace=e(max(sg.lib().swiglu_moe_route_workspace_size(T, E, k), 16), d=torch.uint8)), dict(
+                    A=e(T, K, d=I8), a=e(T), Y=e(P, N, d=BF), B=e(P, N, d=I8), b=e(P), Z=e(P, K, d=BF),
+                    ws=e(max(size(T, P, E, N, K, 1), size(P, P, E, K, N, 0), 16), d=torch.uint8))
+
+    def turn(x, route, m, out, pause):
+        logits, H, R = x
+        sg.swiglu_moe_route_scored(logits, k, bias=bias, groups=4, kept_groups=2, **route)
+        pause()
+        sg.swiglu_quant_int8(H, m["A"], m["a"])
+        pause()
+        sg.swiglu_fused_grouped_int8(m["A"], m["a"], *W1, *W2, route["offsets"], route["rows"], m["Y"], workspace=m["ws"])
+        pause()
+        sg.swiglu_quant_int8(m["Y"], m["B"], m["b"])
+        pause()
+        sg.swiglu_linear_grouped_int8(m["B"], m["b"], *W3, route["offsets"], None, m["Z"], workspace=m["ws"])
+        pause()
+        sg.swiglu_residual_norm(m["Z"], R, slots=route["slots"], weights=route["weights"], Rout=out[0], H=out[1])
+        pause()
+
+    outs = lambda: [(e(T, K), e(T, K, d=BF)) for _ in range(turns)]  # noqa: E731
+    want, got = outs(), outs()
+    for x, out in zip(ins, want):
+        turn(x, *buffers(), out, torch.cuda.synchronize)
+    route, m = buffers()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(4_000_000)
+        for x, out in zip(ins, got):
+            turn(x, route, m, out, lambda: None)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            a[0].zero_(), a[1].zero_()
+    _status(sg)
