@@ -46,6 +46,14 @@ SWIGLU_UNITS_FN uint64_t block_limit(uint64_t limit_ns) {
   return limit_ns > UINT64_MAX / kUnitBlock ? UINT64_MAX : limit_ns * kUnitBlock;
 }
 
+// Time limit of a wait for a whole unit's products in the 8-bit kernel: `limit_ns` for
+// each 1024 steps of K begun (128 of K each; a step takes 0.5 us where weights of
+// 5 GB stream past, so K = 2^20 - 1024 takes 4 ms a unit).
+SWIGLU_UNITS_FN uint64_t unit_limit(uint64_t limit_ns, int steps) {
+  const uint64_t times = 1 + static_cast<uint64_t>(steps) / 1024;
+  return limit_ns > UINT64_MAX / times ? UINT64_MAX : limit_ns * times;
+}
+
 // Sums of 32-bit places below stay below 2^31 for groups of up to 2^31 - 257
 // places (the entry points refuse more): a sum that passes it would give a
 // tile of a negative size.

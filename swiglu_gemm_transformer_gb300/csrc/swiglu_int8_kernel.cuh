@@ -32,7 +32,7 @@
 // cluster share one unit's K; then each finishes a part of its rows, to whose
 // sums it adds the others', in order, from its shared memory (the rings, idle by
 // then).  With one pair finishing all 125 rows a call took 15.4 us, 12.8 so.
-// Every wait is bounded as in the other kernels.
+// Every wait is bounded as in the other kernels, the one for a unit's sums by its K.
 #pragma once
 
 #include <cuda.h>
@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       take_scales();
       more = !C::SPLIT && units.next(next, ok);
       if (more) load_names();
-      ok = __all_sync(0xffffffffu, ok && wait(accf + 8u * abuf, aphase, WAIT_EPI_ACC_FULL));
+      ok = __all_sync(0xffffffffu, ok && wait_bar(accf + 8u * abuf, aphase, unit_limit(p.timeout_ns, kb1 - kb0),
+                                                  abort_flag, p.err, WAIT_EPI_ACC_FULL));
       if (!ok) break;
       ptx::tc_fence_after();
       if constexpr (C::SPLIT) {  // the only unit: its sums meet after the roles

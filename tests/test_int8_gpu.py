@@ -722,3 +722,69 @@ def test_a_block_of_buffers_used_again_in_an_unbroken_chain(sg, T):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
             a[0].zero_(), a[1].zero_()
     _status(sg)
+
+
+def one_code_a_step(M, N, K, mats, seed):
+    """Rows of A with a single one in every M-th step of 128 of K, the rows' steps together all of them; weights
+    of +-1; the sums, whole numbers up to 256 for up to 256 M steps.  A step lost or doubled changes a row in every column."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    steps = -(-K // 128)
+    per = -(-steps // M)
+    assert per <= 256
+    step = torch.arange(M, device=DEV)[:, None] + M * torch.arange(per, device=DEV)
+    at = torch.where(step < steps, (step * 128 + torch.randint(0, 128, step.shape, generator=gen, device=DEV)).clamp(max=K - 1), -1)
+    A = torch.zeros(M, K, dtype=I8, device=DEV)
+    for m in range(M):
+        A[m, at[m][at[m] >= 0]] = 1
+    Ws = [torch.randint(0, 2, (N, K), generator=gen, dtype=I8, device=DEV).mul_(2).sub_(1) for _ in range(mats)]
+    sums = []
+    for W in Ws:
+        picked = W[:, at.clamp(min=0).flatten()].view(N, M, per)
+        sums.append((picked * (at >= 0)).sum(2, dtype=torch.int32).t().double())
+    return A, Ws, sums
+
+
+@pytest.mark.parametrize("M,N,K", [(200, 4872, (1 << 17) + 48), (200, 4864, (1 << 20) - 1024), (200, 16, (1 << 20) - 1024),
+                                   (40, 264, (1 << 20) - 1024), (300, 24, (1 << 19) + 16)])
+def test_every_step_of_a_long_k_counts_once(sg, M, N, K):
+    """The persistent and the shared tensor-core forms, under the shortest wait limit: a unit's K takes longer than it."""
+    A, (W,), (want,) = one_code_a_step(M, N, K, 1, N)
+    one = torch.ones(max(M, N), device=DEV)
+    _status(sg)
+    sg.swiglu_set_wait_timeout_ns(1_000_000)
+    try:
+        Z = sg.swiglu_linear_int8(A, one[:M].contiguous(), W, one[:N].contiguous())
+    finally:
+        sg.swiglu_set_wait_timeout_ns(2_000_000_000)
+    _status(sg)
+    assert torch.equal(Z.double(), want)
+
+
+def test_every_step_of_a_long_k_counts_once_fused(sg):
+    M, N, K = 200, 2440, (1 << 17) + 48
+    A, (W1, W2), (g, u) = one_code_a_step(M, N, K, 2, 3)
+    one = torch.ones(N, device=DEV)
+    Y = sg.swiglu_fused_int8(A, one[:M].contiguous(), W1, one, W2, one)
+    _status(sg)
+    want = g * torch.sigmoid(g) * u    # g and u are exact; 2^-19: exp and reciprocal
+    assert ((Y.double() - want).abs() <= (2.0**-8 + 2.0**-19) * want.abs() + 1e-37).all()
+
+
+def test_many_long_units_within_a_short_limit(sg):
+    """The finder's wait for 32 units (about 2 ms here, one takes 0.06 ms) has a limit of its own."""
+    P, K, N = 85000, 16384, 4096        # 443 row tiles x 16 column tiles: 93 units a pair
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    A = torch.randint(-127, 128, (P, K), generator=gen, dtype=I8, device=DEV)
+    W = torch.randint(-127, 128, (1, N, K), generator=gen, dtype=I8, device=DEV)
+    a, w = torch.rand(P, generator=gen, device=DEV) * 0.01, torch.rand(1, N, generator=gen, device=DEV) * 0.01
+    off = torch.tensor([0, P], dtype=torch.int32, device=DEV)
+    _status(sg)
+    sg.swiglu_set_wait_timeout_ns(1_000_000)
+    try:
+        Z = sg.swiglu_linear_grouped_int8(A, a, W, w, off)
+    finally:
+        sg.swiglu_set_wait_timeout_ns(2_000_000_000)
+    _status(sg)
+    for i, j in ((0, 3), (42000, 42002), (P - 3, P)):
+        ref, tol = product_ref(A[i:j], a[i:j], [(W, w)], [0, j - i], None)
+        assert ((Z[i:j].double() - ref).abs() <= tol).all(), (i, j)
