@@ -788,3 +788,17 @@ def test_many_long_units_within_a_short_limit(sg):
     for i, j in ((0, 3), (42000, 42002), (P - 3, P)):
         ref, tol = product_ref(A[i:j], a[i:j], [(W, w)], [0, j - i], None)
         assert ((Z[i:j].double() - ref).abs() <= tol).all(), (i, j)
+
+
+@pytest.mark.parametrize("N,K", [(4872, (1 << 17) + 48), (264, (1 << 18) + 16)])
+def test_long_sums_of_one_sign_by_number_of_rows(sg, N, K):
+    """Sums to 2^32: up to 8 rows integers, exact; more rows K additions of FP32, each off by 2^-23 of the sum at most."""
+    c, d = torch.arange(200, device=DEV) % 128 - 128, torch.arange(N, device=DEV) % 127 - 128
+    A, W = (v.to(I8)[:, None].expand(-1, K).contiguous() for v in (c, d))
+    one = torch.ones(N, device=DEV)
+    exact = (K * c[:, None] * d[None]).double()
+    few = sg.swiglu_linear_int8(A[:8], one[:8].contiguous(), W, one)
+    assert torch.equal(few, exact[:8].float().to(BF))
+    many = sg.swiglu_linear_int8(A, one[:200].contiguous(), W, one)
+    _status(sg)
+    assert ((many.double() - exact).abs() <= (K * 2.0**-23 + 2.0**-8) * exact).all()
