@@ -20,6 +20,11 @@ constexpr int64_t kMaxTiled = kMaxDim - 256;
 // A warp of the rows kernel adds 128 * 128 * K / 8 at most, in whole turns of 1024 of K.
 constexpr int64_t kMaxK = (int64_t(1) << 20) - 1024;
 
+// One expert's matrix: the tensor map's largest stride is 2^40 bytes.
+bool matrix_fits(int64_t N, int64_t K) { return uint64_t(N) * uint64_t(K) < uint64_t(1) << 40; }
+// Rows of K and of N are copied in pieces of 16 bytes.
+bool whole_pieces(int64_t N, int64_t K) { return N % 8 == 0 && K % 16 == 0; }
+
 struct Int8Call {
   const void *A, *W1, *W2;  // W2 == nullptr: the linear form
   const float *sa, *s1, *s2;
@@ -266,8 +271,7 @@ int run_int8(const Int8Call &c) {
   if (T > kMaxDim || P > kMaxTiled || N > kMaxTiled || K > kMaxK || E > kMaxExperts)
     return SWIGLU_ERR_UNSUPPORTED;
   if (P == 0 || N == 0) return SWIGLU_OK;
-  // one expert's matrix: the tensor map's largest stride is 2^40 bytes
-  if (uint64_t(N) * uint64_t(K) >= uint64_t(1) << 40) return SWIGLU_ERR_UNSUPPORTED;
+  if (!matrix_fits(N, K)) return SWIGLU_ERR_UNSUPPORTED;
   if (!c.Y || (c.grouped && !c.offsets)) return SWIGLU_ERR_INVALID_ARG;
   if (K > 0 && (!c.W1 || !c.s1 || (c.fused && (!c.W2 || !c.s2)) || (T > 0 && (!c.A || !c.sa))))
     return SWIGLU_ERR_INVALID_ARG;
@@ -276,7 +280,7 @@ int run_int8(const Int8Call &c) {
   if (K > 0 && (!ptr_aligned(c.A, 16) || !ptr_aligned(c.W1, 16) || !ptr_aligned(c.W2, 16) ||
                 !ptr_aligned(c.sa, 4) || !ptr_aligned(c.s1, 4) || !ptr_aligned(c.s2, 4)))
     return SWIGLU_ERR_MISALIGNED;
-  if (N % 8 != 0 || K % 16 != 0) return SWIGLU_ERR_MISALIGNED;
+  if (!whole_pieces(N, K)) return SWIGLU_ERR_MISALIGNED;
   const uint64_t y_bytes = uint64_t(P) * N * 2, w_bytes = uint64_t(E) * N * K, s_bytes = uint64_t(E) * N * 4;
   if (ranges_overlap(c.Y, y_bytes, c.A, uint64_t(T) * K) || ranges_overlap(c.Y, y_bytes, c.W1, w_bytes) ||
       ranges_overlap(c.Y, y_bytes, c.W2, w_bytes) || ranges_overlap(c.Y, y_bytes, c.sa, uint64_t(T) * 4) ||
@@ -331,7 +335,7 @@ extern "C" uint64_t swiglu_int8_workspace_size(int64_t T, int64_t P, int64_t E, 
                                                int32_t fused) {
   using namespace swiglu;
   if (T < 1 || T > kMaxDim || P < 1 || P > kMaxTiled || E < 0 || E > kMaxExperts || N < 1 || N > kMaxTiled || K < 1 ||
-      K > kMaxK || few_rows(P, E, N, K, fused != 0))
+      K > kMaxK || !matrix_fits(N, K) || !whole_pieces(N, K) || (E == 0 && T != P) || few_rows(P, E, N, K, fused != 0))
     return 0;
   return widened_bytes(T, P, K);
 }

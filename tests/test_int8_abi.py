@@ -134,3 +134,17 @@ def test_python_binding_refuses_cpu_tensors_and_types(lib):
         sg.swiglu_fused_int8(q, s, q, s, None, s)
     with pytest.raises(TypeError):
         sg.swiglu_fused_grouped_int8(q, s, w, ws, w, ws, None)
+
+
+@pytest.mark.parametrize("fused", [0, 1])
+@pytest.mark.parametrize("args", [(512, 512, 8, 60, 64), (512, 512, 8, 64, 56), (512, 512, 0, 64, 8), (512, 300, 0, 64, 64),
+                                  (512, 512, 8, 1 << 22, 1 << 18), (512, 512, 0, (1 << 31) - 512, 1 << 10), (512, 512, 1, 1 << 24, 1 << 16)])
+def test_workspace_size_is_zero_for_refused_sizes(lib, args, fused):
+    """Columns and K of other multiples, matrices of 2^40 bytes, a dense call of two sizes of rows."""
+    assert lib.swiglu_int8_workspace_size(*args, fused) == 0
+
+
+def test_workspace_size_of_the_largest_matrices(lib):
+    size = lib.swiglu_int8_workspace_size
+    assert size(512, 512, 8, (1 << 20) + 1024, (1 << 20) - 1024, 0) == 512 * ((1 << 20) - 1024) * 2   # N K = 2^40 - 2^20
+    assert size(512, 512, 8, (1 << 20) + 1032, (1 << 20) - 1024, 0) == 0
