@@ -22,12 +22,11 @@
 // match_any), the warps' counts are summed in order, and each warp walks its
 // entries again and numbers them within the block.
 //
-// Up to kOneTokens tokens are one launch of one cluster of at most eight blocks, 8
-// tokens a block or as many as it takes: one SM issues the choices of 128 tokens in
-// about 6 us, so a few tokens are spread over several; the blocks read each other's
-// counts through distributed shared memory, which costs 0.8 us.  In a graph, 256
-// experts: 64 tokens by logit 5.7 us, by scores 8.6 (32 tokens a block: 10.1 and
-// 13.4); 8 tokens 4.4 and 7.1 (one a block: 5.1 and 8.1).  Beyond that a first kernel
+// Up to kOneTokens tokens are one launch of one cluster of at most eight blocks: one SM
+// issues the choices of 128 tokens in about 6 us, so they are spread over several
+// (route_blocks.h), which read each other's counts through distributed shared memory.
+// In a graph, 256 experts: 64 tokens by logit 5.5 us, by scores 6.7 (32 tokens a block:
+// 9.7 and 10.9); 8 tokens 4.3 and 5.4.  Beyond that a first kernel
 // numbers the entries within each block of 32 to 128 tokens (in slots) and writes
 // the block's counts to the workspace, and a second one, overlapped by
 // programmatic dependent launch, sums the counts of the blocks before its own
@@ -56,6 +55,7 @@
 #include <cmath>
 
 #include "launch.h"
+#include "route_blocks.h"
 #include "sm103_ptx.cuh"
 #include "swiglu.h"
 
@@ -64,9 +64,6 @@ namespace {
 
 constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
-constexpr int kOneTokens = 256;          // tokens of the one-launch form,
-constexpr int kOneBlocks = 8;            // blocks of its cluster, at most
-constexpr int kOneLeast = 8;             // tokens of a block, a power of two, at least
 constexpr int kBlockTokens = 128;        // most tokens per block otherwise
 // Warps of a block x experts: 32 warps up to 510 experts, and RouteSmem is the 48 KB
 // that a kernel may hold without asking.
@@ -620,6 +617,7 @@ __device__ __noinline__ void choose_in_64(const RouteParams &p, const ScorePlan<
 template <int LPT, int EPL, bool FP32>
 struct ByLogit {
   static constexpr int LANES = LPT, WARPS = 32;  // of a token; most of a block
+  static OneLaunch one(const RouteParams &) { return one_by_logit(LPT); }
   __device__ ByLogit(const RouteParams &, int, void *) {}
   __device__ __forceinline__ void choose(const RouteParams &p, int64_t t, int64_t end, int lane, uint16_t *ids16) {
     swiglu::choose<LPT, EPL, FP32>(p, t, end, lane, ids16);
@@ -632,6 +630,7 @@ struct ByLogit {
 template <int EPL>
 struct ByScore {
   static constexpr int LANES = 32, WARPS = EPL > 16 ? 16 : 32;
+  static OneLaunch one(const RouteParams &p) { return one_by_score(EPL, p.k); }
   ScorePlan<EPL> plan;
   __device__ ByScore(const RouteParams &p, int lane, void *spare)
       : plan(p, lane, static_cast<Candidates *>(spare) + (threadIdx.x >> 5)) {}
@@ -907,13 +906,10 @@ cudaError_t launch_route(const RouteParams &p, cudaStream_t s) {
   };
   if (p.T <= kOneTokens) {
     RouteParams one = p;
-    one.block_tokens = kOneLeast;
-    while (one.block_tokens * kOneBlocks < p.T) one.block_tokens *= 2;
-    one.blocks = 1;  // a power of two
-    while (one.blocks * one.block_tokens < p.T) one.blocks *= 2;
-    const int tokens = std::min(p.T, one.block_tokens);
-    return launch_pdl(route_choose_kernel<How, true>, one.blocks, one.blocks, 32 * warps(tokens),
-                      shared_out(one, tokens), s);
+    one.block_tokens = one_block_tokens(p.T, How::one(p));
+    one.blocks = one_blocks(p.T, one.block_tokens);
+    return launch_pdl(route_choose_kernel<How, true>, one.blocks, one.blocks, 32 * warps(one.block_tokens),
+                      shared_out(one, one.block_tokens), s);
   }
   const cudaError_t e = launch_pdl(route_choose_kernel<How, false>, p.blocks, 1, 32 * warps(p.block_tokens),
                                    shared_out(p, p.block_tokens), s);
