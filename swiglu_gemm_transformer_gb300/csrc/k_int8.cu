@@ -37,22 +37,37 @@ struct Int8Call {
   void *stream;
 };
 
+// One row, or places that hardly share experts: a block for each place.
+bool one_block_a_place(int64_t P, int64_t E) { return P == 1 || 4 * P <= E; }
+
 // Whether the kernels for a few rows run.  They read a matrix once for 8 rows (from
 // L2 after the first time), the tensor-core form once for 192, but that begins with
 // a second kernel and ends with a longer tail, about 4 us together.
-// Dense, by tiles of 8 rows and bytes of weights (us, rows | tensor cores): 136 MB 8
-// rows 27.4 | 29.9, 16 rows 41 | 30; 68 MB 18.0 | 22.1, 27 | 22; 13 MB 16 rows 6.0 |
+// Dense, by tiles of 8 rows and bytes of weights (us, rows | tensor cores): 484 MB 8
+// rows 81 | 102, 16 rows 150 | 105; 242 MB 8 rows 44 | 54 (K = 8192), 53 | 49 (K =
+// 29568); 136 MB 27.8 | 28.7, 49 | 29; 68 MB 17.8 | 22.1, 20.5 | 22.2; 13 MB 16 rows 6.0 |
 // 11.2; 4.4 MB 32 rows 5.7 | 11.8; 8.7 MB 32 rows 9.0 | 9.2.
-// Grouped, where every place has blocks: 64 experts of 4 MB, 32 places 22.4 | 27.9,
-// 64 places 36.3 | 40.6, 128 places 56.3 | 52.8; of 2 MB, 16 places 8.5 | 14.2, 32
-// places 19.1 | 18.6; 8 experts of 13 MB, 32 places 28.4 | 30.1, 64 places 45.9 |
-// 30.2; of 2 MB, 16 places 8.3 | 9.4, 32 places 11.3 | 9.6.
+// Grouped, every place has its blocks of 16 columns, of which those of the first of
+// eight of an expert work; a block costs 2 to 2.5 ns, a matrix read once more 0.15 us a MB,
+// and the tensor-core form reads large matrices slower, by 0.025 us a MB of each expert used
+// (fitted to 330 sizes; the form it takes is 0.3 % slower than the better one on average,
+// 14 % at most).  Places at random, in a graph: one expert of 4.2 MB (2048 x 1024,
+// gate/up) 16 places 6.1 | 8.2, 32 places 10.2 | 8.2; one of 136 MB 2 places 28.6 | 27.9,
+// 32 places 188 | 28; 8 of 8.7 MB (896 x 4864) 8 places 17.2 | 15.8, 16 places 27 | 18.7;
+// 8 of 68 MB (18944 x 3584) 24 places 71 | 111, 64 places 119 | 113; 64 of 4.2 MB 32
+// places 23.6 | 26.4, 96 places 48.8 | 43.3.
+constexpr int64_t kFewPlaces = 128;  // as far as this was measured
+
 bool few_rows(int64_t P, int64_t E, int64_t N, int64_t K, bool fused) {
-  const int64_t bytes = N * K * (fused ? 2 : 1);
-  if (E > 0)
-    return (P <= 16 || (bytes >= 4000000 && P <= std::max<int64_t>(32, std::min<int64_t>(E, 64)))) &&
-           P * ceil_div(N, 8) <= kMaxDim;  // blocks
-  const int64_t tiles = ceil_div(P, 8);
+  const int64_t bytes = N * K * (fused ? 2 : 1), tiles = ceil_div(P, 8);
+  if (E > 0) {
+    const int64_t blocks = ceil_div(N, 16), used = std::min(E, P);
+    if (P > kFewPlaces || P * ceil_div(N, 8) > kMaxDim) return false;
+    // twice the nanoseconds that the rows' kernel takes longer, but for those 4 us
+    const int64_t longer = (4 * (P - used) + 5 * used) * blocks +
+                           (std::max(tiles, used) - used) * bytes * 3 / 10000 - used * bytes / 20000;
+    return one_block_a_place(P, E) || longer < 9000;
+  }
   return tiles == 1 || (tiles <= 16 && bytes <= 200000000 / (9 * tiles - 11));
 }
 
@@ -137,7 +152,7 @@ cudaError_t run_rows(Int8RowsParams &p, bool fused, cudaStream_t s) {
   // 15.2; of 4096 x 8192 11.0 and 8.4).  Grouped, two blocks: a block begins with
   // the search for its expert (one token, 8 of 64 experts, 2048 x 1024, gate/up 9.3
   // and 8.5 us, down 7.2 and 5.8).
-  if (p.P == 1 || (p.offsets && 4 * p.P <= p.E)) {
+  if (one_block_a_place(p.P, p.offsets ? p.E : 0)) {
     const int64_t cols = int64_t(p.N) * p.P / (8 * 152 * (p.offsets ? 2 : 4));  // of a warp
     if (fused)
       return cols >= 2 ? launch_rows(swiglu_int8_token_kernel<true, 2, 8>, p, p.P, 16, s)

@@ -148,3 +148,16 @@ def test_workspace_size_of_the_largest_matrices(lib):
     size = lib.swiglu_int8_workspace_size
     assert size(512, 512, 8, (1 << 20) + 1024, (1 << 20) - 1024, 0) == 512 * ((1 << 20) - 1024) * 2   # N K = 2^40 - 2^20
     assert size(512, 512, 8, (1 << 20) + 1032, (1 << 20) - 1024, 0) == 0
+
+
+@pytest.mark.parametrize("E,N,K,fused,few,many", [   # (places at which either form was measured at least 10 % faster)
+    (1, 1024, 2048, 1, (2, 16), (32, 64, 128)), (1, 4864, 896, 1, (2, 4), (12, 32, 128)), (1, 8192, 8192, 0, (2, 4), (12, 32, 128)),
+    (1, 18944, 3584, 1, (1,), (4, 8, 16, 32, 128)), (2, 18944, 3584, 1, (1,), (8, 16, 32)), (8, 4864, 896, 1, (2, 4), (12, 16, 32)),
+    (8, 896, 4864, 0, (8, 32), (64, 128)), (8, 3584, 18944, 0, (2, 24, 32), (96, 128)), (8, 14336, 4096, 1, (2,), (16, 32)),
+    (64, 1024, 2048, 1, (8, 32), (96, 128)), (64, 4864, 896, 1, (8,), (24, 32, 64)), (256, 2048, 1024, 0, (8, 64), (96, 128))])
+def test_grouped_calls_of_few_places_take_the_faster_form(lib, E, N, K, fused, few, many):
+    """The form of few rows needs no workspace."""
+    for P in few:
+        assert lib.swiglu_int8_workspace_size(P, P, E, N, K, fused) == 0, P
+    for P in many:
+        assert lib.swiglu_int8_workspace_size(P, P, E, N, K, fused) == P * K * 2, P
