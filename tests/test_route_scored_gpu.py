@@ -286,3 +286,15 @@ def test_more_pinned_experts_than_choices(sg, bias):
     for groups, kept, best in ((1, 1, 2), (8, 3, 1), (8, 3, 2)):
         check(sg, x, 6, b, groups=groups, kept=kept, best=best)
     check(sg, x, 6, torch.full((64,), bias), groups=8, kept=3)
+
+
+@SCORES
+@pytest.mark.parametrize("shape", [(300, 1024, 8, 8, 4, 2), (257, 1022, 6, 2, 1, 1), (600, 513, 3, 1, 1, 2), (700, 70, 5, 2, 2, 2),
+                                   (5000, 33, 4, 1, 1, 1)], ids=lambda s: "x".join(map(str, s)))
+def test_two_launches_of_many_or_odd_experts(sg, shape, score):
+    """Blocks of fewer warps, and counts that are no whole pieces of four experts."""
+    T, E, k, groups, kept, best = shape
+    g = _gen("two launches", *shape, score)
+    x = torch.randn(T, E, generator=g) * 1.5
+    x[T // 3] = -math.inf
+    check(sg, x, k, torch.randn(E, generator=g) * 0.1, score=score, groups=groups, kept=kept, best=best)
