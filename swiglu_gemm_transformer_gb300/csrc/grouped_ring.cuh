@@ -57,56 +57,56 @@ __device__ __forceinline__ static void find_units(GroupedUnit *ring, int *off, i
                                                   int num_n_blk, int cid, int ncl, uint64_t timeout_ns,
                                                   uint32_t *err, volatile int *abort_flag) {
   const int lane = threadIdx.x & 31;
-      // Group bounds and row-tile counts.  The bounds are clamped to [0, P] and
-      // made monotone, so that no value of `offsets` reaches past Y.
-      int top = 0, sum = 0;
-      constexpr int AHEAD = 4;  // loads in flight: each is a trip to memory
-      int raw[AHEAD];
-      for (int e0 = 0; e0 <= E; e0 += 32) {
-        const int e = e0 + lane, slot = (e0 / 32) % AHEAD;
-        if (slot == 0) {
+  // Group bounds and row-tile counts.  The bounds are clamped to [0, P] and
+  // made monotone, so that no value of `offsets` reaches past Y.
+  int top = 0, sum = 0;
+  constexpr int AHEAD = 4;  // loads in flight: each is a trip to memory
+  int raw[AHEAD];
+  for (int e0 = 0; e0 <= E; e0 += 32) {
+    const int e = e0 + lane, slot = (e0 / 32) % AHEAD;
+    if (slot == 0) {
 #pragma unroll
-          for (int i = 0; i < AHEAD; ++i)
-            raw[i] = e + 32 * i <= E ? (offsets ? ptx::load(offsets + e + 32 * i) : e == 0 ? 0 : P) : 0;
-        }
-        int v = raw[0];
+      for (int i = 0; i < AHEAD; ++i)
+        raw[i] = e + 32 * i <= E ? (offsets ? ptx::load(offsets + e + 32 * i) : e == 0 ? 0 : P) : 0;
+    }
+    int v = raw[0];
 #pragma unroll
-        for (int i = 1; i < AHEAD; ++i) v = slot == i ? raw[i] : v;
-        v = e <= E ? min(max(v, 0), P) : 0;
+    for (int i = 1; i < AHEAD; ++i) v = slot == i ? raw[i] : v;
+    v = e <= E ? min(max(v, 0), P) : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int w = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v = max(v, w);
-        }
-        v = max(v, top);
-        const int prev = __shfl_up_sync(0xffffffffu, v, 1);
-        // row tiles of expert e - 1
-        int t = e >= 1 && e <= E ? row_tiles<NT>(v - (lane == 0 ? top : prev)) : 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, w);
+    }
+    v = max(v, top);
+    const int prev = __shfl_up_sync(0xffffffffu, v, 1);
+    // row tiles of expert e - 1
+    int t = e >= 1 && e <= E ? row_tiles<NT>(v - (lane == 0 ? top : prev)) : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int w = __shfl_up_sync(0xffffffffu, t, o);
-          if (lane >= o) t += w;
-        }
-        t += sum;
-        if (e <= E) {
-          off[e] = v;
-          tiles[e] = t;
-        }
-        top = __shfl_sync(0xffffffffu, v, 31);
-        sum = __shfl_sync(0xffffffffu, t, 31);
-      }
-      __syncwarp();
-      for (uint32_t block = 0;; ++block) {
-        const bool ok = wait_bar(unite_bar + 8u * (block & 1u), ((block >> 1) & 1u) ^ 1u,
-                                 block_limit(timeout_ns), abort_flag, err, WAIT_SCHED_EMPTY);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        const GroupedUnit r = grouped_unit<GROUP>(cid + (int64_t(block) * 32 + lane) * ncl, off,
-                                                     tiles, E, num_n_blk);
-        *reinterpret_cast<int4 *>(ring + 32 * (block & 1u) + lane) = make_int4(r.row0, r.end, r.e, r.nb);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(unitf_bar + 8u * (block & 1u));
-        if (__any_sync(0xffffffffu, r.row0 < 0)) break;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += w;
+    }
+    t += sum;
+    if (e <= E) {
+      off[e] = v;
+      tiles[e] = t;
+    }
+    top = __shfl_sync(0xffffffffu, v, 31);
+    sum = __shfl_sync(0xffffffffu, t, 31);
+  }
+  __syncwarp();
+  for (uint32_t block = 0;; ++block) {
+    const bool ok = wait_bar(unite_bar + 8u * (block & 1u), ((block >> 1) & 1u) ^ 1u,
+                             block_limit(timeout_ns), abort_flag, err, WAIT_SCHED_EMPTY);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    const GroupedUnit r = grouped_unit<GROUP>(cid + (int64_t(block) * 32 + lane) * ncl, off,
+                                                 tiles, E, num_n_blk);
+    *reinterpret_cast<int4 *>(ring + 32 * (block & 1u) + lane) = make_int4(r.row0, r.end, r.e, r.nb);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(unitf_bar + 8u * (block & 1u));
+    if (__any_sync(0xffffffffu, r.row0 < 0)) break;
+  }
 }
 
 }  // namespace swiglu

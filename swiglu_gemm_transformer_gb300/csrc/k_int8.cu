@@ -145,15 +145,15 @@ cudaError_t launch_rows(void (*kern)(Int8RowsParams), Int8RowsParams &p, int64_t
 }
 
 // The kernels for a few rows.
-cudaError_t run_rows(Int8RowsParams &p, bool fused, cudaStream_t s) {
+cudaError_t run_rows(Int8RowsParams &p, bool fused, int sms, cudaStream_t s) {
   // One row, or places that hardly share experts: a block for each place, whose
   // warps take one, two or four columns of each matrix, as many as leave four blocks
-  // to each of the 152 SMs (one row of 18944 x 3584 with four columns 25.1 us, so
+  // to each SM (one row of 18944 x 3584 with four columns 25.1 us, so
   // 15.2; of 4096 x 8192 11.0 and 8.4).  Grouped, two blocks: a block begins with
   // the search for its expert (one token, 8 of 64 experts, 2048 x 1024, gate/up 9.3
   // and 8.5 us, down 7.2 and 5.8).
   if (one_block_a_place(p.P, p.offsets ? p.E : 0)) {
-    const int64_t cols = int64_t(p.N) * p.P / (8 * 152 * (p.offsets ? 2 : 4));  // of a warp
+    const int64_t cols = int64_t(p.N) * p.P / (8 * sms * (p.offsets ? 2 : 4));  // of a warp
     if (fused)
       return cols >= 2 ? launch_rows(swiglu_int8_token_kernel<true, 2, 8>, p, p.P, 16, s)
                        : launch_rows(swiglu_int8_token_kernel<true, 1, 8>, p, p.P, 8, s);
@@ -229,7 +229,7 @@ int run_tensor(const Int8Call &c, uint32_t *err, uint64_t timeout_ns, uint64_t c
   const int32_t k_blk = int32_t(ceil_div(c.K, Fused::BK)), n_blk = int32_t(ceil_div(c.N, c.fused ? 128 : 256));
   auto units = [&](int nt) { return (c.offsets ? std::min(c.E, c.P) + c.P / nt : ceil_div(c.P, nt)) * n_blk; };
   // Few units and enough K to share: several pairs to a unit.  A cluster of four
-  // or eight CTAs fits the GPU 36 or 15 times.  125 rows of 4864 x 896 22.7 -> 13.5
+  // or eight CTAs fits the GB300 36 or 15 times.  125 rows of 4864 x 896 22.7 -> 13.5
   // us, 128 rows of 3584 x 3584 19.2 -> 13.8, of 2048 x 2048 13.9 -> 11.5; at 8 K
   // steps (64 rows of 1024 x 2048) 9.6 and 9.7.
   const int64_t few = units(Split::NT);
@@ -339,7 +339,7 @@ int run_int8(const Int8Call &c) {
   p.N = int32_t(N);
   p.K = int32_t(K);
   if (need > 0) return run_tensor(c, err, timeout_ns, gen);
-  const cudaError_t e = run_rows(p, c.fused, s);
+  const cudaError_t e = run_rows(p, c.fused, sms, s);
   return e == cudaSuccess ? SWIGLU_OK : SWIGLU_ERR_CUDA;
 }
 

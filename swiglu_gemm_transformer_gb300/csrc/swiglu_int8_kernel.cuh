@@ -278,12 +278,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   // `release` (cluster address) once the warp has read it.
   auto finish = [&](uint32_t tacc, uint32_t release) {
     const uint32_t stg = base + C::STG_OFF + warp * C::STG_BYTES;
-    const int nchunk = mine.n() / 16, col0 = tile_col(mine);
-    if (!C::SPLIT && h >= nchunk) {
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster_relaxed(release);
-    }
+    const int nchunk = mine.n() / 16, col0 = tile_col(mine);  // at least two chunks: one for each h
 #pragma unroll 1
     for (int c = h, i = 0; c < nchunk; c += 2, ++i) {
       if (C::SPLIT && owner(c) != static_cast<int>(lead >> 1)) continue;

@@ -245,6 +245,18 @@ __global__ void __launch_bounds__(32 * WARPS, 3) swiglu_int8_rows_kernel(const _
     if ((row0 - start) % ROWS != 0) return;  // another block's
   }
   end = min(min(end, p.P), row0 + ROWS);
+  // the thread's result, of row r and column col, and its scales, on their way meanwhile
+  const int r = threadIdx.x / 16, col = col0 + threadIdx.x % 16;
+  const bool mine = r < ROWS && row0 + r < end && col < p.N;
+  const int from = mine ? row_of(r) : -1;
+  const bool named = from >= 0 && from < p.T;
+  float s = 0.0f, s1 = 0.0f, s2 = 0.0f;
+  if (named) {
+    const int64_t at = int64_t(e) * p.N + col;
+    s = ptx::load(p.sa + from);
+    s1 = ptx::load(p.s1 + at);
+    if (FUSED) s2 = ptx::load(p.s2 + at);
+  }
   // the lane's row g; past the end, zeros
   const bool live = row0 + g < end;
   const int8_t *a = p.A + int64_t(min(max(src, 0), p.T - 1)) * p.K + 16 * t;
@@ -275,21 +287,17 @@ __global__ void __launch_bounds__(32 * WARPS, 3) swiglu_int8_rows_kernel(const _
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[warp][m][2 * t + (i & 1)][g + 8 * (i >> 1)] = acc[m][i];
   __syncthreads();
-  const int r = threadIdx.x / 16, col = col0 + threadIdx.x % 16;
-  if (r < ROWS && row0 + r < end && col < p.N) {
-    const int from = row_of(r);
+  if (mine) {
     float y = 0.0f;  // a row number that names no row of A gives zeros
-    if (from >= 0 && from < p.T) {
+    if (named) {
       // (a warp's sum stays below 2^31 up to the largest K, the block's perhaps not)
       long long z[MATS] = {};
 #pragma unroll
       for (int m = 0; m < MATS; ++m)
 #pragma unroll
         for (int v = 0; v < WARPS; ++v) z[m] += sums[v][m][r][threadIdx.x % 16];
-      const float s = ptx::load(p.sa + from);
-      const int64_t at = int64_t(e) * p.N + col;
-      y = static_cast<float>(z[0]) * s * ptx::load(p.s1 + at);
-      if (FUSED) y = quick_silu_mul(y, static_cast<float>(z[MATS - 1]) * s * ptx::load(p.s2 + at));
+      y = static_cast<float>(z[0]) * s * s1;
+      if (FUSED) y = quick_silu_mul(y, static_cast<float>(z[MATS - 1]) * s * s2);
     }
     p.Y[int64_t(row0 + r) * p.N + col] = __float2bfloat16_rn(y);
   }
