@@ -374,7 +374,10 @@ __global__ void __launch_bounds__(THREADS + 32, ring_most_blocks(THREADS, VPT))
   // The norms' weights and a gate of one row stay in registers where these
   // suffice; longer rows read them again (from L1 or L2) for every row.
   constexpr bool HOLD = VPT <= 2;
-  uint4 gpost[VPT], gpre[VPT], gb[VPT];  // gb: the gate, of one row or of the row at hand
+  // A gate of one row and that of the row at hand share registers, but for FP32 rows of
+  // up to 4096 (8191 rows of 4096 76 us with registers of their own, 88 without).
+  constexpr bool SHARE = !R32 || THREADS > 256;
+  uint4 gpost[VPT], gpre[VPT], gvec[VPT];
   const bool gate_vec = p.gate && !l.g_bytes;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(THREADS + 32, ring_most_blocks(THREADS, VPT))
     if (!HOLD || v >= nv) continue;
     if (p.gamma_post) gpost[i] = ptx::load(reinterpret_cast<const uint4 *>(p.gamma_post) + v);
     if (p.gamma_pre) gpre[i] = ptx::load(reinterpret_cast<const uint4 *>(p.gamma_pre) + v);
-    if (gate_vec) gb[i] = ptx::load(reinterpret_cast<const uint4 *>(p.gate) + v);
+    if (gate_vec) gvec[i] = ptx::load(reinterpret_cast<const uint4 *>(p.gate) + v);
   }
   const float inv_d = 1.0f / p.D;
   int parity = 0;
@@ -396,6 +399,8 @@ __global__ void __launch_bounds__(THREADS + 32, ring_most_blocks(THREADS, VPT))
     float z[VPT][8], f[8];
     float ss = 0.0f;
     float r[VPT][8];
+    uint4 own[VPT];
+    auto &gb = SHARE ? gvec : own;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = threadIdx.x + i * THREADS;
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(THREADS + 32, ring_most_blocks(THREADS, VPT))
         for (int c = 0; c < 8; ++c) z[i][c] *= f[c];
       }
       if (p.gate) {
-        bf16x8(HOLD || !gate_vec ? gb[i] : ptx::load(reinterpret_cast<const uint4 *>(p.gate) + v), f);
+        bf16x8(!gate_vec ? gb[i] : HOLD ? gvec[i] : ptx::load(reinterpret_cast<const uint4 *>(p.gate) + v), f);
 #pragma unroll
         for (int c = 0; c < 8; ++c) z[i][c] *= f[c];
       }
