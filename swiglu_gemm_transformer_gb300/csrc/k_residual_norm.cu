@@ -21,7 +21,7 @@
 //     for R, one for the gate), so that memory stays busy through the
 //     reductions, and the norms' weights stay in registers from row to row.
 //     Its outputs are stored evict-first (8191 rows x 8192, FP32 residual and a
-//     gate per row: 156.5 -> 151.2 us; 8192 rows x 2048, 8 joined: 64.4 and 64.9).
+//     gate per row: 156.5 -> 151.2 us; now 156.6; 8192 rows x 2048, 8 joined: 59.9).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

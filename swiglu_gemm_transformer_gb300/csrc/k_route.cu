@@ -43,8 +43,8 @@
 // lie further apart than their rounding errors together, and where two do not,
 // which is so for about a token in a thousand, FP64 settles the few values
 // concerned (without a bias the logits' own order decides, and only sums of two
-// scores are compared).  Bound by instructions: 16384 tokens, 256 experts in 8
-// groups, 34 us (55 with all scores of such a token in FP64 and a round over all
+// scores are compared).  16384 tokens, 256 experts in 8 groups, 33.5 us, of which a
+// scheduler issues 14 in the first launch, 1042 instructions a token (55 with all scores of such a token in FP64 and a round over all
 // experts for each choice; 8 lanes of 32 experts a token instead of a warp 70).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
