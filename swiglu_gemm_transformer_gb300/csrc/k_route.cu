@@ -26,11 +26,10 @@
 // issues the choices of 128 tokens in about 6 us, so they are spread over several
 // (route_blocks.h), which read each other's counts through distributed shared memory.
 // In a graph, 256 experts: 64 tokens by logit 5.5 us, by scores 6.7 (32 tokens a block:
-// 9.7 and 10.9); 8 tokens 4.3 and 5.4.  Beyond that a first kernel
-// numbers the entries within each block of 32 to 128 tokens (in slots) and writes
-// the block's counts to the workspace, and a second one, overlapped by
-// programmatic dependent launch, sums the counts of the blocks before its own
-// and adds them (16384 tokens: 14.0 us; in clusters of eight blocks of 32
+// 9.7 and 10.9); 8 tokens 4.2 and 5.0.  Beyond that a first kernel numbers the entries
+// within each block of 32 to 128 tokens (in slots) and writes the block's counts to
+// the workspace, and a second one, overlapped by programmatic dependent launch, sums
+// the counts of the blocks before its own and adds them (16384 tokens: 14.0 us; in clusters of eight blocks of 32
 // tokens about a fifth more).  Every block of the second launch reads the counts
 // of all blocks, which is little at such sizes but grows with the square of the
 // tokens: 131072 tokens take 89 us with 64 experts and 243 us with 256.
@@ -43,9 +42,10 @@
 // lie further apart than their rounding errors together, and where two do not,
 // which is so for about a token in a thousand, FP64 settles the few values
 // concerned (without a bias the logits' own order decides, and only sums of two
-// scores are compared).  16384 tokens, 256 experts in 8 groups, 33.5 us, of which a
-// scheduler issues 14 in the first launch, 1042 instructions a token (55 with all scores of such a token in FP64 and a round over all
-// experts for each choice; 8 lanes of 32 experts a token instead of a warp 70).
+// scores are compared).  16384 tokens, 256 experts in 8 groups, 33.5 us; a scheduler
+// issues for 14 of the first launch's 31, 1042 instructions a token (55 us with all
+// scores of such a token in FP64 and a round over all experts for each choice; 8 lanes
+// of 32 experts a token instead of a warp 70).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
